@@ -393,6 +393,158 @@ mdcn_status mdcn_forward_noalloc(mdcn_handle handle, const void* x, const void* 
  * still running on another stream. The source pages have no counterpart. */
 mdcn_status mdcn_noalloc_query_status(void* stream, uint32_t* device_bits);
 
+/* ---------------------------------------------------------------- attention
+ * Operators on tokens, for models that let the pixels of a feature map (or
+ * the words read from it) attend to one another: rotary positions over
+ * several axes with the norms of queries and keys in the same pass, and
+ * attention over packed sequences; each with its gradient. No handle: the
+ * attributes come with the call. Beside the conventions above:
+ *   - A tensor is [tokens][heads][head_dim] with the last index contiguous and
+ *     the other two at the strides given (in elements), so that the queries,
+ *     keys and values can be slices of one projection's output. A stride is
+ *     positive; that of an index of extent 1 is not looked at. Outputs must not
+ *     overlap each other or themselves.
+ *   - A tensor without elements may be NULL.
+ *   - Sums, norms, angles and softmax statistics are held in 32 bits. */
+typedef struct mdcn_strides {
+    int64_t token, head; /* elements from one token, one head, to the next */
+} mdcn_strides;
+
+/* Which elements of a head form the rotated pairs, P = sum of the sections:
+ * pair p of the P is (lo, hi); elements from 2P on are not rotated. */
+typedef enum mdcn_rotary_layout {
+    MDCN_ROTARY_HALF = 0,        /* (p, p + P) */
+    MDCN_ROTARY_INTERLEAVED = 1, /* (2p, 2p + 1) */
+    MDCN_ROTARY_BLOCKS = 2       /* each section its own block of 2 * sections[a] elements, in halves */
+} mdcn_rotary_layout;
+
+typedef struct mdcn_rotary_attrs {
+    int32_t layout; /* mdcn_rotary_layout */
+    int32_t norm;   /* 1: each head is divided by its root mean square first; 0: rotation only */
+    float eps;      /* added to the mean square; >= 0 and finite */
+} mdcn_rotary_attrs;
+
+typedef struct mdcn_rotary_dims {
+    int64_t tokens, q_heads, k_heads; /* k_heads 0: no k */
+    int64_t head_dim;                 /* a multiple of 8 up to 256 */
+    int64_t axes;                     /* 1..4: columns of positions, sections in use */
+    int64_t sections[4];              /* pairs that turn with each axis, >= 0; 2 * their sum <= head_dim */
+    mdcn_strides q, k;                /* of q and k */
+    mdcn_strides q_out, k_out;        /* of q_out and k_out, in the backward of their gradients */
+    mdcn_strides q_grad, k_grad;      /* of grad_q and grad_k; the forward does not look at them */
+} mdcn_rotary_dims;
+
+/* Queries and keys of one layer, normed and rotated, in one launch:
+ *   n = x * rsqrt(mean(x^2 over the head) + eps) * weight   (norm 1; else n = x)
+ *   (y[lo], y[hi]) = (n[lo] cos t - n[hi] sin t, n[hi] cos t + n[lo] sin t),
+ *   t = positions[token][axis of the pair] * inv_freq[pair],
+ * the pairs taking the axes in order, sections[0] of them the first. One
+ * rounding to the type of y. The angle is reduced to a turn from the exact
+ * product, so it keeps 32-bit precision at any position up to 2^24.
+ *   q [tokens][q_heads][head_dim], k_or_null likewise with k_heads;
+ *   positions int32 [tokens][axes], inv_freq float32 [P], both contiguous;
+ *   q_weight_or_null, k_weight_or_null [head_dim], the type of q (NULL: ones;
+ *   must be NULL with norm 0); q_out, k_out_or_null (may be q and k themselves,
+ *   with the same strides).
+ * Pointers aligned to 16 bytes, except that q, k and their outputs need only
+ * their type's alignment: with strides or pointers off 16 bytes the loads
+ * narrow to one element.
+ * Errors: MDCN_ERR_NULL, MDCN_ERR_ATTR (attrs out of range, or a weight with
+ * norm 0), MDCN_ERR_SHAPE, MDCN_ERR_DTYPE, MDCN_ERR_ALIGN,
+ * MDCN_ERR_UNSUPPORTED (head_dim not a multiple of 8 up to 256, an extent
+ * beyond 2^31-1), MDCN_ERR_ARCH, MDCN_ERR_CUDA. */
+mdcn_status mdcn_rotary_forward(const mdcn_rotary_attrs* attrs, const mdcn_rotary_dims* dims, mdcn_dtype dtype,
+                                const void* q, const void* k_or_null, const void* positions, const void* inv_freq,
+                                const void* q_weight_or_null, const void* k_weight_or_null, void* q_out,
+                                void* k_out_or_null, void* stream);
+
+/* Bytes of device workspace mdcn_rotary_backward needs (the weights' partial
+ * sums; 0 without weights). Host only. */
+mdcn_status mdcn_rotary_backward_workspace_size(const mdcn_rotary_attrs* attrs, const mdcn_rotary_dims* dims,
+                                                mdcn_dtype dtype, size_t* bytes);
+
+/* The gradients of L = sum(grad_q_out * q_out) + sum(grad_k_out * k_out): with
+ * g = grad rotated back, r = rsqrt(mean(x^2) + eps), n = x * r,
+ *   grad_weight = sum over tokens and heads of g * n
+ *   grad_x      = r * (g * weight - n * mean(g * weight * n))   (norm 0: g)
+ * q and k are read with norm 1 only (else may be NULL). grad_q_weight_or_null
+ * and grad_k_weight_or_null [head_dim], the type of q: given exactly when the
+ * weight is. grad_q may be grad_q_out itself (with the same strides), grad_k
+ * likewise. Deterministic: the weights' sums over blocks are added in a fixed
+ * order by a second, small launch (made only with a weight). workspace may be
+ * NULL where its size is 0. Alignment and errors as the forward's, plus
+ * MDCN_ERR_WORKSPACE. */
+mdcn_status mdcn_rotary_backward(const mdcn_rotary_attrs* attrs, const mdcn_rotary_dims* dims, mdcn_dtype dtype,
+                                 const void* grad_q_out, const void* grad_k_out_or_null, const void* q_or_null,
+                                 const void* k_or_null, const void* positions, const void* inv_freq,
+                                 const void* q_weight_or_null, const void* k_weight_or_null, void* grad_q,
+                                 void* grad_k_or_null, void* grad_q_weight_or_null, void* grad_k_weight_or_null,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+typedef struct mdcn_attention_attrs {
+    int32_t causal; /* 1: query i of a sequence sees its keys j <= i + keys - queries; 0: all of its keys */
+    float scale;    /* of the products q . k; finite */
+} mdcn_attention_attrs;
+
+typedef struct mdcn_attention_dims {
+    int64_t batch;              /* sequences */
+    int64_t q_tokens, k_tokens; /* rows of q, and of k and v, in all */
+    int64_t q_heads, k_heads;   /* k_heads divides q_heads: head h of q uses head h / (q_heads / k_heads) of k, v */
+    int64_t head_dim;           /* a multiple of 8 up to 128 */
+    mdcn_strides q, k, v, out;
+    mdcn_strides grad_out, grad_q, grad_k, grad_v; /* the forward does not look at these */
+} mdcn_attention_dims;
+
+/* Attention over packed sequences: sequence b holds the queries
+ * [q_starts[b], q_starts[b+1]) and the keys [k_starts[b], k_starts[b+1]), or
+ * the first k_lengths_or_null[b] of these (a cache with room left over). For
+ * each query and head, over the keys that it sees,
+ *   out = sum softmax(scale * q . k) v,   lse = log sum exp(scale * q . k);
+ * a query that sees none gets out = 0 and lse = -infinity.
+ *   q [q_tokens][q_heads][head_dim], k and v [k_tokens][k_heads][head_dim],
+ *   q_starts and k_starts int32 [batch + 1], from 0, not decreasing,
+ *   k_lengths_or_null int32 [batch]: device memory; values outside the tensors
+ *   are clamped to them; rows of no sequence are not written;
+ *   out (the type of q, not q itself), lse float32 [q_heads][q_tokens].
+ * Keys and values past a sequence's last key are not used, whatever they hold
+ * (infinities, NaN). Inside a sequence, the value of a key that a query must
+ * not see yet reaches that query only as 0 * value, so it has to be finite.
+ * Few queries against many keys (new tokens of a decoder): the keys of a
+ * sequence are shared out between blocks whose partial results are joined.
+ * float16, bfloat16: products on the tensor cores, the probabilities rounded
+ * to the type of v for the second product; strides of q, k and v multiples of
+ * 16 bytes. float32: fp32 products on the CUDA cores. Deterministic.
+ * Pointers aligned to 16 bytes, and the strides of all four tensors too.
+ * Errors: MDCN_ERR_NULL, MDCN_ERR_ATTR, MDCN_ERR_SHAPE, MDCN_ERR_DTYPE,
+ * MDCN_ERR_ALIGN (a pointer or a stride off 16 bytes), MDCN_ERR_WORKSPACE,
+ * MDCN_ERR_UNSUPPORTED (head_dim, more than 64 query heads to a key head, an
+ * extent beyond 2^31-1), MDCN_ERR_ARCH, MDCN_ERR_CUDA. */
+mdcn_status mdcn_attention_workspace_size(const mdcn_attention_attrs* attrs, const mdcn_attention_dims* dims,
+                                          mdcn_dtype dtype, size_t* bytes);
+mdcn_status mdcn_attention_forward(const mdcn_attention_attrs* attrs, const mdcn_attention_dims* dims,
+                                   mdcn_dtype dtype, const void* q, const void* k, const void* v,
+                                   const void* q_starts, const void* k_starts, const void* k_lengths_or_null,
+                                   void* out, void* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The gradients of L = sum(grad_out * out), from the forward's out and lse:
+ *   p = exp(scale * q . k - lse), delta = sum(grad_out * out over the head)
+ *   grad_v = p^T grad_out, ds = p * (grad_out . v - delta) * scale,
+ *   grad_q = ds k, grad_k = ds^T q (summed over the query heads of a key head).
+ * Keys past a sequence's last key (and queries that see no key) get gradient
+ * 0; rows of no sequence are not written. Deterministic: grad_q and
+ * (grad_k, grad_v) are computed by kernels of their own, each output by one
+ * block, instead of with atomic additions. Arguments, alignment (strides of
+ * all eight tensors) and errors as the forward's; q, k, v and out must not be
+ * written to by the outputs. The workspace's first word is the call's status
+ * word, as for the forward (mdcn_query_status). */
+mdcn_status mdcn_attention_backward_workspace_size(const mdcn_attention_attrs* attrs, const mdcn_attention_dims* dims,
+                                                   mdcn_dtype dtype, size_t* bytes);
+mdcn_status mdcn_attention_backward(const mdcn_attention_attrs* attrs, const mdcn_attention_dims* dims,
+                                    mdcn_dtype dtype, const void* grad_out, const void* q, const void* k,
+                                    const void* v, const void* out, const void* lse, const void* q_starts,
+                                    const void* k_starts, const void* k_lengths_or_null, void* grad_q, void* grad_k,
+                                    void* grad_v, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Reads the device status word that the last mdcn_forward on this workspace
  * left (synchronising the stream), stores its raw bits in *device_bits (may
  * be NULL) and clears it. Returns MDCN_ERR_TIMEOUT when a pipeline wait in

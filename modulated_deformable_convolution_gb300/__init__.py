@@ -25,7 +25,10 @@ __all__ = ["Handle", "MdcnError", "forward", "mdcn_create", "mdcn_destroy", "mdc
            "mdcn_forward_prepared", "mdcn_im2col_gemm_workspace_size", "mdcn_forward_im2col_gemm",
            "mdcn_query_plan", "mdcn_query_status", "mdcn_selftest_wait_timeout", "mdcn_status_string",
            "library_path", "backward", "mdcn_backward_workspace_size", "mdcn_backward_launches",
-           "mdcn_backward"]
+           "mdcn_backward", "rotary", "rotary_backward", "rotary_frequencies", "attention", "attention_backward",
+           "sequence_starts", "mdcn_rotary_forward", "mdcn_rotary_backward", "mdcn_rotary_backward_workspace_size",
+           "mdcn_attention_forward", "mdcn_attention_workspace_size", "mdcn_attention_backward",
+           "mdcn_attention_backward_workspace_size"]
 
 _DTYPES = {torch.float32: MDCN_F32, torch.float16: MDCN_F16, torch.bfloat16: MDCN_BF16}
 
@@ -399,3 +402,9 @@ def backward(x, offset, mask, weight, grad_out, with_bias=True, stride=1, paddin
          "weight": torch.empty_like(weight), "bias": gb}
     mdcn_backward(h, x, offset, mask, weight, grad_out, g["x"], g["offset"], g["mask"], g["weight"], gb, workspace)
     return g
+
+
+from .token_ops import (attention, attention_backward, mdcn_attention_backward,  # noqa: E402
+                        mdcn_attention_backward_workspace_size, mdcn_attention_forward, mdcn_attention_workspace_size,
+                        mdcn_rotary_backward, mdcn_rotary_backward_workspace_size, mdcn_rotary_forward, rotary,
+                        rotary_backward, rotary_frequencies, sequence_starts)

@@ -26,6 +26,10 @@ MDCN_F32 = 0
 MDCN_F16 = 1
 MDCN_BF16 = 2
 
+MDCN_ROTARY_HALF = 0
+MDCN_ROTARY_INTERLEAVED = 1
+MDCN_ROTARY_BLOCKS = 2
+
 i64 = ctypes.c_int64
 vp = ctypes.c_void_p
 
@@ -50,6 +54,31 @@ class mdcn_plan_info(ctypes.Structure):
 
 class mdcn_dims(ctypes.Structure):
     _fields_ = [("x", i64 * 4), ("offset", i64 * 4), ("mask", i64 * 4), ("weight", i64 * 4), ("bias", i64)]
+
+
+class mdcn_strides(ctypes.Structure):
+    _fields_ = [("token", i64), ("head", i64)]
+
+
+class mdcn_rotary_attrs(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int32), ("norm", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class mdcn_rotary_dims(ctypes.Structure):
+    _fields_ = [("tokens", i64), ("q_heads", i64), ("k_heads", i64), ("head_dim", i64), ("axes", i64),
+                ("sections", i64 * 4), ("q", mdcn_strides), ("k", mdcn_strides), ("q_out", mdcn_strides),
+                ("k_out", mdcn_strides), ("q_grad", mdcn_strides), ("k_grad", mdcn_strides)]
+
+
+class mdcn_attention_attrs(ctypes.Structure):
+    _fields_ = [("causal", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class mdcn_attention_dims(ctypes.Structure):
+    _fields_ = [("batch", i64), ("q_tokens", i64), ("k_tokens", i64), ("q_heads", i64), ("k_heads", i64),
+                ("head_dim", i64), ("q", mdcn_strides), ("k", mdcn_strides), ("v", mdcn_strides),
+                ("out", mdcn_strides), ("grad_out", mdcn_strides), ("grad_q", mdcn_strides),
+                ("grad_k", mdcn_strides), ("grad_v", mdcn_strides)]
 
 
 _lock = threading.Lock()
@@ -125,6 +154,21 @@ def load(path: str = LIB_PATH):
         lib.mdcn_query_status.restype = st
         lib.mdcn_selftest_wait_timeout.argtypes = [vp, ctypes.c_uint32, vp]
         lib.mdcn_selftest_wait_timeout.restype = st
+        rot = [ctypes.POINTER(mdcn_rotary_attrs), ctypes.POINTER(mdcn_rotary_dims), ctypes.c_int]
+        lib.mdcn_rotary_forward.argtypes = rot + [vp] * 9
+        lib.mdcn_rotary_forward.restype = st
+        lib.mdcn_rotary_backward_workspace_size.argtypes = rot + [ctypes.POINTER(ctypes.c_size_t)]
+        lib.mdcn_rotary_backward_workspace_size.restype = st
+        lib.mdcn_rotary_backward.argtypes = rot + [vp] * 13 + [ctypes.c_size_t, vp]
+        lib.mdcn_rotary_backward.restype = st
+        attn = [ctypes.POINTER(mdcn_attention_attrs), ctypes.POINTER(mdcn_attention_dims), ctypes.c_int]
+        for name in ("mdcn_attention_workspace_size", "mdcn_attention_backward_workspace_size"):
+            getattr(lib, name).argtypes = attn + [ctypes.POINTER(ctypes.c_size_t)]
+            getattr(lib, name).restype = st
+        lib.mdcn_attention_forward.argtypes = attn + [vp] * 9 + [ctypes.c_size_t, vp]
+        lib.mdcn_attention_forward.restype = st
+        lib.mdcn_attention_backward.argtypes = attn + [vp] * 13 + [ctypes.c_size_t, vp]
+        lib.mdcn_attention_backward.restype = st
         lib.mdcn_last_cuda_error.argtypes = []
         lib.mdcn_last_cuda_error.restype = ctypes.c_int
         lib.mdcn_status_string.argtypes = [ctypes.c_int]

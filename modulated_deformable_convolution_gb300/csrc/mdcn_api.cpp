@@ -13,6 +13,7 @@
 #include <mutex>
 #include <new>
 
+#include "mdcn_api.h"
 #include "mdcn_backward.h"
 #include "mdcn_launch.h"
 #include "mdcn_plan.h"
@@ -504,6 +505,13 @@ mdcn_status make_bwd_plan(const mdcn_attrs& a, const mdcn_dims* d, mdcn_dtype dt
 }
 
 }  // namespace
+
+namespace mdcn {
+
+mdcn_status api_cuda_fail(cudaError_t e) { return cuda_fail(e); }
+mdcn_status api_check_device(int* sms) { return check_device(sms); }
+
+}  // namespace mdcn
 
 extern "C" {
 

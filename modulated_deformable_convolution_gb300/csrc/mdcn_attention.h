@@ -1,0 +1,57 @@
+// Problem description and launchers of the attention over packed sequences
+// (internal; the public interface is include/mdcn.h).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+namespace mdcn {
+
+struct AttnTensor {
+    void* p;
+    int64_t st, sh;  // token and head strides, elements
+};
+
+struct AttnArgs {
+    AttnTensor q, k, v, out;          // out: written by the forward, read by the backward
+    AttnTensor g, gq, gk, gv;         // backward: grad_out (read), gradients (written)
+    float* lse;                       // [hq][tq]
+    const int32_t* q_starts;          // [batch + 1]
+    const int32_t* k_starts;          // [batch + 1]
+    const int32_t* k_lengths;         // [batch] or null
+    uint32_t* status;                 // first word of the workspace
+    float* part_out;                  // forward, keys shared out: [splits][tq][hq][D]
+    float* part_lse;                  // [splits][hq][tq]
+    float* delta;                     // backward: [hq][tq]
+    int32_t batch, tq, tk, hq, hk, group, D;
+    int32_t causal;
+    float scale;
+    int32_t splits;                   // blocks that share a row tile's keys
+    int32_t tiles;                    // row tiles of one key head at most (see attn_tiles)
+};
+
+// Row tiles hold the query heads of one key head together: row r of a tile is
+// token r / group, head r % group, so that each key and value is read once for
+// all heads that share it. A tile of `rows` rows takes rows / group tokens.
+// The number of tiles of `tokens` tokens each that `batch` sequences of `total`
+// tokens in all can need at most.
+inline int64_t attn_tiles(int64_t total, int64_t batch, int64_t tokens) {
+    const int64_t least = total < batch ? total : batch;  // sequences that are not empty
+    return (total - least) / tokens + least;
+}
+
+constexpr size_t kAttnHeaderBytes = 256;  // the workspace's status word
+
+// CUDA-core kernels (64 rows x 64 keys).
+constexpr int kAttnSimtRows = 64;
+cudaError_t launch_attention_simt_forward(int dtype, const AttnArgs& a, cudaStream_t st);
+cudaError_t launch_attention_simt_backward(int dtype, const AttnArgs& a, cudaStream_t st);
+
+// Joins the partial results of rows whose keys were shared out.
+cudaError_t launch_attention_join(int dtype, const AttnArgs& a, cudaStream_t st);
+// delta[h][t] = sum over the head of grad_out * out; clears the status word.
+cudaError_t launch_attention_delta(int dtype, const AttnArgs& a, cudaStream_t st);
+
+}  // namespace mdcn

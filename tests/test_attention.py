@@ -1,0 +1,425 @@
+"""Attention over packed sequences, forward and backward, against a plain
+implementation in 64 bits.
+
+Tolerances, derived from the arithmetic, with u the unit roundoff of the
+tensors' type and e = 2^-24:
+- a score is a sum of head_dim products in fp32 (tensor cores may drop the bits
+  below the largest term's fp32 unit): off by (2 head_dim + 8) e of the sum of
+  the products' magnitudes; a probability is off by that relatively, plus 16 e
+  for the exponential, and by u more where it is rounded to the tensors' type;
+- out = sum p v: that share of sum p |v|, and its own rounding, u |out|;
+- delta = sum grad_out * out reads an out that is rounded: u sum |grad_out out|;
+- ds = p (dp - delta) scale is rounded once more, u |ds|; the three sums take
+  over their terms' errors, and the gradients are rounded, u |.|.
+The sums over many terms add (64 + terms / 64) e of the magnitudes' sum."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+import modulated_deformable_convolution_gb300 as mdcn
+from modulated_deformable_convolution_gb300 import _abi
+
+gpu = pytest.mark.gpu
+U = {torch.float32: 2.0**-24, torch.float16: 2.0**-11, torch.bfloat16: 2.0**-8}
+TINY = {torch.float32: 2.0**-126, torch.float16: 2.0**-25, torch.bfloat16: 2.0**-126}
+E = 2.0**-24
+
+
+class Problem:
+    def __init__(self, dtype, ql, kl, hq, hk, d, causal, room=None, seed=0, fused=False, scale=None, gap=0):
+        g = torch.Generator().manual_seed(seed)
+        rnd = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+        self.dtype, self.ql, self.kl, self.causal = dtype, list(ql), list(kl), causal
+        self.room = list(room or kl)
+        self.scale = d**-0.5 if scale is None else scale
+        tq, tk = sum(ql) + gap, sum(self.room) + gap
+        if fused:
+            assert tq == tk
+            qkv = rnd(tq, hq + 2 * hk, d).to(dtype)
+            self.q, self.k, self.v = qkv[:, :hq], qkv[:, hq:hq + hk], qkv[:, hq + hk:]
+        else:
+            self.q, self.k, self.v = (rnd(t, h, d).to(dtype) for t, h in ((tq, hq), (tk, hk), (tk, hk)))
+        self.g = rnd(tq, hq, d).to(dtype)
+        self.qs, self.ks = mdcn.sequence_starts(ql, "cpu"), mdcn.sequence_starts(self.room, "cpu")
+        self.kn = torch.tensor(self.kl, dtype=torch.int32) if room else None
+
+    def cuda(self, name):
+        t = getattr(self, name)
+        if t is None or t.is_contiguous():
+            return None if t is None else t.cuda()
+        base = t._base.cuda()
+        return base.as_strided(t.shape, t.stride(), t.storage_offset())
+
+    def kw(self):
+        return dict(k_lengths=self.cuda("kn"), causal=self.causal, scale=self.scale)
+
+    def forward(self):
+        return mdcn.attention(self.cuda("q"), self.cuda("k"), self.cuda("v"), self.cuda("qs"), self.cuda("ks"), **self.kw())
+
+    def backward(self, out, lse):
+        return mdcn.attention_backward(self.cuda("g"), self.cuda("q"), self.cuda("k"), self.cuda("v"), out, lse, self.cuda("qs"), self.cuda("ks"), **self.kw())
+
+    def reference(self):
+        """Values and tolerances of out, lse and the gradients, in 64 bits on the CPU."""
+        u, d = U[self.dtype], self.q.shape[2]
+        hq, hk = self.q.shape[1], self.k.shape[1]
+        n = hq // hk
+        r = {x: torch.zeros(t.shape, dtype=torch.float64) for x, t in (("out", self.q), ("q", self.q), ("k", self.k), ("v", self.v))}
+        tol = {x: torch.zeros_like(t) for x, t in r.items()}
+        r["lse"] = torch.full((hq, self.q.shape[0]), -math.inf, dtype=torch.float64)
+        tol["lse"] = torch.zeros_like(r["lse"])
+        rounded = 0.0 if self.dtype == torch.float32 else u
+        a = b = 0
+        for lq, lk, room in zip(self.ql, self.kl, self.room):
+            for h in range(hq):
+                q, g = self.q[a:a + lq, h].double(), self.g[a:a + lq, h].double()
+                k, v = self.k[b:b + lk, h // n].double(), self.v[b:b + lk, h // n].double()
+                seen = torch.ones(lq, lk, dtype=torch.bool)
+                if self.causal:
+                    seen = torch.arange(lk)[None] <= torch.arange(lq)[:, None] + lk - lq
+                s = (q @ k.T * self.scale).masked_fill(~seen, -math.inf)
+                z = torch.logsumexp(s, 1) if lk else torch.full((lq,), -math.inf, dtype=torch.float64)
+                p = torch.exp(s - z.masked_fill(z == -math.inf, 0.0)[:, None])
+                mag = (q.abs() @ k.abs().T * abs(self.scale)).masked_fill(~seen, 0.0)
+                rel = (2 * d + 8) * E * mag + 16 * E  # of each probability, before rounding
+                worst = rel.amax(1, keepdim=True) if lk else torch.zeros(lq, 1)
+                rel = rel + worst  # its row's sum is off too
+                add = (64 + lk / 64) * E
+                o, av = p @ v, p @ v.abs()
+                r["out"][a:a + lq, h], r["lse"][h, a:a + lq] = o, z
+                tol["out"][a:a + lq, h] = u * o.abs() + (p * (rel + rounded + add)) @ v.abs()
+                tol["lse"][h, a:a + lq] = worst[:, 0] + 4 * E * z.masked_fill(z == -math.inf, 0.0).abs() + 8 * E
+                # backward
+                dp, adp = g @ v.T, g.abs() @ v.abs().T
+                delta, adelta = (g * o).sum(1, keepdim=True), (g * o).abs().sum(1, keepdim=True)
+                ds = p * (dp - delta)
+                eds = (rel + rounded) * ds.abs() + p * (2 * d + 8) * E * (adp + adelta) + p * u * adelta
+                dsum = (64 + max(lq * n, lk) / 64) * E
+                r["q"][a:a + lq, h] = ds @ k * self.scale
+                tol["q"][a:a + lq, h] = ((eds + dsum * ds.abs()) @ k.abs()) * abs(self.scale)
+                r["k"][b:b + lk, h // n] += ds.T @ q * self.scale
+                tol["k"][b:b + lk, h // n] += ((eds + dsum * ds.abs()).T @ q.abs()) * abs(self.scale)
+                r["v"][b:b + lk, h // n] += p.T @ g
+                tol["v"][b:b + lk, h // n] += (p * (rel + rounded + dsum)).T @ g.abs()
+            a, b = a + lq, b + room
+        for x in ("q", "k", "v"):
+            tol[x] += u * r[x].abs()
+        for x in ("out", "q", "k", "v"):
+            tol[x] = tol[x] * 1.02 + TINY[self.dtype] * (1 + max([1] + self.kl + self.ql))
+        return r, tol
+
+    def check(self, got, ref, tol, what):
+        got = got.double().cpu()
+        inf = torch.isinf(ref)
+        assert torch.equal(got[inf], ref[inf]), what
+        assert torch.isfinite(got[~inf]).all(), what
+        over = ((got - ref).abs() - tol)[~inf]
+        if over.numel():
+            assert over.max() <= 0, f"{what}: beyond the tolerance by {over.max():.3e}"
+
+
+def _run(p, backward=True):
+    r, tol = p.reference()
+    out, lse = p.forward()
+    p.check(out, r["out"], tol["out"], "out")
+    p.check(lse, r["lse"], tol["lse"], "lse")
+    if backward:
+        g = p.backward(r["out"].to(p.dtype).cuda(), r["lse"].float().cuda())
+        for x in ("q", "k", "v"):
+            p.check(g[x], r[x], tol[x], "grad_" + x)
+
+
+BF, FH, FS = torch.bfloat16, torch.float16, torch.float32
+CASES = [
+    # dtype, query lengths, key lengths, q heads, k heads, head_dim, causal
+    (BF, [1], [1], 1, 1, 64, True),
+    (BF, [128], [128], 2, 1, 64, True),
+    (FH, [127, 129, 1], [127, 129, 1], 2, 2, 64, False),
+    (BF, [300, 0, 5, 257], [300, 0, 5, 257], 4, 2, 128, True),
+    (FH, [64, 64, 200], [64, 64, 200], 3, 1, 40, True),
+    (BF, [513], [513], 1, 1, 128, False),
+    (BF, [100, 30], [37, 400], 4, 4, 80, True),     # the first rows of the first see no key
+    (FH, [9, 20, 3], [0, 1, 130], 6, 2, 96, False),  # no keys at all
+    (FH, [50, 3], [50, 700], 5, 1, 72, True),
+    (BF, [260], [260], 7, 1, 128, True),            # 7 heads share a key head
+    (FH, [70], [333], 40, 2, 8, False),             # 20 to a key head, 8 elements
+    (BF, [33], [65], 64, 1, 128, True),             # 64 to a key head
+    (FS, [65, 1, 130], [65, 1, 130], 2, 1, 64, True),
+    (FS, [100, 30, 4], [37, 100, 0], 4, 2, 72, True),
+    (FS, [64], [191], 3, 3, 128, False),
+    (FS, [17], [70], 20, 1, 24, True),
+]
+IDS = [f"{i}_{str(c[0])[6:]}_{c[3]}over{c[4]}x{c[5]}" for i, c in enumerate(CASES)]
+
+
+@gpu
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_against_64_bits(case):
+    _run(Problem(*case, seed=len(case[1])))
+
+
+@gpu
+@pytest.mark.parametrize("dtype,hq,hk,d,causal", [(BF, 4, 2, 64, True), (FH, 6, 1, 128, False), (FS, 2, 2, 40, True)])
+def test_slices_of_one_projection(dtype, hq, hk, d, causal):
+    _run(Problem(dtype, [130, 7, 66], [130, 7, 66], hq, hk, d, causal, fused=True, seed=5))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF, FH, FS])
+@pytest.mark.parametrize("new", [1, 3])
+def test_new_tokens_against_a_cache(dtype, new):
+    """A few new tokens a request, against caches with room left over that
+    holds NaN and infinities; enough keys that they are shared out."""
+    kl = [1500, 1, 700, 129, 128, 0, 64]
+    p = Problem(dtype, [new] * len(kl), kl, 8, 2, 64, True, room=[1600] * len(kl), seed=new)
+    for i, n in enumerate(kl):
+        p.k[1600 * i + n:1600 * (i + 1)] = math.nan
+        p.v[1600 * i + n:1600 * (i + 1)] = math.inf if i % 2 else math.nan
+    assert torch.isfinite(p.reference()[0]["out"]).all()
+    _run(p)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF, FS])
+def test_neighbours_do_not_leak(dtype):
+    """What the next sequence holds (NaN, infinities) reaches no other."""
+    p = Problem(dtype, [100, 50, 30], [100, 50, 30], 2, 1, 64, True, seed=2)
+    want, wlse = p.forward()
+    wg = p.backward(want, wlse)
+    for t in (p.q, p.k, p.v, p.g):
+        t[100:150] = math.nan
+    p.v[101] = math.inf
+    out, lse = p.forward()
+    o2, l2 = want.clone(), wlse.clone()
+    g = p.backward(o2, l2)
+    keep = torch.ones(180, dtype=torch.bool, device="cuda")
+    keep[100:150] = False
+    assert torch.equal(out[keep], want[keep]) and torch.equal(lse[:, keep], wlse[:, keep])
+    for x in ("q", "k", "v"):
+        assert torch.equal(g[x][keep], wg[x][keep]), x
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF, FH, FS])
+def test_large_scores(dtype):
+    """Scores in the hundreds: probabilities of 0 and 1, a maximum that grows
+    along the keys."""
+    p = Problem(dtype, [140], [300], 2, 1, 64, False, seed=3, scale=4.0)
+    p.k *= torch.linspace(0.1, 2.0, 300)[:, None, None].to(dtype)
+    _run(p)
+    p.scale = -1.0
+    _run(p)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF, FS])
+def test_rows_of_no_sequence_stay(dtype):
+    p = Problem(dtype, [40, 20], [40, 20], 2, 1, 64, True, gap=9)
+    q, k, v = p.cuda("q"), p.cuda("k"), p.cuda("v")
+    out, lse = torch.full_like(q, 7.0), torch.full((2, 69), 7.0, device="cuda")
+    mdcn.attention(q, k, v, p.cuda("qs"), p.cuda("ks"), causal=True, out=out, lse=lse)
+    assert (out[60:] == 7).all() and (lse[:, 60:] == 7).all() and (out[:60] != 7).any()
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    g = [torch.full_like(t, 7.0) for t in (q, k, v)]
+    mdcn.mdcn_attention_backward(p.cuda("g"), q, k, v, out, lse, p.cuda("qs"), p.cuda("ks"), *g, ws, causal=True)
+    for t in g:
+        assert (t[60:] == 7).all() and torch.isfinite(t[:60]).all()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF, FH, FS])
+def test_deterministic_on_a_stream_and_status(dtype):
+    p = Problem(dtype, [700, 130], [700, 130], 4, 2, 64, True, seed=9)
+    q, k, v, g = (p.cuda(x) for x in ("q", "k", "v", "g"))
+    qs, ks = p.cuda("qs"), p.cuda("ks")
+    ws = torch.full((mdcn.mdcn_attention_workspace_size(q, k, v, q, qs, ks),), 255, dtype=torch.uint8, device="cuda")
+    out, lse = mdcn.attention(q, k, v, qs, ks, causal=True, workspace=ws)
+    assert mdcn.mdcn_query_status(ws) == (0, 0)
+    grads = mdcn.attention_backward(g, q, k, v, out, lse, qs, ks, causal=True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            o2, l2 = mdcn.attention(q, k, v, qs, ks, causal=True)
+            g2 = mdcn.attention_backward(g, q, k, v, o2, l2, qs, ks, causal=True)
+    side.synchronize()
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+    for x in grads:
+        assert torch.equal(grads[x], g2[x]), x
+
+
+@gpu
+def test_capture_in_a_graph():
+    p = Problem(BF, [200, 56], [200, 56], 4, 2, 64, True, seed=4)
+    q, k, v, qs, ks = (p.cuda(x) for x in ("q", "k", "v", "qs", "ks"))
+    want, wlse = mdcn.attention(q, k, v, qs, ks, causal=True)
+    out, lse = torch.zeros_like(want), torch.zeros_like(wlse)
+    ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mdcn.mdcn_attention_forward(q, k, v, qs, ks, out, lse, ws, causal=True)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF, FS])
+def test_empty(dtype):
+    e = Problem(dtype, [], [], 2, 1, 64, True)
+    out, lse = e.forward()
+    assert out.shape == (0, 2, 64) and lse.shape == (2, 0)
+    assert {n: tuple(t.shape) for n, t in e.backward(out, lse).items()} == {"q": (0, 2, 64), "k": (0, 1, 64), "v": (0, 1, 64)}
+    # keys without queries: their gradients are zero
+    p = Problem(dtype, [0], [70], 2, 1, 64, False)
+    out, lse = p.forward()
+    g = p.backward(out, lse)
+    assert (g["k"] == 0).all() and (g["v"] == 0).all()
+    # queries without keys
+    p = Problem(dtype, [5], [0], 2, 1, 64, False)
+    out, lse = p.forward()
+    assert (out == 0).all() and (lse == -math.inf).all()
+    assert (p.backward(out, lse)["q"] == 0).all()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [FS, FH])
+def test_starts_out_of_range_are_clamped(dtype):
+    """Offsets beyond the tensors read and write nothing outside them: what is
+    left is attention over the clamped rows."""
+    p = Problem(dtype, [64], [64], 2, 1, 64, False, seed=6)
+    want, _ = p.forward()
+    p.qs, p.ks = torch.tensor([-5, 1000], dtype=torch.int32), torch.tensor([-7, 900], dtype=torch.int32)
+    out, _ = p.forward()
+    assert torch.equal(out, want)
+
+
+@gpu
+def test_gradient_against_differences():
+    """<gradient, direction> against the central difference of the 64-bit
+    forward; the fp32 gradient's error is a few 1e-6 of the terms' magnitudes."""
+    p = Problem(FS, [40, 9], [40, 30], 4, 2, 40, True, seed=8)
+    out, lse = p.forward()
+    grads = p.backward(out, lse)
+    gen = torch.Generator().manual_seed(1)
+
+    def loss(q, k, v):
+        save = p.q, p.k, p.v
+        p.q, p.k, p.v = q, k, v
+        o = p.reference()[0]["out"]
+        p.q, p.k, p.v = save
+        return (o * p.g.double()).sum()
+
+    base = [p.q.double(), p.k.double(), p.v.double()]
+    for i, x in enumerate(("q", "k", "v")):
+        step = torch.randn(base[i].shape, generator=gen, dtype=torch.float64)
+        h = 1e-5
+        up, down = list(base), list(base)
+        up[i], down[i] = base[i] + h * step, base[i] - h * step
+        diff = (loss(*up) - loss(*down)) / (2 * h)
+        terms = grads[x].double().cpu() * step
+        assert abs(terms.sum() - diff) <= 1e-5 * terms.abs().sum()
+
+
+# ---------------------------------------------------------------- refusals
+FAKE = 0x7F0000000000  # never dereferenced: each call below fails validation first
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from modulated_deformable_convolution_gb300 import build
+
+    build.build()
+    return _abi.load()
+
+
+def _dims(**kw):
+    d = _abi.mdcn_attention_dims()
+    d.batch, d.q_tokens, d.k_tokens, d.q_heads, d.k_heads, d.head_dim = 2, 10, 12, 4, 2, 64
+    for n in ("q", "k", "v", "out", "grad_out", "grad_q", "grad_k", "grad_v"):
+        s = getattr(d, n)
+        s.token, s.head = 4 * 64, 64
+    for k, v in kw.items():
+        if k.endswith("_stride"):
+            getattr(d, k[:-7]).token = v
+        else:
+            setattr(d, k, v)
+    return d
+
+
+def _fwd(lib, d, a=None, ptrs=None, dt=_abi.MDCN_BF16, nbytes=1 << 30):
+    a = a or _abi.mdcn_attention_attrs(1, 0.125)
+    p = ptrs or [FAKE + 256 * i for i in range(9)]
+    return lib.mdcn_attention_forward(ctypes.byref(a), ctypes.byref(d), dt, *p, nbytes, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(batch=-1), _abi.MDCN_ERR_SHAPE), (dict(batch=0), _abi.MDCN_ERR_SHAPE), (dict(q_heads=3), _abi.MDCN_ERR_SHAPE),
+    (dict(k_heads=0), _abi.MDCN_ERR_SHAPE), (dict(q_tokens=-1), _abi.MDCN_ERR_SHAPE), (dict(head_dim=0), _abi.MDCN_ERR_SHAPE),
+    (dict(head_dim=60), _abi.MDCN_ERR_UNSUPPORTED), (dict(head_dim=136), _abi.MDCN_ERR_UNSUPPORTED),
+    (dict(q_heads=130, k_heads=2), _abi.MDCN_ERR_UNSUPPORTED), (dict(k_tokens=2**31), _abi.MDCN_ERR_UNSUPPORTED),
+    (dict(q_stride=0), _abi.MDCN_ERR_SHAPE), (dict(out_stride=-8), _abi.MDCN_ERR_SHAPE), (dict(v_stride=260), _abi.MDCN_ERR_ALIGN),
+])
+def test_refuses_dims(lib, kw, status):
+    assert _fwd(lib, _dims(**kw)) == status
+
+
+def test_refuses_attrs_pointers_and_workspace(lib):
+    d = _dims()
+    for a in ((2, 1.0), (-1, 1.0), (0, math.inf), (0, math.nan)):
+        assert _fwd(lib, d, _abi.mdcn_attention_attrs(*a)) == _abi.MDCN_ERR_ATTR
+    assert _fwd(lib, d, dt=7) == _abi.MDCN_ERR_DTYPE
+    p = [FAKE + 256 * i for i in range(9)]  # q k v q_starts k_starts k_lengths out lse workspace
+    for i in (0, 1, 2, 3, 4, 6, 7, 8):
+        q = list(p)
+        q[i] = None
+        assert _fwd(lib, d, ptrs=q) == _abi.MDCN_ERR_NULL, i
+    for i in range(9):
+        q = list(p)
+        q[i] += 8
+        assert _fwd(lib, d, ptrs=q) == _abi.MDCN_ERR_ALIGN, i
+    assert _fwd(lib, d, nbytes=16) == _abi.MDCN_ERR_WORKSPACE
+    n = ctypes.c_size_t()
+    a = _abi.mdcn_attention_attrs(1, 0.125)
+    assert lib.mdcn_attention_backward_workspace_size(ctypes.byref(a), ctypes.byref(d), _abi.MDCN_BF16, ctypes.byref(n)) == 0
+    assert lib.mdcn_attention_backward_workspace_size(ctypes.byref(a), ctypes.byref(d), _abi.MDCN_BF16, None) == _abi.MDCN_ERR_NULL
+    # grad_out q k v out lse q_starts k_starts k_lengths grad_q grad_k grad_v workspace
+    p = [FAKE + 256 * i for i in range(13)]
+    back = lambda p, n: lib.mdcn_attention_backward(ctypes.byref(a), ctypes.byref(d), _abi.MDCN_BF16, *p, n, None)  # noqa: E731
+    assert back(p, n.value - 1) == _abi.MDCN_ERR_WORKSPACE
+    for i in range(13):
+        q = list(p)
+        q[i] = None
+        if i != 8:
+            assert back(q, n.value) == _abi.MDCN_ERR_NULL, i
+        q[i] = p[i] + 8
+        assert back(q, n.value) == _abi.MDCN_ERR_ALIGN, i
+
+
+def test_binding_refuses(lib):
+    q = torch.zeros(4, 2, 64)
+    s = mdcn.sequence_starts([4], "cpu")
+    with pytest.raises(ValueError):
+        mdcn.attention(q, q, q, s, s)  # not on a GPU
+
+
+@gpu
+def test_binding_refuses_on_gpu():
+    p = Problem(BF, [8], [8], 4, 2, 64, True)
+    q, k, v, qs = p.cuda("q"), p.cuda("k"), p.cuda("v"), p.cuda("qs")
+    with pytest.raises(TypeError):
+        mdcn.attention(q, k.float(), v, qs, qs)
+    with pytest.raises(ValueError):
+        mdcn.attention(q, k, v[:4], qs, qs)
+    with pytest.raises(TypeError):
+        mdcn.attention(q, k, v, qs.long(), qs)
+    with pytest.raises(ValueError):
+        mdcn.attention(q, k, v, qs, qs[:1])
+    with pytest.raises(ValueError):
+        mdcn.attention(q.transpose(1, 2), k, v, qs, qs)
+    with pytest.raises(mdcn.MdcnError):
+        mdcn.attention(q[:, :3], k, v, qs, qs)  # 3 heads over 2
+    with pytest.raises(mdcn.MdcnError):
+        mdcn.attention(q, k[:, :1].expand(8, 2, 64), v, qs, qs)  # a stride of 0

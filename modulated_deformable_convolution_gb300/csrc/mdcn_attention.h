@@ -49,6 +49,11 @@ constexpr int kAttnSimtRows = 64;
 cudaError_t launch_attention_simt_forward(int dtype, const AttnArgs& a, cudaStream_t st);
 cudaError_t launch_attention_simt_backward(int dtype, const AttnArgs& a, cudaStream_t st);
 
+// Tensor-core kernels (float16, bfloat16; 128 rows x 128 keys, two row tiles to
+// a block).
+constexpr int kAttnTcBlockRows = 128;
+cudaError_t launch_attention_tc_forward(int dtype, const AttnArgs& a, cudaStream_t st);
+
 // Joins the partial results of rows whose keys were shared out.
 cudaError_t launch_attention_join(int dtype, const AttnArgs& a, cudaStream_t st);
 // delta[h][t] = sum over the head of grad_out * out; clears the status word.

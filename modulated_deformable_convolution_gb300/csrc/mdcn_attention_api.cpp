@@ -142,15 +142,18 @@ struct AttnPlan {
     size_t off_out, off_lse, bytes;
 };
 
-AttnPlan attn_plan(const mdcn_attention_dims& d, mdcn_dtype) {
+AttnPlan attn_plan(const mdcn_attention_dims& d, mdcn_dtype dtype) {
     constexpr int64_t kSms = 152;
     AttnPlan p{};
     const int64_t group = d.q_heads / d.k_heads;
-    p.tiles = mdcn::attn_tiles(d.q_tokens, d.batch, mdcn::kAttnSimtRows / group);
+    const bool tc = dtype != MDCN_F32;
+    const int64_t tokens = tc ? 2 * (mdcn::kAttnTcBlockRows / group) : mdcn::kAttnSimtRows / group;
+    const int64_t keys = tc ? 128 : 64;
+    p.tiles = mdcn::attn_tiles(d.q_tokens, d.batch, tokens);
     const int64_t blocks = p.tiles * d.k_heads;
     p.splits = 1;
     if (blocks > 0 && blocks * 2 <= kSms) {
-        const int64_t key_tiles = (d.k_tokens / d.batch + 63) / 64;
+        const int64_t key_tiles = (d.k_tokens / d.batch + keys - 1) / keys;
         p.splits = 2 * kSms / blocks;
         if (p.splits > key_tiles / 2) p.splits = key_tiles / 2;
         if (p.splits < 1) p.splits = 1;
@@ -351,7 +354,8 @@ mdcn_status mdcn_attention_forward(const mdcn_attention_attrs* attrs, const mdcn
     if (p.tiles == 0) {
         e = cudaMemsetAsync(ws, 0, sizeof(uint32_t), st);
     } else {
-        e = mdcn::launch_attention_simt_forward(dtype, a, st);
+        e = dtype == MDCN_F32 ? mdcn::launch_attention_simt_forward(dtype, a, st)
+                              : mdcn::launch_attention_tc_forward(dtype, a, st);
         if (e == cudaSuccess && p.splits > 1) e = mdcn::launch_attention_join(dtype, a, st);
     }
     return e == cudaSuccess ? MDCN_OK : mdcn::api_cuda_fail(e);
@@ -384,8 +388,9 @@ mdcn_status mdcn_attention_backward(const mdcn_attention_attrs* attrs, const mdc
                         workspace};
     for (const void* p : al)
         if (!aligned16(p)) return MDCN_ERR_ALIGN;
-    const AttnPlan p = attn_plan(*dims, dtype);
-    if (p.tiles > kI31) return MDCN_ERR_UNSUPPORTED;
+    const int64_t tiles = mdcn::attn_tiles(dims->q_tokens, dims->batch,
+                                           mdcn::kAttnSimtRows / (dims->q_heads / dims->k_heads));
+    if (tiles > kI31) return MDCN_ERR_UNSUPPORTED;
     if (workspace_bytes < attn_bwd_bytes(*dims)) return MDCN_ERR_WORKSPACE;
     s = mdcn::api_check_device(nullptr);
     if (s != MDCN_OK) return s;
@@ -398,7 +403,7 @@ mdcn_status mdcn_attention_backward(const mdcn_attention_attrs* attrs, const mdc
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     a.status = reinterpret_cast<uint32_t*>(ws);
     a.delta = reinterpret_cast<float*>(ws + mdcn::kAttnHeaderBytes);
-    a.tiles = static_cast<int32_t>(p.tiles);
+    a.tiles = static_cast<int32_t>(tiles);
     cudaError_t e = mdcn::launch_attention_delta(dtype, a, st);
     if (e == cudaSuccess) e = mdcn::launch_attention_simt_backward(dtype, a, st);
     return e == cudaSuccess ? MDCN_OK : mdcn::api_cuda_fail(e);

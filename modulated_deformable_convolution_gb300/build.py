@@ -24,7 +24,7 @@ LIB = os.path.join(HERE, "libmdcn.so")
 
 CU_SOURCES = ["mdcn_fused.cu", "mdcn_prep.cu", "mdcn_im2col.cu", "mdcn_noalloc.cu", "mdcn_backward.cu", "mdcn_gemm.cu",
               "mdcn_direct.cu", "mdcn_rotary.cu", "mdcn_attention_simt.cu",
-              "mdcn_attention_tc.cu"]
+              "mdcn_attention_tc.cu", "mdcn_attention_tc_backward.cu"]
 CPP_SOURCES = ["mdcn_api.cpp", "mdcn_attention_api.cpp"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -71,9 +71,10 @@ __device__ __forceinline__ void attn_range(const int32_t* starts, int b, int32_t
 }
 
 // The sequence and tile of tile `index`, sequences in order and each cut into
-// tiles of `tokens` rows of `starts`; the tiles of a sequence from its last to
-// its first, since under a causal mask the last rows see the most keys. All 32
-// lanes of a warp call it; every lane gets the answer.
+// tiles of `tokens` rows. Under a causal mask the last queries see the most
+// keys and the first keys are seen by the most queries, so that tiles of
+// queries come from a sequence's last to its first, tiles of keys from its
+// first. All 32 lanes of a warp call it; every lane gets the answer.
 __device__ __forceinline__ AttnSeq attn_find(const AttnArgs& a, bool by_keys, int32_t tokens, int32_t index) {
     const int lane = threadIdx.x & 31;
     const int32_t* starts = by_keys ? a.k_starts : a.q_starts;
@@ -98,7 +99,7 @@ __device__ __forceinline__ AttnSeq attn_find(const AttnArgs& a, bool by_keys, in
             const int32_t before = __shfl_sync(0xffffffffu, sum - n, src);
             const int32_t tiles = __shfl_sync(0xffffffffu, n, src);
             const int b = b0 + src;
-            s.tile = tiles - 1 - (left - before);
+            s.tile = by_keys ? left - before : tiles - 1 - (left - before);
             attn_range(a.q_starts, b, a.tq, s.q0, s.lq);
             attn_range(a.k_starts, b, a.tk, s.k0, s.room);
             s.lk = a.k_lengths ? min(max(__ldg(a.k_lengths + b), 0), s.room) : s.room;

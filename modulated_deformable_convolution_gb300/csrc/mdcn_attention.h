@@ -44,15 +44,16 @@ inline int64_t attn_tiles(int64_t total, int64_t batch, int64_t tokens) {
 
 constexpr size_t kAttnHeaderBytes = 256;  // the workspace's status word
 
-// CUDA-core kernels (64 rows x 64 keys).
+// CUDA-core kernels (float32; 64 rows x 64 keys).
 constexpr int kAttnSimtRows = 64;
-cudaError_t launch_attention_simt_forward(int dtype, const AttnArgs& a, cudaStream_t st);
-cudaError_t launch_attention_simt_backward(int dtype, const AttnArgs& a, cudaStream_t st);
+cudaError_t launch_attention_simt_forward(const AttnArgs& a, cudaStream_t st);
+cudaError_t launch_attention_simt_backward(const AttnArgs& a, cudaStream_t st);
 
 // Tensor-core kernels (float16, bfloat16; 128 rows x 128 keys, two row tiles to
 // a block).
 constexpr int kAttnTcBlockRows = 128;
 cudaError_t launch_attention_tc_forward(int dtype, const AttnArgs& a, cudaStream_t st);
+cudaError_t launch_attention_tc_backward(int dtype, const AttnArgs& a, cudaStream_t st);
 
 // Joins the partial results of rows whose keys were shared out.
 cudaError_t launch_attention_join(int dtype, const AttnArgs& a, cudaStream_t st);

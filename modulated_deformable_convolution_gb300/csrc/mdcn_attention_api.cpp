@@ -354,7 +354,7 @@ mdcn_status mdcn_attention_forward(const mdcn_attention_attrs* attrs, const mdcn
     if (p.tiles == 0) {
         e = cudaMemsetAsync(ws, 0, sizeof(uint32_t), st);
     } else {
-        e = dtype == MDCN_F32 ? mdcn::launch_attention_simt_forward(dtype, a, st)
+        e = dtype == MDCN_F32 ? mdcn::launch_attention_simt_forward(a, st)
                               : mdcn::launch_attention_tc_forward(dtype, a, st);
         if (e == cudaSuccess && p.splits > 1) e = mdcn::launch_attention_join(dtype, a, st);
     }
@@ -405,7 +405,9 @@ mdcn_status mdcn_attention_backward(const mdcn_attention_attrs* attrs, const mdc
     a.delta = reinterpret_cast<float*>(ws + mdcn::kAttnHeaderBytes);
     a.tiles = static_cast<int32_t>(tiles);
     cudaError_t e = mdcn::launch_attention_delta(dtype, a, st);
-    if (e == cudaSuccess) e = mdcn::launch_attention_simt_backward(dtype, a, st);
+    if (e == cudaSuccess)
+        e = dtype == MDCN_F32 ? mdcn::launch_attention_simt_backward(a, st)
+                              : mdcn::launch_attention_tc_backward(dtype, a, st);
     return e == cudaSuccess ? MDCN_OK : mdcn::api_cuda_fail(e);
 }
 

@@ -26,6 +26,7 @@ constexpr int kR = kAttnSimtRows;  // rows of a tile
 constexpr int kC = 64;             // keys of a tile
 constexpr int kT = 256;
 constexpr int kPP = kC + 4;        // padded row of the probability tile
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kAcc = 2;            // 4-element pieces of a row per thread: 64 * kAcc >= D
 
 __device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(kT) attn_forward_simt_kernel(const __grid_cons
     const int32_t most = attn_seen(a, s, tok0 + ntok - 1);
     const int32_t ktiles = (most + kC - 1) / kC, per = (ktiles + a.splits - 1) / a.splits;
     const int32_t t0 = min(split * per, ktiles), t1 = min(t0 + per, ktiles);
-    const float to_log2 = a.scale * 1.4426950408889634f;
+    const float to_log2 = a.scale * kLog2e;
     for (int32_t t = t0; t < t1; ++t) {
         __syncthreads();
         load_keys<T>(ks, pitch, a.k, a, s, t * kC, kh);
@@ -253,13 +254,12 @@ __global__ void __launch_bounds__(kT) attn_grad_q_simt_kernel(const __grid_const
         const bool live = r < ntok * a.group;
         const int64_t at = live ? static_cast<int64_t>(kh * a.group + r % a.group) * a.tq + s.q0 + tok0 + r / a.group : 0;
         seen[i] = live ? attn_seen(a, s, tok0 + r / a.group) : 0;
-        lse[i] = live ? a.lse[at] * 1.4426950408889634f : 0.0f;
+        lse[i] = live ? a.lse[at] : 0.0f;
         delta[i] = live ? a.delta[at] : 0.0f;
 #pragma unroll
         for (int c = 0; c < kAcc; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     const int32_t ktiles = (attn_seen(a, s, tok0 + ntok - 1) + kC - 1) / kC;
-    const float to_log2 = a.scale * 1.4426950408889634f;
     for (int32_t t = 0; t < ktiles; ++t) {
         __syncthreads();
         load_keys<T>(ks, pitch, a.k, a, s, t * kC, kh);
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kT) attn_grad_q_simt_kernel(const __grid_const
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const bool on = t * kC + tx + 16 * j < seen[i];
-                const float p = on ? exp2f(fmaf(x[i][j], to_log2, -lse[i])) : 0.0f;
+                const float p = on ? exp2f(fmaf(x[i][j], a.scale, -lse[i]) * kLog2e) : 0.0f;
                 ps[(ty + 16 * i) * kPP + tx + 16 * j] = on ? p * (dp[i][j] - delta[i]) : 0.0f;
             }
         __syncthreads();
@@ -342,7 +342,6 @@ __global__ void __launch_bounds__(kT) attn_grad_kv_simt_kernel(const __grid_cons
         for (int c = 0; c < kAcc; ++c) ok[i][c] = ov[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
     // the first query that sees key j0
     const int32_t first = j0 >= s.lk ? s.lq : (a.causal ? max(0, j0 + s.lq - s.lk) : 0);
-    const float to_log2 = a.scale * 1.4426950408889634f;
     for (int32_t tok0 = first / tpt * tpt; tok0 < s.lq; tok0 += tpt) {
         const int32_t ntok = min(tpt, s.lq - tok0);
         __syncthreads();
@@ -359,11 +358,11 @@ __global__ void __launch_bounds__(kT) attn_grad_kv_simt_kernel(const __grid_cons
             const int64_t at =
                 live ? static_cast<int64_t>(kh * a.group + r % a.group) * a.tq + s.q0 + tok0 + r / a.group : 0;
             const int32_t seen = live ? attn_seen(a, s, tok0 + r / a.group) : 0;
-            const float lse = live ? a.lse[at] * 1.4426950408889634f : 0.0f, delta = live ? a.delta[at] : 0.0f;
+            const float lse = live ? a.lse[at] : 0.0f, delta = live ? a.delta[at] : 0.0f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const bool on = j0 + tx + 16 * j < seen;
-                const float p = on ? exp2f(fmaf(x[i][j], to_log2, -lse)) : 0.0f;
+                const float p = on ? exp2f(fmaf(x[i][j], a.scale, -lse) * kLog2e) : 0.0f;  // one rounding before the small difference is scaled
                 ps[r * kPP + tx + 16 * j] = p;
                 ds[r * kPP + tx + 16 * j] = on ? p * (dp[i][j] - delta) : 0.0f;
             }
@@ -485,17 +484,9 @@ cudaError_t backward_t(const AttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_attention_simt_forward(int dtype, const AttnArgs& a, cudaStream_t st) {
-    if (dtype == kF32) return forward_t<float>(a, st);
-    if (dtype == kF16) return forward_t<__half>(a, st);
-    return forward_t<__nv_bfloat16>(a, st);
-}
+cudaError_t launch_attention_simt_forward(const AttnArgs& a, cudaStream_t st) { return forward_t<float>(a, st); }
 
-cudaError_t launch_attention_simt_backward(int dtype, const AttnArgs& a, cudaStream_t st) {
-    if (dtype == kF32) return backward_t<float>(a, st);
-    if (dtype == kF16) return backward_t<__half>(a, st);
-    return backward_t<__nv_bfloat16>(a, st);
-}
+cudaError_t launch_attention_simt_backward(const AttnArgs& a, cudaStream_t st) { return backward_t<float>(a, st); }
 
 template <typename F>
 static cudaError_t launch_after(F kernel, int64_t grid, const AttnArgs& a, cudaStream_t st) {

@@ -407,19 +407,21 @@ cudaError_t launch_forward(int dtype, const AttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
+// Of a tensor without tokens nothing is loaded, but a map needs an address and
+// an extent: those of the offsets, which are always there.
 bool attn_encode_rows(CUtensorMap* m, const AttnArgs& a, const AttnTensor& t, int dtype, int tokens) {
     const cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.D), static_cast<cuuint64_t>(a.group),
-                                static_cast<cuuint64_t>(a.hk), static_cast<cuuint64_t>(a.tq)};
+                                static_cast<cuuint64_t>(a.hk), static_cast<cuuint64_t>(a.tq > 0 ? a.tq : 1)};
+    const void* base = a.tq > 0 ? t.p : a.q_starts;
     const cuuint64_t strides[3] = {map_stride(t.sh), map_stride(t.sh * a.group), map_stride(t.st)};
     const cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(a.group), 1u, static_cast<cuuint32_t>(tokens)};
-    return encode(m, t.p, 4, dims, strides, box, dtype);
+    return encode(m, base, 4, dims, strides, box, dtype);
 }
 
 bool attn_encode_keys(CUtensorMap* m, const AttnArgs& a, const AttnTensor& t, int dtype, int rows) {
-    // without keys nothing is loaded, but a map needs an address and an extent
-    const void* base = a.tk > 0 ? t.p : a.q.p;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.D), static_cast<cuuint64_t>(a.hk),
                                 static_cast<cuuint64_t>(a.tk > 0 ? a.tk : 1)};
+    const void* base = a.tk > 0 ? t.p : a.k_starts;
     const cuuint64_t strides[2] = {map_stride(t.sh), map_stride(t.st)};
     const cuuint32_t box[3] = {64u, 1u, static_cast<cuuint32_t>(rows)};
     return encode(m, base, 3, dims, strides, box, dtype);

@@ -96,6 +96,8 @@ def load(path: str = LIB_PATH):
     """Loads libmdcn.so (built by ``build.py``). Raises if it is missing:
     there is no fallback implementation."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -154,14 +156,15 @@ def load(path: str = LIB_PATH):
         lib.mdcn_query_status.restype = st
         lib.mdcn_selftest_wait_timeout.argtypes = [vp, ctypes.c_uint32, vp]
         lib.mdcn_selftest_wait_timeout.restype = st
-        rot = [ctypes.POINTER(mdcn_rotary_attrs), ctypes.POINTER(mdcn_rotary_dims), ctypes.c_int]
+        # attrs and dims: pointers to the structs above, or their bytes
+        rot = [vp, vp, ctypes.c_int]
         lib.mdcn_rotary_forward.argtypes = rot + [vp] * 9
         lib.mdcn_rotary_forward.restype = st
         lib.mdcn_rotary_backward_workspace_size.argtypes = rot + [ctypes.POINTER(ctypes.c_size_t)]
         lib.mdcn_rotary_backward_workspace_size.restype = st
         lib.mdcn_rotary_backward.argtypes = rot + [vp] * 13 + [ctypes.c_size_t, vp]
         lib.mdcn_rotary_backward.restype = st
-        attn = [ctypes.POINTER(mdcn_attention_attrs), ctypes.POINTER(mdcn_attention_dims), ctypes.c_int]
+        attn = [vp, vp, ctypes.c_int]
         for name in ("mdcn_attention_workspace_size", "mdcn_attention_backward_workspace_size"):
             getattr(lib, name).argtypes = attn + [ctypes.POINTER(ctypes.c_size_t)]
             getattr(lib, name).restype = st

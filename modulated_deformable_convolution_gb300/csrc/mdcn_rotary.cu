@@ -9,14 +9,16 @@
 //
 // Both move each element once in and once out (the backward reads two) and do
 // a few operations on it: bound by device memory. So a row is 16 or 32 bytes
-// per lane, D / 8 lanes per row, and several rows are in flight per warp. A
-// warp takes all heads of a token (or a share of them, when tokens are few),
-// because the cosines and sines depend on the token alone: it computes each
-// pair's once, into shared memory, and each lane keeps those of its own 8
-// elements in registers for all of the token's heads. The partner of an
-// element lies in the same lane for neighbouring pairs; otherwise the row goes
-// through the warp's shared memory (any distance, so odd sections cost the
-// same as even ones).
+// per lane, D / 8 lanes per row, several rows in flight per warp, and the
+// arithmetic is kept short: two values per instruction, weights folded into
+// the cosines and sines, the norm's factor applied last. A warp takes all heads
+// of a token (or a share of them, when tokens are few), because the cosines
+// and sines depend on the token alone: it computes each pair's once, into
+// shared memory, and each lane keeps those of its own 8 elements in registers
+// for all of the token's heads. The partner of an element lies in the same lane
+// for neighbouring pairs; otherwise the lane loads the partners' values too, of
+// the row that the warp is loading anyway (first-level cache): as a vector where
+// they are 8 neighbours on a multiple of 8, else one by one.
 //
 // Angles: position * frequency is taken in turns as an exact product (two
 // fp32 words), its whole turns are dropped, and only then is it rounded, so
@@ -57,6 +59,37 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
     return __float2bfloat16_rn(v);
 }
 
+// Two fp32 values in one register pair: one instruction works on both.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t swap2(uint64_t v) {
+    float lo, hi;
+    unpack2(v, lo, hi);
+    return pack2(hi, lo);
+}
+__device__ __forceinline__ float sum2(uint64_t v) {
+    float lo, hi;
+    unpack2(v, lo, hi);
+    return lo + hi;
+}
+
+// 8 elements of a row.
 template <typename T>
 struct Pack {
     static constexpr int kV = static_cast<int>(kE * sizeof(T) / 16);
@@ -81,6 +114,19 @@ struct Pack {
         } else {
 #pragma unroll
             for (int i = 0; i < kE; ++i) p[i] = e[i];
+        }
+    }
+    __device__ __forceinline__ void widen(uint64_t (&x)[kE / 2]) const {
+#pragma unroll
+        for (int i = 0; i < kE / 2; ++i) x[i] = pack2(to_f(e[2 * i]), to_f(e[2 * i + 1]));
+    }
+    __device__ __forceinline__ void round(const uint64_t (&x)[kE / 2]) {
+#pragma unroll
+        for (int i = 0; i < kE / 2; ++i) {
+            float lo, hi;
+            unpack2(x[i], lo, hi);
+            e[2 * i] = from_f<T>(lo);
+            e[2 * i + 1] = from_f<T>(hi);
         }
     }
 };
@@ -139,66 +185,55 @@ __device__ __forceinline__ float row_sum(float v, int lanes) {
     return v;
 }
 
-// One warp's shared memory: a token's (cos, sin) and one row per lane group.
+// One warp's shared memory: a token's (cos, sin) of each pair.
 struct alignas(16) WarpSmem {
-    float cs[kMaxD];         // (cos, sin) of each pair
-    float row[32 * kE];
+    float cs[kMaxD];
 };
 
-// What a lane keeps for its 8 elements: where each partner's value lies in
-// the warp's row buffer (4 x 16 bits would do; kept as shorts).
-struct LaneMap {
-    int16_t pair[kE];
-    int16_t partner[kE];
-    float sign[kE];
-};
-
-template <bool kNeighbour>
-__device__ __forceinline__ void rotate(float (&n)[kE], const float (&c)[kE], const float (&s)[kE], const LaneMap& m,
-                                       float* row, int lane) {
-    if constexpr (kNeighbour) {
-#pragma unroll
-        for (int i = 0; i < kE; i += 2) {
-            const float a = n[i], b = n[i + 1];
-            n[i] = fmaf(a, c[i], b * s[i]);
-            n[i + 1] = fmaf(b, c[i + 1], a * s[i + 1]);
-        }
-    } else {
-        __syncwarp();
-        float4* mine = reinterpret_cast<float4*>(row + lane * kE);
-        mine[0] = make_float4(n[0], n[1], n[2], n[3]);
-        mine[1] = make_float4(n[4], n[5], n[6], n[7]);
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < kE; ++i) n[i] = fmaf(n[i], c[i], row[m.partner[i]] * s[i]);
-    }
-}
-
-// Lane set-up shared by both directions.
+// A lane's place in its row: 8 elements from e0 on, and where their partners
+// lie.
 struct LaneSetup {
-    int lane, sub, row_in_warp, rows_per_warp, e0;
-    bool on;
-    LaneMap m;
+    int lane, rows_per_warp, row_in_warp, e0;
+    bool on;               // the lane has elements
+    bool run;              // its 8 partners are 8 neighbouring elements that start on a multiple of 8
+    uint32_t code[kE / 2]; // two elements each: partner, 8 bits; pair, 7 bits; rotated, 1 bit
     __device__ __forceinline__ LaneSetup(const RotaryArgs& a) {
         lane = threadIdx.x & 31;
-        sub = lane & (a.lanes - 1);
+        const int sub = lane & (a.lanes - 1);
         rows_per_warp = 32 / a.lanes;
         row_in_warp = lane / a.lanes;
         e0 = sub * kE;
         on = e0 < a.D;
-        const int base = row_in_warp * a.lanes * kE;
+        run = true;
+        int first = 0;
 #pragma unroll
         for (int i = 0; i < kE; ++i) {
-            int partner = e0 + i;
+            int to = e0 + i;
             float sg = 0.0f;
-            m.pair[i] = static_cast<int16_t>(on ? pair_of(a, e0 + i, partner, sg) : -1);
-            m.partner[i] = static_cast<int16_t>(base + partner);
-            m.sign[i] = sg;
+            const int p = on ? pair_of(a, e0 + i, to, sg) : -1;
+            if (i == 0) first = to;
+            run = run && to == first + i;
+            const uint32_t v = static_cast<uint32_t>(to) | (p >= 0 ? (static_cast<uint32_t>(p) << 8 | 0x8000u) : 0u);
+            code[i / 2] = i & 1 ? code[i / 2] | v << 16 : v;
+        }
+        run = run && (first & 7) == 0;
+        // one path for the warp: narrow partner loads wherever one lane needs them
+        run = __all_sync(0xffffffffu, run || !on) != 0;
+    }
+    __device__ __forceinline__ uint32_t entry(int i) const { return code[i / 2] >> (16 * (i & 1)); }
+    __device__ __forceinline__ int partner(int i) const { return static_cast<int>(entry(i) & 0xffu); }
+    // The partners of the lane's elements, from the row that starts at `row`.
+    template <typename T>
+    __device__ __forceinline__ void load_partners(Pack<T>& p, const T* row, bool vec) const {
+        if (run) {
+            p.load(row + partner(0), vec);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kE; ++i) p.e[i] = row[partner(i)];
         }
     }
-    // The token's cosines and signed sines of this lane's elements.
-    __device__ __forceinline__ void turns(const RotaryArgs& a, int token, WarpSmem& w, float direction, float (&c)[kE],
-                                          float (&s)[kE]) const {
+    // The cosine of each of the token's pairs, and its sine, into the warp's shared memory.
+    __device__ __forceinline__ void turn_pairs(const RotaryArgs& a, int token, WarpSmem& w) const {
         __syncwarp();
         for (int p = lane; p < a.pairs; p += 32) {
             int ax = 0;
@@ -208,32 +243,34 @@ struct LaneSetup {
             *reinterpret_cast<float2*>(&w.cs[2 * p]) = make_float2(cp, sp);
         }
         __syncwarp();
-#pragma unroll
-        for (int i = 0; i < kE; ++i) {
-            c[i] = 1.0f;
-            s[i] = 0.0f;
-            if (m.pair[i] >= 0) {
-                const float2 v = *reinterpret_cast<const float2*>(&w.cs[2 * m.pair[i]]);
-                c[i] = v.x;
-                s[i] = v.y * m.sign[i] * direction;
-            }
+    }
+    // Of this lane's element i: the cosine, and the sine with the sign that it
+    // has in the forward (first of its pair: minus) times `direction`.
+    __device__ __forceinline__ void turn_of(const WarpSmem& w, int i, float direction, float& c, float& s) const {
+        const uint32_t v = entry(i);
+        c = 1.0f;
+        s = 0.0f;
+        if (v & 0x8000u) {
+            const float2 t = *reinterpret_cast<const float2*>(&w.cs[2 * ((v >> 8) & 0x7fu)]);
+            c = t.x;
+            s = static_cast<int>(v & 0xffu) > e0 + i ? -direction * t.y : direction * t.y;
         }
     }
 };
 
+// The rows of q (t 0) or k (t 1) in rows [r0, r1) of a token.
+__device__ __forceinline__ void part_rows(const RotaryArgs& a, int t, int r0, int r1, int& h0, int& h1) {
+    h0 = t ? max(r0 - a.hq, 0) : r0;
+    h1 = t ? r1 - a.hq : min(r1, a.hq);
+}
+
 template <typename T, bool kNeighbour>
-__global__ void __launch_bounds__(kThreads) rotary_forward_kernel(const __grid_constant__ RotaryArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) rotary_forward_kernel(const __grid_constant__ RotaryArgs a) {
     __shared__ WarpSmem smem[kWarps];
     WarpSmem& w = smem[threadIdx.x >> 5];
     const LaneSetup L(a);
     const bool vec = a.vec != 0;
     const float inv_d = 1.0f / static_cast<float>(a.D);
-    float wt[2][kE];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < kE; ++i)
-            wt[t][i] = (L.on && a.w[t]) ? to_f(static_cast<const T*>(a.w[t])[L.e0 + i]) : 1.0f;
 
     const int64_t units = static_cast<int64_t>(a.tokens) * a.parts;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps;
@@ -243,50 +280,78 @@ __global__ void __launch_bounds__(kThreads) rotary_forward_kernel(const __grid_c
         const int token = static_cast<int>(u / a.parts), part = static_cast<int>(u % a.parts);
         const int r0 = part * share, r1 = min(r0 + share, a.rows);
         if (r0 >= r1) continue;
-        auto addr = [&](const RotaryTensor* t, int r) {
-            const int i = r >= a.hq ? 1 : 0;
-            const int h = i ? r - a.hq : r;
-            return static_cast<T*>(t[i].p) + static_cast<int64_t>(token) * t[i].st + static_cast<int64_t>(h) * t[i].sh +
-                   L.e0;
-        };
-        // the next rows' loads are in flight while a row is worked on
-        constexpr int kAhead = 4;
-        Pack<T> buf[kAhead];
+        bool turned = false;
+#pragma unroll 1
+        for (int t = 0; t < 2; ++t) {
+            int h0, h1;
+            part_rows(a, t, r0, r1, h0, h1);
+            if (h0 >= h1) continue;
+            const T* in = static_cast<const T*>(a.x[t].p) + static_cast<int64_t>(token) * a.x[t].st;
+            T* out = static_cast<T*>(a.y[t].p) + static_cast<int64_t>(token) * a.y[t].st + L.e0;
+            const int64_t in_h = a.x[t].sh, out_h = a.y[t].sh;
+            // the next rows' loads are in flight while a row is worked on
+            constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
+            Pack<T> own[kAhead];
+            auto fetch = [&](int k, int h) {
+                if (L.on && h < h1) own[k].load(in + h * in_h + L.e0, vec);
+            };
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int r = r0 + k * L.rows_per_warp + L.row_in_warp;
-            if (L.on && r < r1) buf[k].load(addr(a.x, r), vec);
-        }
-        float c[kE], s[kE];
-        L.turns(a, token, w, 1.0f, c, s);
-        for (int rb = r0; rb < r1; rb += kAhead * L.rows_per_warp) {
+            for (int k = 0; k < kAhead; ++k) fetch(k, h0 + k * L.rows_per_warp + L.row_in_warp);
+            if (!turned) L.turn_pairs(a, token, w);
+            turned = true;
+            // y = r (x w c + x' w' s), x' the partner and w' its weight: the norm's factor r comes last
+            uint64_t wc[kE / 2], ws[kE / 2];
+            const T* wt = static_cast<const T*>(a.w[t]);
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int base = rb + k * L.rows_per_warp;
-                if (base >= r1) break;
-                const int r = base + L.row_in_warp;
-                const bool live = L.on && r < r1;
-                float n[kE];
+            for (int i = 0; i < kE / 2; ++i) {
+                float c[2], s[2];
 #pragma unroll
-                for (int i = 0; i < kE; ++i) n[i] = live ? to_f(buf[k].e[i]) : 0.0f;
-                const int rn = r + kAhead * L.rows_per_warp;
-                if (L.on && rn < r1) buf[k].load(addr(a.x, rn), vec);
-                if (a.norm) {
-                    float ss = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < kE; ++i) ss = fmaf(n[i], n[i], ss);
-                    ss = row_sum(ss, a.lanes);
-                    const float inv = rsqrtf(fmaf(ss, inv_d, a.eps));
-                    const int t = r >= a.hq ? 1 : 0;
-#pragma unroll
-                    for (int i = 0; i < kE; ++i) n[i] *= inv * (t ? wt[1][i] : wt[0][i]);
+                for (int j = 0; j < 2; ++j) {
+                    L.turn_of(w, 2 * i + j, 1.0f, c[j], s[j]);
+                    if (wt && L.on) {
+                        c[j] *= to_f(wt[L.e0 + 2 * i + j]);
+                        s[j] *= to_f(wt[L.partner(2 * i + j)]);
+                    }
                 }
-                rotate<kNeighbour>(n, c, s, L.m, w.row, L.lane);
-                if (live) {
-                    Pack<T> o;
+                wc[i] = pack2(c[0], c[1]);
+                ws[i] = pack2(s[0], s[1]);
+            }
+            for (int hb = h0; hb < h1; hb += kAhead * L.rows_per_warp) {
 #pragma unroll
-                    for (int i = 0; i < kE; ++i) o.e[i] = from_f<T>(n[i]);
-                    o.store(addr(a.y, r), vec);
+                for (int k = 0; k < kAhead; ++k) {
+                    const int first = hb + k * L.rows_per_warp;
+                    if (first >= h1) break;
+                    const int h = first + L.row_in_warp;
+                    const bool live = L.on && h < h1;
+                    uint64_t x[kE / 2], y[kE / 2];
+                    own[k].widen(x);
+                    if constexpr (kNeighbour) {
+#pragma unroll
+                        for (int i = 0; i < kE / 2; ++i) y[i] = swap2(x[i]);
+                    } else {
+                        Pack<T> far;
+                        if (live) L.load_partners(far, in + h * in_h, vec);
+                        far.widen(y);
+                    }
+                    fetch(k, h + kAhead * L.rows_per_warp);
+#pragma unroll
+                    for (int i = 0; i < kE / 2; ++i) y[i] = fma2(x[i], wc[i], mul2(y[i], ws[i]));
+                    if (a.norm) {
+                        uint64_t q = mul2(x[0], x[0]);
+#pragma unroll
+                        for (int i = 1; i < kE / 2; ++i) q = fma2(x[i], x[i], q);
+                        const float ss = row_sum(live ? sum2(q) : 0.0f, a.lanes);
+                        const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
+                        const uint64_t r2 = pack2(r, r);
+#pragma unroll
+                        for (int i = 0; i < kE / 2; ++i) y[i] = mul2(y[i], r2);
+                    }
+                    __syncwarp();  // y may be x: every lane has loaded its partners
+                    if (live) {
+                        Pack<T> o;
+                        o.round(y);
+                        o.store(out + h * out_h, vec);
+                    }
                 }
             }
         }
@@ -294,20 +359,18 @@ __global__ void __launch_bounds__(kThreads) rotary_forward_kernel(const __grid_c
 }
 
 template <typename T, bool kNeighbour>
-__global__ void __launch_bounds__(kThreads) rotary_backward_kernel(const __grid_constant__ RotaryArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) rotary_backward_kernel(const __grid_constant__ RotaryArgs a) {
     __shared__ WarpSmem smem[kWarps];
+    __shared__ alignas(16) float sums[kWarps][32 * kE];
     WarpSmem& w = smem[threadIdx.x >> 5];
     const LaneSetup L(a);
     const bool vec = a.vec != 0;
     const float inv_d = 1.0f / static_cast<float>(a.D);
-    float wt[2][kE], gw[2][kE];
+    uint64_t gw[2][kE / 2];
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int i = 0; i < kE; ++i) {
-            wt[t][i] = (L.on && a.w[t]) ? to_f(static_cast<const T*>(a.w[t])[L.e0 + i]) : 1.0f;
-            gw[t][i] = 0.0f;
-        }
+        for (int i = 0; i < kE / 2; ++i) gw[t][i] = 0;
 
     const int64_t units = static_cast<int64_t>(a.tokens) * a.parts;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps;
@@ -316,84 +379,109 @@ __global__ void __launch_bounds__(kThreads) rotary_backward_kernel(const __grid_
         const int token = static_cast<int>(u / a.parts), part = static_cast<int>(u % a.parts);
         const int r0 = part * share, r1 = min(r0 + share, a.rows);
         if (r0 >= r1) continue;
-        auto addr = [&](const RotaryTensor* t, int r) {
-            const int i = r >= a.hq ? 1 : 0;
-            const int h = i ? r - a.hq : r;
-            return static_cast<T*>(t[i].p) + static_cast<int64_t>(token) * t[i].st + static_cast<int64_t>(h) * t[i].sh +
-                   L.e0;
-        };
-        constexpr int kAhead = 2;
-        Pack<T> gb[kAhead], xb[kAhead];
+        uint64_t c[kE / 2], s[kE / 2];
+        bool turned = false;
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int r = r0 + k * L.rows_per_warp + L.row_in_warp;
-            if (L.on && r < r1) {
-                gb[k].load(addr(a.y, r), vec);
-                if (a.norm) xb[k].load(addr(a.x, r), vec);
+        for (int t = 0; t < 2; ++t) {
+            int h0, h1;
+            part_rows(a, t, r0, r1, h0, h1);
+            if (h0 >= h1) continue;
+            const T* gin = static_cast<const T*>(a.y[t].p) + static_cast<int64_t>(token) * a.y[t].st;
+            const T* xin = static_cast<const T*>(a.x[t].p) + static_cast<int64_t>(token) * a.x[t].st + L.e0;
+            T* out = static_cast<T*>(a.g[t].p) + static_cast<int64_t>(token) * a.g[t].st + L.e0;
+            const int64_t g_h = a.y[t].sh, x_h = a.x[t].sh, out_h = a.g[t].sh;
+            constexpr int kAhead = 2;
+            Pack<T> own[kAhead], val[kAhead];
+            auto fetch = [&](int k, int h) {
+                if (L.on && h < h1) {
+                    own[k].load(gin + h * g_h + L.e0, vec);
+                    if (a.norm) val[k].load(xin + h * x_h, vec);
+                }
+            };
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) fetch(k, h0 + k * L.rows_per_warp + L.row_in_warp);
+            if (!turned) {
+                L.turn_pairs(a, token, w);
+#pragma unroll
+                for (int i = 0; i < kE / 2; ++i) {
+                    float cf[2], sf[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) L.turn_of(w, 2 * i + j, -1.0f, cf[j], sf[j]);
+                    c[i] = pack2(cf[0], cf[1]);
+                    s[i] = pack2(sf[0], sf[1]);
+                }
             }
-        }
-        float c[kE], s[kE];
-        L.turns(a, token, w, -1.0f, c, s);
-        for (int rb = r0; rb < r1; rb += kAhead * L.rows_per_warp) {
+            turned = true;
+            uint64_t wt[kE / 2];
+            const T* wp = static_cast<const T*>(a.w[t]);
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int base = rb + k * L.rows_per_warp;
-                if (base >= r1) break;
-                const int r = base + L.row_in_warp;
-                const bool live = L.on && r < r1;
-                float g[kE], x[kE];
+            for (int i = 0; i < kE / 2; ++i)
+                wt[i] = wp && L.on ? pack2(to_f(wp[L.e0 + 2 * i]), to_f(wp[L.e0 + 2 * i + 1])) : pack2(1.0f, 1.0f);
+            for (int hb = h0; hb < h1; hb += kAhead * L.rows_per_warp) {
 #pragma unroll
-                for (int i = 0; i < kE; ++i) {
-                    g[i] = live ? to_f(gb[k].e[i]) : 0.0f;
-                    x[i] = (live && a.norm) ? to_f(xb[k].e[i]) : 0.0f;
-                }
-                const int rn = r + kAhead * L.rows_per_warp;
-                if (L.on && rn < r1) {
-                    gb[k].load(addr(a.y, rn), vec);
-                    if (a.norm) xb[k].load(addr(a.x, rn), vec);
-                }
-                rotate<kNeighbour>(g, c, s, L.m, w.row, L.lane);
-                if (a.norm) {
-                    const int t = r >= a.hq ? 1 : 0;
-                    float ss = 0.0f, dot = 0.0f;
+                for (int k = 0; k < kAhead; ++k) {
+                    const int first = hb + k * L.rows_per_warp;
+                    if (first >= h1) break;
+                    const int h = first + L.row_in_warp;
+                    const bool live = L.on && h < h1;
+                    uint64_t g[kE / 2], x[kE / 2], o[kE / 2];
+                    own[k].widen(o);
+                    if constexpr (kNeighbour) {
 #pragma unroll
-                    for (int i = 0; i < kE; ++i) {
-                        ss = fmaf(x[i], x[i], ss);
-                        dot = fmaf(g[i] * (t ? wt[1][i] : wt[0][i]), x[i], dot);
+                        for (int i = 0; i < kE / 2; ++i) g[i] = swap2(o[i]);
+                    } else {
+                        Pack<T> far;
+                        if (live) L.load_partners(far, gin + h * g_h, vec);
+                        far.widen(g);
                     }
-                    ss = row_sum(ss, a.lanes);
-                    dot = row_sum(dot, a.lanes);
-                    const float inv = rsqrtf(fmaf(ss, inv_d, a.eps));
-                    const float mean = dot * inv * inv_d;  // mean(g w n)
+                    val[k].widen(x);
+                    fetch(k, h + kAhead * L.rows_per_warp);
 #pragma unroll
-                    for (int i = 0; i < kE; ++i) {
-                        const float n = x[i] * inv;
-                        gw[0][i] += t ? 0.0f : g[i] * n;
-                        gw[1][i] += t ? g[i] * n : 0.0f;
-                        g[i] = inv * fmaf(-n, mean, g[i] * (t ? wt[1][i] : wt[0][i]));
+                    for (int i = 0; i < kE / 2; ++i) o[i] = fma2(o[i], c[i], mul2(g[i], s[i]));
+                    if (a.norm) {
+                        // o = g rotated back; x the head
+                        uint64_t q = mul2(x[0], x[0]), d = 0;
+#pragma unroll
+                        for (int i = 1; i < kE / 2; ++i) q = fma2(x[i], x[i], q);
+#pragma unroll
+                        for (int i = 0; i < kE / 2; ++i) {
+                            g[i] = mul2(o[i], wt[i]);
+                            d = fma2(g[i], x[i], d);
+                        }
+                        const float ss = row_sum(live ? sum2(q) : 0.0f, a.lanes);
+                        const float dot = row_sum(live ? sum2(d) : 0.0f, a.lanes);
+                        const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
+                        const float mean = dot * r * inv_d;  // mean(g w n)
+                        const uint64_t r2 = pack2(r, r), m2 = pack2(-mean, -mean);
+#pragma unroll
+                        for (int i = 0; i < kE / 2; ++i) {
+                            const uint64_t n = mul2(x[i], r2);
+                            if (live) gw[t][i] = fma2(o[i], n, gw[t][i]);
+                            o[i] = mul2(r2, fma2(n, m2, g[i]));
+                        }
                     }
-                }
-                if (live) {
-                    Pack<T> o;
-#pragma unroll
-                    for (int i = 0; i < kE; ++i) o.e[i] = from_f<T>(g[i]);
-                    o.store(addr(a.g, r), vec);
+                    __syncwarp();  // the output may be the gradient read: every lane has loaded its partners
+                    if (live) {
+                        Pack<T> y;
+                        y.round(o);
+                        y.store(out + h * out_h, vec);
+                    }
                 }
             }
         }
     }
     if (!a.part) return;
     // the block's partial sums, warps and row groups added in order
-#pragma unroll 1
-    for (int t = 0; t < 2; ++t) {
-        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < kE; ++i) w.row[L.lane * kE + i] = t ? gw[1][i] : gw[0][i];
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int i = 0; i < kE / 2; ++i)
+            *reinterpret_cast<uint64_t*>(&sums[threadIdx.x >> 5][L.lane * kE + 2 * i]) = gw[t][i];
         __syncthreads();
         for (int e = threadIdx.x; e < a.D; e += kThreads) {
             float sum = 0.0f;
             for (int v = 0; v < kWarps; ++v)
-                for (int r = 0; r < L.rows_per_warp; ++r) sum += smem[v].row[r * a.lanes * kE + e];
+                for (int r = 0; r < L.rows_per_warp; ++r) sum += sums[v][r * a.lanes * kE + e];
             a.part[(static_cast<int64_t>(blockIdx.x) * 2 + t) * a.D + e] = sum;
         }
         __syncthreads();

@@ -8,17 +8,17 @@
 //   gw = sum g * n0,  gx = r * (g w - n0 mean(g w n0)),  n0 = x r.
 //
 // Both move each element once in and once out (the backward reads two) and do
-// a few operations on it: bound by device memory. So a row is 16 or 32 bytes
-// per lane, D / 8 lanes per row, several rows in flight per warp, and the
-// arithmetic is kept short: two values per instruction, weights folded into
-// the cosines and sines, the norm's factor applied last. A warp takes all heads
-// of a token (or a share of them, when tokens are few), because the cosines
-// and sines depend on the token alone: it computes each pair's once, into
-// shared memory, and each lane keeps those of its own 8 elements in registers
-// for all of the token's heads. The partner of an element lies in the same lane
-// for neighbouring pairs; otherwise the lane loads the partners' values too, of
-// the row that the warp is loading anyway (first-level cache): as a vector where
-// they are 8 neighbours on a multiple of 8, else one by one.
+// a few operations on it: bound by device memory. So rows are read and written
+// in 16-byte pieces, several rows in flight per warp, and the arithmetic is
+// kept short: two values per instruction, weights folded into the cosines and
+// sines, the norm's factor applied last. A warp takes all heads of a token (or
+// a share of them, when tokens are few), because the cosines and sines depend
+// on the token alone: it computes each pair's once, into shared memory, and
+// each lane keeps those of its own elements in registers for all of the token's
+// heads. Where an element's partner is decides what a lane holds: neighbouring
+// pairs, or runs of 8 elements whose partners are a run of 8 too, lie in one
+// lane (16 elements); at any other distance the row goes through the warp's
+// shared memory (8 elements a lane).
 //
 // Angles: position * frequency is taken in turns as an exact product (two
 // fp32 words), its whole turns are dropped, and only then is it rounded, so
@@ -38,6 +38,8 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kBwdWarps = 4;
+constexpr int kBwdThreads = 32 * kBwdWarps;
 constexpr int kMaxD = 256;
 constexpr int kE = 8;  // elements of a row per lane
 
@@ -78,11 +80,6 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-__device__ __forceinline__ uint64_t swap2(uint64_t v) {
-    float lo, hi;
-    unpack2(v, lo, hi);
-    return pack2(hi, lo);
-}
 __device__ __forceinline__ float sum2(uint64_t v) {
     float lo, hi;
     unpack2(v, lo, hi);
@@ -116,6 +113,10 @@ struct Pack {
             for (int i = 0; i < kE; ++i) p[i] = e[i];
         }
     }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < kV; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
     __device__ __forceinline__ void widen(uint64_t (&x)[kE / 2]) const {
 #pragma unroll
         for (int i = 0; i < kE / 2; ++i) x[i] = pack2(to_f(e[2 * i]), to_f(e[2 * i + 1]));
@@ -131,23 +132,39 @@ struct Pack {
     }
 };
 
-// cos and sin of position * frequency.
-__device__ __forceinline__ void pair_turn(int32_t pos, float freq, float& c, float& s) {
+// A pair's frequency in turns per position (two fp32 words) and its axis.
+struct PairFreq {
+    float hi, lo;
+    int32_t axis;
+};
+
+__device__ __forceinline__ PairFreq pair_freq(const RotaryArgs& a, int p) {
     constexpr float kHi = 0.15915494309189535f;                                        // 1 / (2 pi), rounded
     constexpr float kLo = static_cast<float>(0.15915494309189533577 - static_cast<double>(kHi));  // what is left
-    const float hi = freq * kHi;
-    const float lo = fmaf(freq, kHi, -hi) + freq * kLo;
+    const float freq = a.freq[p];
+    PairFreq f;
+    f.hi = freq * kHi;
+    f.lo = fmaf(freq, kHi, -f.hi) + freq * kLo;
+    f.axis = 0;
+    while (f.axis < 3 && p >= a.sec_end[f.axis]) ++f.axis;
+    return f;
+}
+
+// cos and sin of position * frequency.
+__device__ __forceinline__ float2 pair_turn(int32_t pos, const PairFreq& f) {
     // the position in two parts that fp32 holds exactly
     const float pb = static_cast<float>(pos & 4095), pa = static_cast<float>(pos - (pos & 4095));
-    float ta = pa * hi, tb = pb * hi;
-    float ea = fmaf(pa, hi, -ta), eb = fmaf(pb, hi, -tb);
+    float ta = pa * f.hi, tb = pb * f.hi;
+    float ea = fmaf(pa, f.hi, -ta), eb = fmaf(pb, f.hi, -tb);
     ta -= rintf(ta);
     tb -= rintf(tb);
     ea -= rintf(ea);
-    const float rest = (pa + pb) * lo;
+    const float rest = (pa + pb) * f.lo;
     float t = (ta + tb) + ((ea + eb) + (rest - rintf(rest)));
     t -= rintf(t);
-    sincospif(2.0f * t, &s, &c);
+    float2 cs;
+    sincospif(2.0f * t, &cs.y, &cs.x);
+    return cs;
 }
 
 // Element e of a head: its pair (or -1 past the rotated part), its partner,
@@ -179,81 +196,182 @@ __device__ __forceinline__ int pair_of(const RotaryArgs& a, int e, int& partner,
     return p;
 }
 
-// Sum over the lanes that share a row.
+// Sum over the lanes that share a row (a power of two of them).
 __device__ __forceinline__ float row_sum(float v, int lanes) {
-    for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        if (lanes > o) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
-// One warp's shared memory: a token's (cos, sin) of each pair.
-struct alignas(16) WarpSmem {
-    float cs[kMaxD];
+// Where an element's partner is.
+enum RotaryMode {
+    kBeside = 0,   // neighbouring pairs: in the same register pair
+    kChunks = 1,   // every run of 8 elements has a run of 8 partners: the lane holds both
+    kAnywhere = 2  // any distance, or rows off 16 bytes: through the warp's shared memory
 };
 
-// A lane's place in its row: 8 elements from e0 on, and where their partners
-// lie.
+template <int kMode>
+struct alignas(16) WarpSmem {
+    float2 cs[kMaxD / 2];                             // (cos, sin) of a token's pairs
+    float row[2][kMode == kAnywhere ? 32 * kE : 4];   // kAnywhere: the warp's rows, two in turn
+};
+
+// A lane's place in its row: one chunk of 8 elements (kAnywhere) or two, at
+// e0[0] and e0[1]; and where to find its pairs' cosines and sines.
+template <int kMode>
 struct LaneSetup {
-    int lane, rows_per_warp, row_in_warp, e0;
-    bool on;               // the lane has elements
-    bool run;              // its 8 partners are 8 neighbouring elements that start on a multiple of 8
-    uint32_t code[kE / 2]; // two elements each: partner, 8 bits; pair, 7 bits; rotated, 1 bit
+    static constexpr int kC = kMode == kAnywhere ? 1 : 2;
+    int lane, rows_per_warp, row_in_warp;
+    int e0[kC];
+    bool on[kC];  // the chunk exists
+    int pair0;    // kBeside, kChunks: the lane's first pair; kChunks: past the pairs where it is not rotated
+    // kAnywhere, two elements to a word: partner's index in the warp's rows (8 bits) and
+    // pair (7 bits), rotated (1 bit)
+    uint32_t code[kMode == kAnywhere ? kE / 2 : 1];
     __device__ __forceinline__ LaneSetup(const RotaryArgs& a) {
         lane = threadIdx.x & 31;
         const int sub = lane & (a.lanes - 1);
         rows_per_warp = 32 / a.lanes;
         row_in_warp = lane / a.lanes;
-        e0 = sub * kE;
-        on = e0 < a.D;
-        run = true;
-        int first = 0;
+        if constexpr (kMode == kAnywhere) {
+            e0[0] = sub * kE;
+#pragma unroll
+            for (int i = 0; i < kE; ++i) {
+                int to = e0[0] + i;
+                float sign;
+                const int p = e0[0] < a.D ? pair_of(a, e0[0] + i, to, sign) : -1;
+                const uint32_t v = static_cast<uint32_t>(row_in_warp * a.lanes * kE + to) |
+                                   (p >= 0 ? static_cast<uint32_t>(p) << 8 | 0x8000u : 0u);
+                code[i / 2] = i & 1 ? code[i / 2] | v << 16 : v;
+            }
+        } else if constexpr (kMode == kBeside) {
+            e0[0] = sub * 2 * kE;
+            e0[1] = e0[0] + kE;
+            pair0 = sub * kE;
+        } else {
+            // the rotated chunks first, each with its partner, then the others two by two
+            const int pairs8 = a.pairs / kE;
+            pair0 = sub * kE;
+            if (sub >= pairs8) {
+                e0[0] = (2 * pairs8 + 2 * (sub - pairs8)) * kE;
+                e0[1] = e0[0] + kE;
+            } else if (a.layout == 0) {
+                e0[0] = sub * kE;
+                e0[1] = e0[0] + a.pairs;
+            } else {
+                int first = 0, ax = 0;
+                while (ax < 3 && sub * kE >= a.sec_end[ax]) first = a.sec_end[ax++];
+                e0[0] = first + sub * kE;  // 2 first + (8 sub - first)
+                e0[1] = e0[0] + a.sec_end[ax] - first;
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < kC; ++c) on[c] = e0[c] < a.D;
+    }
+};
+
+// The block's table of pair frequencies (all threads; ends with a barrier).
+__device__ __forceinline__ void fill_freqs(const RotaryArgs& a, PairFreq* table) {
+    for (int p = threadIdx.x; p < a.pairs; p += blockDim.x) table[p] = pair_freq(a, p);
+    __syncthreads();
+}
+
+// The cosine of each of the token's pairs, and its sine, into the warp's shared memory.
+template <int kMode>
+__device__ __forceinline__ void turn_pairs(const RotaryArgs& a, int token, const PairFreq* table, WarpSmem<kMode>& w,
+                                           int lane) {
+    const int32_t* pos = a.pos + static_cast<int64_t>(token) * a.axes;
+    __syncwarp();
+    for (int p = lane; p < a.pairs; p += 32) {
+        const PairFreq f = table[p];
+        w.cs[p] = pair_turn(__ldg(pos + f.axis), f);
+    }
+    __syncwarp();
+}
+
+// A token's turns for the lane's 8 pairs (kBeside, kChunks: one cosine and
+// sine per pair) or 8 elements (kAnywhere: the sine has the sign of the
+// element's place in its pair). direction -1 turns back.
+template <int kMode>
+struct Turns {
+    float c[kE], s[kE];
+    __device__ __forceinline__ Turns(const RotaryArgs& a, const LaneSetup<kMode>& L, const WarpSmem<kMode>& w,
+                                     float direction) {
 #pragma unroll
         for (int i = 0; i < kE; ++i) {
-            int to = e0 + i;
-            float sg = 0.0f;
-            const int p = on ? pair_of(a, e0 + i, to, sg) : -1;
-            if (i == 0) first = to;
-            run = run && to == first + i;
-            const uint32_t v = static_cast<uint32_t>(to) | (p >= 0 ? (static_cast<uint32_t>(p) << 8 | 0x8000u) : 0u);
-            code[i / 2] = i & 1 ? code[i / 2] | v << 16 : v;
+            float2 v = make_float2(1.0f, 0.0f);
+            if constexpr (kMode == kAnywhere) {
+                const uint32_t e = L.code[i / 2] >> (16 * (i & 1));
+                if (e & 0x8000u) v = w.cs[(e >> 8) & 0x7fu];
+                // the first element of a pair lies before its partner
+                const bool low = static_cast<int>(e & 0xffu) > L.lane * kE + i;
+                s[i] = low ? -direction * v.y : direction * v.y;
+            } else {
+                if (L.pair0 + i < a.pairs) v = w.cs[L.pair0 + i];
+                s[i] = direction * v.y;
+            }
+            c[i] = v.x;
         }
-        run = run && (first & 7) == 0;
-        // one path for the warp: narrow partner loads wherever one lane needs them
-        run = __all_sync(0xffffffffu, run || !on) != 0;
     }
-    __device__ __forceinline__ uint32_t entry(int i) const { return code[i / 2] >> (16 * (i & 1)); }
-    __device__ __forceinline__ int partner(int i) const { return static_cast<int>(entry(i) & 0xffu); }
-    // The partners of the lane's elements, from the row that starts at `row`.
-    template <typename T>
-    __device__ __forceinline__ void load_partners(Pack<T>& p, const T* row, bool vec) const {
-        if (run) {
-            p.load(row + partner(0), vec);
-        } else {
+    // x turned; kAnywhere: through `buf`, a row buffer of the warp that no lane reads any more.
+    template <int kC>
+    __device__ __forceinline__ void turn(uint64_t (&x)[kC][kE / 2], const LaneSetup<kMode>& L, float* buf) const {
+        if constexpr (kMode == kBeside) {
 #pragma unroll
-            for (int i = 0; i < kE; ++i) p.e[i] = row[partner(i)];
+            for (int k = 0; k < kC; ++k)
+#pragma unroll
+                for (int i = 0; i < kE / 2; ++i) {
+                    const int p = k * (kE / 2) + i;
+                    float lo, hi;
+                    unpack2(x[k][i], lo, hi);
+                    x[k][i] = pack2(fmaf(lo, c[p], -(hi * s[p])), fmaf(hi, c[p], lo * s[p]));
+                }
+        } else if constexpr (kMode == kChunks) {
+#pragma unroll
+            for (int i = 0; i < kE / 2; ++i) {
+                const uint64_t c2 = pack2(c[2 * i], c[2 * i + 1]), s2 = pack2(s[2 * i], s[2 * i + 1]);
+                const uint64_t n2 = pack2(-s[2 * i], -s[2 * i + 1]);
+                const uint64_t lo = fma2(x[1][i], n2, mul2(x[0][i], c2));
+                x[1][i] = fma2(x[0][i], s2, mul2(x[1][i], c2));
+                x[0][i] = lo;
+            }
+        } else {
+            ulonglong2* mine = reinterpret_cast<ulonglong2*>(buf + L.lane * kE);
+            mine[0] = make_ulonglong2(x[0][0], x[0][1]);
+            mine[1] = make_ulonglong2(x[0][2], x[0][3]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < kE / 2; ++i) {
+                const uint64_t far = pack2(buf[L.code[i] & 0xffu], buf[(L.code[i] >> 16) & 0xffu]);
+                const uint64_t c2 = pack2(c[2 * i], c[2 * i + 1]), s2 = pack2(s[2 * i], s[2 * i + 1]);
+                x[0][i] = fma2(x[0][i], c2, mul2(far, s2));
+            }
         }
     }
-    // The cosine of each of the token's pairs, and its sine, into the warp's shared memory.
-    __device__ __forceinline__ void turn_pairs(const RotaryArgs& a, int token, WarpSmem& w) const {
-        __syncwarp();
-        for (int p = lane; p < a.pairs; p += 32) {
-            int ax = 0;
-            while (ax < 3 && p >= a.sec_end[ax]) ++ax;
-            float cp, sp;
-            pair_turn(__ldg(a.pos + static_cast<int64_t>(token) * a.axes + ax), __ldg(a.freq + p), cp, sp);
-            *reinterpret_cast<float2*>(&w.cs[2 * p]) = make_float2(cp, sp);
+};
+
+// The weight of the lane's elements (ones where there is none).
+template <typename T, int kMode>
+struct Weights {
+    static constexpr int kC = LaneSetup<kMode>::kC;
+    Pack<T> w[kC];
+    bool given;
+    __device__ __forceinline__ Weights(const void* p, const LaneSetup<kMode>& L) {
+        given = p != nullptr;
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            w[c].clear();
+            if (given && L.on[c]) w[c].load(static_cast<const T*>(p) + L.e0[c], true);
         }
-        __syncwarp();
     }
-    // Of this lane's element i: the cosine, and the sine with the sign that it
-    // has in the forward (first of its pair: minus) times `direction`.
-    __device__ __forceinline__ void turn_of(const WarpSmem& w, int i, float direction, float& c, float& s) const {
-        const uint32_t v = entry(i);
-        c = 1.0f;
-        s = 0.0f;
-        if (v & 0x8000u) {
-            const float2 t = *reinterpret_cast<const float2*>(&w.cs[2 * ((v >> 8) & 0x7fu)]);
-            c = t.x;
-            s = static_cast<int>(v & 0xffu) > e0 + i ? -direction * t.y : direction * t.y;
+    __device__ __forceinline__ void apply(uint64_t (&x)[kC][kE / 2], const uint64_t (&y)[kC][kE / 2]) const {
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            uint64_t f[kE / 2];
+            w[c].widen(f);
+#pragma unroll
+            for (int i = 0; i < kE / 2; ++i) x[c][i] = given ? mul2(y[c][i], f[i]) : y[c][i];
         }
     }
 };
@@ -264,13 +382,16 @@ __device__ __forceinline__ void part_rows(const RotaryArgs& a, int t, int r0, in
     h1 = t ? r1 - a.hq : min(r1, a.hq);
 }
 
-template <typename T, bool kNeighbour>
-__global__ void __launch_bounds__(kThreads, 3) rotary_forward_kernel(const __grid_constant__ RotaryArgs a) {
-    __shared__ WarpSmem smem[kWarps];
-    WarpSmem& w = smem[threadIdx.x >> 5];
-    const LaneSetup L(a);
-    const bool vec = a.vec != 0;
+template <typename T, int kMode>
+__global__ void __launch_bounds__(kThreads, 2) rotary_forward_kernel(const __grid_constant__ RotaryArgs a) {
+    constexpr int kC = LaneSetup<kMode>::kC;
+    __shared__ WarpSmem<kMode> smem[kWarps];
+    __shared__ PairFreq table[kMaxD / 2];
+    WarpSmem<kMode>& w = smem[threadIdx.x >> 5];
+    const LaneSetup<kMode> L(a);
+    const bool vec = kMode != kAnywhere || a.vec != 0;
     const float inv_d = 1.0f / static_cast<float>(a.D);
+    fill_freqs(a, table);
 
     const int64_t units = static_cast<int64_t>(a.tokens) * a.parts;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps;
@@ -287,201 +408,192 @@ __global__ void __launch_bounds__(kThreads, 3) rotary_forward_kernel(const __gri
             part_rows(a, t, r0, r1, h0, h1);
             if (h0 >= h1) continue;
             const T* in = static_cast<const T*>(a.x[t].p) + static_cast<int64_t>(token) * a.x[t].st;
-            T* out = static_cast<T*>(a.y[t].p) + static_cast<int64_t>(token) * a.y[t].st + L.e0;
+            T* out = static_cast<T*>(a.y[t].p) + static_cast<int64_t>(token) * a.y[t].st;
             const int64_t in_h = a.x[t].sh, out_h = a.y[t].sh;
             // the next rows' loads are in flight while a row is worked on
-            constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
-            Pack<T> own[kAhead];
+            constexpr int kAhead = sizeof(T) == 4 ? 2 : (kMode == kAnywhere ? 4 : 3);
+            Pack<T> own[kAhead][kC];
             auto fetch = [&](int k, int h) {
-                if (L.on && h < h1) own[k].load(in + h * in_h + L.e0, vec);
+#pragma unroll
+                for (int c = 0; c < kC; ++c)
+                    if (L.on[c] && h < h1) own[k][c].load(in + h * in_h + L.e0[c], vec);
             };
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) fetch(k, h0 + k * L.rows_per_warp + L.row_in_warp);
-            if (!turned) L.turn_pairs(a, token, w);
+            const Weights<T, kMode> wt(a.w[t], L);
+            if (!turned) turn_pairs(a, token, table, w, L.lane);
             turned = true;
-            // y = r (x w c + x' w' s), x' the partner and w' its weight: the norm's factor r comes last
-            uint64_t wc[kE / 2], ws[kE / 2];
-            const T* wt = static_cast<const T*>(a.w[t]);
-#pragma unroll
-            for (int i = 0; i < kE / 2; ++i) {
-                float c[2], s[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    L.turn_of(w, 2 * i + j, 1.0f, c[j], s[j]);
-                    if (wt && L.on) {
-                        c[j] *= to_f(wt[L.e0 + 2 * i + j]);
-                        s[j] *= to_f(wt[L.partner(2 * i + j)]);
-                    }
-                }
-                wc[i] = pack2(c[0], c[1]);
-                ws[i] = pack2(s[0], s[1]);
-            }
+            const Turns<kMode> turns(a, L, w, 1.0f);
+            int which = 0;
             for (int hb = h0; hb < h1; hb += kAhead * L.rows_per_warp) {
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k) {
                     const int first = hb + k * L.rows_per_warp;
                     if (first >= h1) break;
                     const int h = first + L.row_in_warp;
-                    const bool live = L.on && h < h1;
-                    uint64_t x[kE / 2], y[kE / 2];
-                    own[k].widen(x);
-                    if constexpr (kNeighbour) {
+                    uint64_t x[kC][kE / 2];
 #pragma unroll
-                        for (int i = 0; i < kE / 2; ++i) y[i] = swap2(x[i]);
-                    } else {
-                        Pack<T> far;
-                        if (live) L.load_partners(far, in + h * in_h, vec);
-                        far.widen(y);
+                    for (int c = 0; c < kC; ++c) {
+                        if (!L.on[c] || h >= h1) own[k][c].clear();
+                        own[k][c].widen(x[c]);
                     }
                     fetch(k, h + kAhead * L.rows_per_warp);
-#pragma unroll
-                    for (int i = 0; i < kE / 2; ++i) y[i] = fma2(x[i], wc[i], mul2(y[i], ws[i]));
+                    float r = 1.0f;
                     if (a.norm) {
-                        uint64_t q = mul2(x[0], x[0]);
+                        uint64_t q = 0;
 #pragma unroll
-                        for (int i = 1; i < kE / 2; ++i) q = fma2(x[i], x[i], q);
-                        const float ss = row_sum(live ? sum2(q) : 0.0f, a.lanes);
-                        const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
-                        const uint64_t r2 = pack2(r, r);
+                        for (int c = 0; c < kC; ++c)
 #pragma unroll
-                        for (int i = 0; i < kE / 2; ++i) y[i] = mul2(y[i], r2);
+                            for (int i = 0; i < kE / 2; ++i) q = fma2(x[c][i], x[c][i], q);
+                        r = rsqrtf(fmaf(row_sum(sum2(q), a.lanes), inv_d, a.eps));
+                        wt.apply(x, x);
                     }
-                    __syncwarp();  // y may be x: every lane has loaded its partners
-                    if (live) {
-                        Pack<T> o;
-                        o.round(y);
-                        o.store(out + h * out_h, vec);
-                    }
+                    turns.turn(x, L, w.row[which]);
+                    which ^= 1;
+                    const uint64_t r2 = pack2(r, r);
+#pragma unroll
+                    for (int c = 0; c < kC; ++c)
+                        if (L.on[c] && h < h1) {
+                            // the norm's factor, common to the row, comes last
+#pragma unroll
+                            for (int i = 0; i < kE / 2; ++i) x[c][i] = mul2(x[c][i], r2);
+                            Pack<T> o;
+                            o.round(x[c]);
+                            o.store(out + h * out_h + L.e0[c], vec);
+                        }
                 }
             }
         }
     }
 }
 
-template <typename T, bool kNeighbour>
-__global__ void __launch_bounds__(kThreads, 2) rotary_backward_kernel(const __grid_constant__ RotaryArgs a) {
-    __shared__ WarpSmem smem[kWarps];
-    __shared__ alignas(16) float sums[kWarps][32 * kE];
-    WarpSmem& w = smem[threadIdx.x >> 5];
-    const LaneSetup L(a);
-    const bool vec = a.vec != 0;
+// First all heads of q, then all of k, so that one weight's sums and values
+// are live at a time: 12 warps to an SM with 168 registers, two rows of each in
+// flight (8 warps of 4 groups, or 16 with half the elements a lane, spill or
+// issue more instructions than the bytes leave time for).
+template <typename T, int kMode>
+__global__ void __launch_bounds__(kBwdThreads, 3) rotary_backward_kernel(const __grid_constant__ RotaryArgs a) {
+    constexpr int kC = LaneSetup<kMode>::kC;
+    __shared__ WarpSmem<kMode> smem[kBwdWarps];
+    __shared__ PairFreq table[kMaxD / 2];
+    __shared__ float sums[kBwdWarps][kMaxD];
+    WarpSmem<kMode>& w = smem[threadIdx.x >> 5];
+    const LaneSetup<kMode> L(a);
+    const bool vec = kMode != kAnywhere || a.vec != 0;
     const float inv_d = 1.0f / static_cast<float>(a.D);
-    uint64_t gw[2][kE / 2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < kE / 2; ++i) gw[t][i] = 0;
+    fill_freqs(a, table);
 
     const int64_t units = static_cast<int64_t>(a.tokens) * a.parts;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps;
-    const int share = ((a.rows + a.parts * L.rows_per_warp - 1) / (a.parts * L.rows_per_warp)) * L.rows_per_warp;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); u < units; u += stride) {
-        const int token = static_cast<int>(u / a.parts), part = static_cast<int>(u % a.parts);
-        const int r0 = part * share, r1 = min(r0 + share, a.rows);
-        if (r0 >= r1) continue;
-        uint64_t c[kE / 2], s[kE / 2];
-        bool turned = false;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kBwdWarps;
+#pragma unroll 1
+    for (int t = 0; t < 2; ++t) {
+        const int heads = t ? a.rows - a.hq : a.hq;
+        const int share = ((heads + a.parts * L.rows_per_warp - 1) / (a.parts * L.rows_per_warp)) * L.rows_per_warp;
+        const int64_t g_h = a.y[t].sh, x_h = a.x[t].sh, out_h = a.g[t].sh;
+        uint64_t gw[kC][kE / 2];
+        const Weights<T, kMode> wt(a.w[t], L);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            int h0, h1;
-            part_rows(a, t, r0, r1, h0, h1);
+        for (int c = 0; c < kC; ++c)
+#pragma unroll
+            for (int i = 0; i < kE / 2; ++i) gw[c][i] = 0;
+        for (int64_t u = static_cast<int64_t>(blockIdx.x) * kBwdWarps + (threadIdx.x >> 5); u < units; u += stride) {
+            const int token = static_cast<int>(u / a.parts), part = static_cast<int>(u % a.parts);
+            const int h0 = part * share, h1 = min(h0 + share, heads);
             if (h0 >= h1) continue;
             const T* gin = static_cast<const T*>(a.y[t].p) + static_cast<int64_t>(token) * a.y[t].st;
-            const T* xin = static_cast<const T*>(a.x[t].p) + static_cast<int64_t>(token) * a.x[t].st + L.e0;
-            T* out = static_cast<T*>(a.g[t].p) + static_cast<int64_t>(token) * a.g[t].st + L.e0;
-            const int64_t g_h = a.y[t].sh, x_h = a.x[t].sh, out_h = a.g[t].sh;
-            constexpr int kAhead = 2;
-            Pack<T> own[kAhead], val[kAhead];
+            const T* xin = static_cast<const T*>(a.x[t].p) + static_cast<int64_t>(token) * a.x[t].st;
+            T* out = static_cast<T*>(a.g[t].p) + static_cast<int64_t>(token) * a.g[t].st;
+            constexpr int kAhead = sizeof(T) == 4 ? 1 : 2;
+            Pack<T> own[kAhead][kC], val[kAhead][kC];
             auto fetch = [&](int k, int h) {
-                if (L.on && h < h1) {
-                    own[k].load(gin + h * g_h + L.e0, vec);
-                    if (a.norm) val[k].load(xin + h * x_h, vec);
-                }
+#pragma unroll
+                for (int c = 0; c < kC; ++c)
+                    if (L.on[c] && h < h1) {
+                        own[k][c].load(gin + h * g_h + L.e0[c], vec);
+                        if (a.norm) val[k][c].load(xin + h * x_h + L.e0[c], vec);
+                    }
             };
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) fetch(k, h0 + k * L.rows_per_warp + L.row_in_warp);
-            if (!turned) {
-                L.turn_pairs(a, token, w);
-#pragma unroll
-                for (int i = 0; i < kE / 2; ++i) {
-                    float cf[2], sf[2];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) L.turn_of(w, 2 * i + j, -1.0f, cf[j], sf[j]);
-                    c[i] = pack2(cf[0], cf[1]);
-                    s[i] = pack2(sf[0], sf[1]);
-                }
-            }
-            turned = true;
-            uint64_t wt[kE / 2];
-            const T* wp = static_cast<const T*>(a.w[t]);
-#pragma unroll
-            for (int i = 0; i < kE / 2; ++i)
-                wt[i] = wp && L.on ? pack2(to_f(wp[L.e0 + 2 * i]), to_f(wp[L.e0 + 2 * i + 1])) : pack2(1.0f, 1.0f);
+            turn_pairs(a, token, table, w, L.lane);
+            const Turns<kMode> turns(a, L, w, -1.0f);
+            int which = 0;
             for (int hb = h0; hb < h1; hb += kAhead * L.rows_per_warp) {
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k) {
                     const int first = hb + k * L.rows_per_warp;
                     if (first >= h1) break;
                     const int h = first + L.row_in_warp;
-                    const bool live = L.on && h < h1;
-                    uint64_t g[kE / 2], x[kE / 2], o[kE / 2];
-                    own[k].widen(o);
-                    if constexpr (kNeighbour) {
+                    uint64_t g[kC][kE / 2], x[kC][kE / 2], o[kC][kE / 2];
 #pragma unroll
-                        for (int i = 0; i < kE / 2; ++i) g[i] = swap2(o[i]);
-                    } else {
-                        Pack<T> far;
-                        if (live) L.load_partners(far, gin + h * g_h, vec);
-                        far.widen(g);
-                    }
-                    val[k].widen(x);
-                    fetch(k, h + kAhead * L.rows_per_warp);
-#pragma unroll
-                    for (int i = 0; i < kE / 2; ++i) o[i] = fma2(o[i], c[i], mul2(g[i], s[i]));
-                    if (a.norm) {
-                        // o = g rotated back; x the head
-                        uint64_t q = mul2(x[0], x[0]), d = 0;
-#pragma unroll
-                        for (int i = 1; i < kE / 2; ++i) q = fma2(x[i], x[i], q);
-#pragma unroll
-                        for (int i = 0; i < kE / 2; ++i) {
-                            g[i] = mul2(o[i], wt[i]);
-                            d = fma2(g[i], x[i], d);
+                    for (int c = 0; c < kC; ++c) {
+                        if (!L.on[c] || h >= h1) {
+                            own[k][c].clear();
+                            val[k][c].clear();
                         }
-                        const float ss = row_sum(live ? sum2(q) : 0.0f, a.lanes);
-                        const float dot = row_sum(live ? sum2(d) : 0.0f, a.lanes);
+                        own[k][c].widen(o[c]);
+                        if (a.norm) val[k][c].widen(x[c]);
+                    }
+                    fetch(k, h + kAhead * L.rows_per_warp);
+                    turns.turn(o, L, w.row[which]);
+                    which ^= 1;
+                    if (a.norm) {
+                        // o = the gradient rotated back; x the head
+                        uint64_t q = 0, d = 0;
+                        wt.apply(g, o);
+#pragma unroll
+                        for (int c = 0; c < kC; ++c)
+#pragma unroll
+                            for (int i = 0; i < kE / 2; ++i) {
+                                q = fma2(x[c][i], x[c][i], q);
+                                d = fma2(g[c][i], x[c][i], d);
+                            }
+                        const float ss = row_sum(sum2(q), a.lanes), dot = row_sum(sum2(d), a.lanes);
                         const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
                         const float mean = dot * r * inv_d;  // mean(g w n)
                         const uint64_t r2 = pack2(r, r), m2 = pack2(-mean, -mean);
 #pragma unroll
-                        for (int i = 0; i < kE / 2; ++i) {
-                            const uint64_t n = mul2(x[i], r2);
-                            if (live) gw[t][i] = fma2(o[i], n, gw[t][i]);
-                            o[i] = mul2(r2, fma2(n, m2, g[i]));
+                        for (int c = 0; c < kC; ++c)
+#pragma unroll
+                            for (int i = 0; i < kE / 2; ++i) {
+                                const uint64_t n = mul2(x[c][i], r2);
+                                gw[c][i] = fma2(o[c][i], n, gw[c][i]);
+                                o[c][i] = mul2(r2, fma2(n, m2, g[c][i]));
+                            }
+                    }
+#pragma unroll
+                    for (int c = 0; c < kC; ++c)
+                        if (L.on[c] && h < h1) {
+                            Pack<T> y;
+                            y.round(o[c]);
+                            y.store(out + h * out_h + L.e0[c], vec);
                         }
-                    }
-                    __syncwarp();  // the output may be the gradient read: every lane has loaded its partners
-                    if (live) {
-                        Pack<T> y;
-                        y.round(o);
-                        y.store(out + h * out_h, vec);
-                    }
                 }
             }
         }
-    }
-    if (!a.part) return;
-    // the block's partial sums, warps and row groups added in order
+        if (!a.part) continue;
+        // the block's partial sums, warps and row groups added in order
+        for (int g = 0; g < L.rows_per_warp; ++g) {
+            if (L.row_in_warp == g) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+                for (int c = 0; c < kC; ++c)
+                    if (L.on[c]) {
 #pragma unroll
-        for (int i = 0; i < kE / 2; ++i)
-            *reinterpret_cast<uint64_t*>(&sums[threadIdx.x >> 5][L.lane * kE + 2 * i]) = gw[t][i];
+                        for (int i = 0; i < kE / 2; ++i) {
+                            float lo, hi;
+                            unpack2(gw[c][i], lo, hi);
+                            float* at = &sums[threadIdx.x >> 5][L.e0[c] + 2 * i];
+                            at[0] = g ? at[0] + lo : lo;
+                            at[1] = g ? at[1] + hi : hi;
+                        }
+                    }
+            }
+            __syncwarp();
+        }
         __syncthreads();
-        for (int e = threadIdx.x; e < a.D; e += kThreads) {
+        for (int e = threadIdx.x; e < a.D; e += kBwdThreads) {
             float sum = 0.0f;
-            for (int v = 0; v < kWarps; ++v)
-                for (int r = 0; r < L.rows_per_warp; ++r) sum += sums[v][r * a.lanes * kE + e];
+            for (int v = 0; v < kBwdWarps; ++v) sum += sums[v][e];
             a.part[(static_cast<int64_t>(blockIdx.x) * 2 + t) * a.D + e] = sum;
         }
         __syncthreads();
@@ -509,38 +621,49 @@ __global__ void __launch_bounds__(kThreads) rotary_weight_sum_kernel(const float
     }
 }
 
-// Lanes per row, and how many warps share a token's rows: one where tokens
-// alone fill the GPU (the token's cosines are then computed once), more where
-// they are few.
-void plan_lanes(RotaryArgs* a, int sms) {
+// Where the partners are; lanes per row; and how many warps share a token's
+// rows: one where tokens alone fill the GPU (the token's cosines are then
+// computed once), more where they are few.
+RotaryMode plan_lanes(RotaryArgs* a, int sms) {
+    bool runs = a->layout == 0 ? a->pairs % kE == 0 : true;
+    for (int i = 0; a->layout == 2 && i < 4; ++i) runs = runs && a->sec_end[i] % kE == 0;
+    const RotaryMode mode = !a->vec ? kAnywhere : a->layout == 1 ? kBeside : runs ? kChunks : kAnywhere;
+    const int per_lane = mode == kAnywhere ? kE : 2 * kE;
     a->lanes = 1;
-    while (a->lanes * kE < a->D) a->lanes *= 2;
+    while (a->lanes * per_lane < a->D) a->lanes *= 2;
     const int rpw = 32 / a->lanes;
     const int most = (a->rows + rpw - 1) / rpw;
-    const int64_t want = static_cast<int64_t>(sms) * 24;  // warps that keep the loads in flight
+    const int64_t want = static_cast<int64_t>(sms) * 16;  // warps that keep the loads in flight
     int64_t parts = (want + a->tokens - 1) / a->tokens;
     a->parts = static_cast<int32_t>(parts < most ? parts : most);
+    return mode;
 }
 
-int64_t blocks_for(const RotaryArgs& a) {
-    return (static_cast<int64_t>(a.tokens) * a.parts + kWarps - 1) / kWarps;
+int64_t blocks_for(const RotaryArgs& a, int warps) {
+    return (static_cast<int64_t>(a.tokens) * a.parts + warps - 1) / warps;
 }
 
 template <typename T>
-cudaError_t forward_t(const RotaryArgs& a, int64_t grid, cudaStream_t st) {
-    if (a.layout == 1)
-        rotary_forward_kernel<T, true><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a);
+cudaError_t forward_t(const RotaryArgs& a, RotaryMode mode, int64_t grid, cudaStream_t st) {
+    const unsigned g = static_cast<unsigned>(grid);
+    if (mode == kBeside)
+        rotary_forward_kernel<T, kBeside><<<g, kThreads, 0, st>>>(a);
+    else if (mode == kChunks)
+        rotary_forward_kernel<T, kChunks><<<g, kThreads, 0, st>>>(a);
     else
-        rotary_forward_kernel<T, false><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a);
+        rotary_forward_kernel<T, kAnywhere><<<g, kThreads, 0, st>>>(a);
     return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t backward_t(const RotaryArgs& a, int64_t grid, void* gqw, void* gkw, cudaStream_t st) {
-    if (a.layout == 1)
-        rotary_backward_kernel<T, true><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a);
+cudaError_t backward_t(const RotaryArgs& a, RotaryMode mode, int64_t grid, void* gqw, void* gkw, cudaStream_t st) {
+    const unsigned g = static_cast<unsigned>(grid);
+    if (mode == kBeside)
+        rotary_backward_kernel<T, kBeside><<<g, kBwdThreads, 0, st>>>(a);
+    else if (mode == kChunks)
+        rotary_backward_kernel<T, kChunks><<<g, kBwdThreads, 0, st>>>(a);
     else
-        rotary_backward_kernel<T, false><<<static_cast<unsigned>(grid), kThreads, 0, st>>>(a);
+        rotary_backward_kernel<T, kAnywhere><<<g, kBwdThreads, 0, st>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !a.part) return e;
     cudaLaunchConfig_t cfg = {};
@@ -560,21 +683,22 @@ cudaError_t backward_t(const RotaryArgs& a, int64_t grid, void* gqw, void* gkw, 
 }  // namespace
 
 cudaError_t launch_rotary_forward(int dtype, RotaryArgs a, int sms, cudaStream_t st) {
-    plan_lanes(&a, sms);
-    int64_t grid = blocks_for(a);
+    const RotaryMode mode = plan_lanes(&a, sms);
+    int64_t grid = blocks_for(a, kWarps);
     if (grid > static_cast<int64_t>(sms) * 16) grid = static_cast<int64_t>(sms) * 16;
-    if (dtype == kF32) return forward_t<float>(a, grid, st);
-    if (dtype == kF16) return forward_t<__half>(a, grid, st);
-    return forward_t<__nv_bfloat16>(a, grid, st);
+    if (dtype == kF32) return forward_t<float>(a, mode, grid, st);
+    if (dtype == kF16) return forward_t<__half>(a, mode, grid, st);
+    return forward_t<__nv_bfloat16>(a, mode, grid, st);
 }
 
 cudaError_t launch_rotary_backward(int dtype, RotaryArgs a, void* gqw, void* gkw, int sms, cudaStream_t st) {
-    plan_lanes(&a, sms);
-    int64_t grid = blocks_for(a);
+    const RotaryMode mode = plan_lanes(&a, sms);
+    int64_t grid = blocks_for(a, kBwdWarps);
+    if (grid > static_cast<int64_t>(sms) * 3) grid = static_cast<int64_t>(sms) * 3;  // one wave
     if (grid > kRotaryMaxBlocks) grid = kRotaryMaxBlocks;
-    if (dtype == kF32) return backward_t<float>(a, grid, gqw, gkw, st);
-    if (dtype == kF16) return backward_t<__half>(a, grid, gqw, gkw, st);
-    return backward_t<__nv_bfloat16>(a, grid, gqw, gkw, st);
+    if (dtype == kF32) return backward_t<float>(a, mode, grid, gqw, gkw, st);
+    if (dtype == kF16) return backward_t<__half>(a, mode, grid, gqw, gkw, st);
+    return backward_t<__nv_bfloat16>(a, mode, grid, gqw, gkw, st);
 }
 
 }  // namespace mdcn

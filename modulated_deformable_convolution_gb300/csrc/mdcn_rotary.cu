@@ -41,7 +41,10 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kBwdWarps = 4;
 constexpr int kBwdThreads = 32 * kBwdWarps;
 constexpr int kMaxD = 256;
-constexpr int kE = 8;  // elements of a row per lane
+constexpr int kE = 8;  // elements of a chunk
+// A warp's rows together have at most 32 lanes' 16 elements, so 256 pairs,
+// whether they are of one token or of several.
+constexpr int kMaxTurns = 256;
 
 __device__ __forceinline__ float to_f(float v) { return v; }
 __device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
@@ -59,6 +62,18 @@ __device__ __forceinline__ __half from_f<__half>(float v) {
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
     return __float2bfloat16_rn(v);
+}
+
+// (lo, hi) rounded to two neighbouring 16-bit elements.
+__device__ __forceinline__ void round_pair(float lo, float hi, __half* e) {
+    *reinterpret_cast<__half2*>(e) = __floats2half2_rn(lo, hi);
+}
+__device__ __forceinline__ void round_pair(float lo, float hi, __nv_bfloat16* e) {
+    *reinterpret_cast<__nv_bfloat162*>(e) = __floats2bfloat162_rn(lo, hi);
+}
+__device__ __forceinline__ void round_pair(float lo, float hi, float* e) {
+    e[0] = lo;
+    e[1] = hi;
 }
 
 // Two fp32 values in one register pair: one instruction works on both.
@@ -126,8 +141,7 @@ struct Pack {
         for (int i = 0; i < kE / 2; ++i) {
             float lo, hi;
             unpack2(x[i], lo, hi);
-            e[2 * i] = from_f<T>(lo);
-            e[2 * i + 1] = from_f<T>(hi);
+            round_pair(lo, hi, e + 2 * i);
         }
     }
 };
@@ -213,7 +227,7 @@ enum RotaryMode {
 
 template <int kMode>
 struct alignas(16) WarpSmem {
-    float2 cs[kMaxD / 2];                             // (cos, sin) of a token's pairs
+    float2 cs[kMaxTurns];                             // (cos, sin) of the pairs of the warp's tokens
     float row[2][kMode == kAnywhere ? 32 * kE : 4];   // kAnywhere: the warp's rows, two in turn
 };
 
@@ -277,16 +291,18 @@ __device__ __forceinline__ void fill_freqs(const RotaryArgs& a, PairFreq* table)
     __syncthreads();
 }
 
-// The cosine of each of the token's pairs, and its sine, into the warp's shared memory.
+// The cosine of each pair, and its sine, of `n` tokens from `token` on into the
+// warp's shared memory.
 template <int kMode>
-__device__ __forceinline__ void turn_pairs(const RotaryArgs& a, int token, const PairFreq* table, WarpSmem<kMode>& w,
-                                           int lane) {
+__device__ __forceinline__ void turn_pairs(const RotaryArgs& a, int token, int n, const PairFreq* table,
+                                           WarpSmem<kMode>& w, int lane) {
     const int32_t* pos = a.pos + static_cast<int64_t>(token) * a.axes;
     __syncwarp();
-    for (int p = lane; p < a.pairs; p += 32) {
-        const PairFreq f = table[p];
-        w.cs[p] = pair_turn(__ldg(pos + f.axis), f);
-    }
+    for (int i = 0; i < n; ++i, pos += a.axes)
+        for (int p = lane; p < a.pairs; p += 32) {
+            const PairFreq f = table[p];
+            w.cs[i * a.pairs + p] = pair_turn(__ldg(pos + f.axis), f);
+        }
     __syncwarp();
 }
 
@@ -296,19 +312,20 @@ __device__ __forceinline__ void turn_pairs(const RotaryArgs& a, int token, const
 template <int kMode>
 struct Turns {
     float c[kE], s[kE];
-    __device__ __forceinline__ Turns(const RotaryArgs& a, const LaneSetup<kMode>& L, const WarpSmem<kMode>& w,
+    // `cs`: the pairs of the lane's token.
+    __device__ __forceinline__ Turns(const RotaryArgs& a, const LaneSetup<kMode>& L, const float2* cs,
                                      float direction) {
 #pragma unroll
         for (int i = 0; i < kE; ++i) {
             float2 v = make_float2(1.0f, 0.0f);
             if constexpr (kMode == kAnywhere) {
                 const uint32_t e = L.code[i / 2] >> (16 * (i & 1));
-                if (e & 0x8000u) v = w.cs[(e >> 8) & 0x7fu];
+                if (e & 0x8000u) v = cs[(e >> 8) & 0x7fu];
                 // the first element of a pair lies before its partner
                 const bool low = static_cast<int>(e & 0xffu) > L.lane * kE + i;
                 s[i] = low ? -direction * v.y : direction * v.y;
             } else {
-                if (L.pair0 + i < a.pairs) v = w.cs[L.pair0 + i];
+                if (L.pair0 + i < a.pairs) v = cs[L.pair0 + i];
                 s[i] = direction * v.y;
             }
             c[i] = v.x;
@@ -351,252 +368,326 @@ struct Turns {
     }
 };
 
-// The weight of the lane's elements (ones where there is none).
+// The weight of the lane's elements (ones where there is none), as it was
+// loaded: half the registers of its fp32 form for 16-bit types.
 template <typename T, int kMode>
 struct Weights {
     static constexpr int kC = LaneSetup<kMode>::kC;
     Pack<T> w[kC];
-    bool given;
     __device__ __forceinline__ Weights(const void* p, const LaneSetup<kMode>& L) {
-        given = p != nullptr;
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
-            w[c].clear();
-            if (given && L.on[c]) w[c].load(static_cast<const T*>(p) + L.e0[c], true);
-        }
-    }
-    __device__ __forceinline__ void apply(uint64_t (&x)[kC][kE / 2], const uint64_t (&y)[kC][kE / 2]) const {
 #pragma unroll
-        for (int c = 0; c < kC; ++c) {
-            uint64_t f[kE / 2];
-            w[c].widen(f);
-#pragma unroll
-            for (int i = 0; i < kE / 2; ++i) x[c][i] = given ? mul2(y[c][i], f[i]) : y[c][i];
+            for (int i = 0; i < kE; ++i) w[c].e[i] = from_f<T>(1.0f);
+            if (p && L.on[c]) w[c].load(static_cast<const T*>(p) + L.e0[c], true);
         }
     }
 };
 
-// The rows of q (t 0) or k (t 1) in rows [r0, r1) of a token.
-__device__ __forceinline__ void part_rows(const RotaryArgs& a, int t, int r0, int r1, int& h0, int& h1) {
-    h0 = t ? max(r0 - a.hq, 0) : r0;
-    h1 = t ? r1 - a.hq : min(r1, a.hq);
-}
+// One direction's work on one row per lane group. `At` is where a row lies in
+// each tensor; `fetch` loads it into buffers, `work` takes it out of them (and
+// then starts their next loads, `next`) and writes the result. Buffers start
+// as zeros, so that the chunks that a lane lacks add nothing to its row's sums.
+template <typename T, int kMode>
+struct Forward {
+    static constexpr int kC = LaneSetup<kMode>::kC;
+    static constexpr int kAhead = sizeof(T) == 4 ? 2 : (kMode == kAnywhere ? 4 : 3);
+    static constexpr float kDirection = 1.0f;
+    struct Buffers {
+        Pack<T> x[kC];
+        __device__ Buffers() {
+#pragma unroll
+            for (int c = 0; c < kC; ++c) x[c].clear();
+        }
+    };
+    struct At {
+        const T* in;
+        T* out;
+    };
+    const LaneSetup<kMode>& L;
+    uint64_t wt[kC][kE / 2];
+    const RotaryTensor x, y;
+    float inv_d, eps;
+    int lanes, norm;
+    bool vec;
+    __device__ __forceinline__ Forward(const RotaryArgs& a, int t, const LaneSetup<kMode>& L)
+        : L(L), x(a.x[t]), y(a.y[t]) {
+        const Weights<T, kMode> w(a.w[t], L);
+#pragma unroll
+        for (int c = 0; c < kC; ++c) w.w[c].widen(wt[c]);
+        inv_d = 1.0f / static_cast<float>(a.D);
+        eps = a.eps;
+        lanes = a.lanes;
+        norm = a.norm;
+        vec = kMode != kAnywhere || a.vec != 0;
+    }
+    __device__ __forceinline__ At at(int64_t token, int64_t head) const {
+        return {static_cast<const T*>(x.p) + token * x.st + head * x.sh + L.e0[0],
+                static_cast<T*>(y.p) + token * y.st + head * y.sh + L.e0[0]};
+    }
+    __device__ __forceinline__ void advance_in(At& p, int heads) const { p.in += heads * x.sh; }
+    __device__ __forceinline__ void advance_out(At& p, int heads) const { p.out += heads * y.sh; }
+    __device__ __forceinline__ void fetch(Buffers& b, const At& p, bool live) const {
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+            if (live && L.on[c]) b.x[c].load(p.in + (L.e0[c] - L.e0[0]), vec);
+    }
+    template <typename F>
+    __device__ __forceinline__ void work(Buffers& b, const At& at, bool live, const Turns<kMode>& turns, float* row,
+                                         F next) {
+        uint64_t v[kC][kE / 2];
+#pragma unroll
+        for (int c = 0; c < kC; ++c) b.x[c].widen(v[c]);
+        next();
+        float r = 1.0f;
+        if (norm) {
+            uint64_t q = 0;
+#pragma unroll
+            for (int c = 0; c < kC; ++c)
+#pragma unroll
+                for (int i = 0; i < kE / 2; ++i) {
+                    q = fma2(v[c][i], v[c][i], q);
+                    v[c][i] = mul2(v[c][i], wt[c][i]);
+                }
+            r = rsqrtf(fmaf(row_sum(sum2(q), lanes), inv_d, eps));
+        }
+        turns.turn(v, L, row);
+        const uint64_t r2 = pack2(r, r);
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+            if (live && L.on[c]) {
+                // the norm's factor, common to the row, comes last
+#pragma unroll
+                for (int i = 0; i < kE / 2; ++i) v[c][i] = mul2(v[c][i], r2);
+                Pack<T> o;
+                o.round(v[c]);
+                o.store(at.out + (L.e0[c] - L.e0[0]), vec);
+            }
+    }
+};
 
 template <typename T, int kMode>
-__global__ void __launch_bounds__(kThreads, 2) rotary_forward_kernel(const __grid_constant__ RotaryArgs a) {
-    constexpr int kC = LaneSetup<kMode>::kC;
-    __shared__ WarpSmem<kMode> smem[kWarps];
-    __shared__ PairFreq table[kMaxD / 2];
-    WarpSmem<kMode>& w = smem[threadIdx.x >> 5];
-    const LaneSetup<kMode> L(a);
-    const bool vec = kMode != kAnywhere || a.vec != 0;
-    const float inv_d = 1.0f / static_cast<float>(a.D);
-    fill_freqs(a, table);
+struct Backward {
+    static constexpr int kC = LaneSetup<kMode>::kC;
+    static constexpr int kAhead = sizeof(T) == 4 ? 1 : 2;
+    static constexpr float kDirection = -1.0f;
+    struct Buffers {
+        Pack<T> g[kC], x[kC];
+        __device__ Buffers() {
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+                g[c].clear();
+                x[c].clear();
+            }
+        }
+    };
+    struct At {
+        const T *g, *x;
+        T* out;
+    };
+    const LaneSetup<kMode>& L;
+    const Weights<T, kMode> wt;
+    const RotaryTensor gy, x, gx;
+    float inv_d, eps;
+    int lanes, norm;
+    bool vec;
+    uint64_t gw[kC][kE / 2];  // the weight's gradient, this lane's rows so far
+    __device__ __forceinline__ Backward(const RotaryArgs& a, int t, const LaneSetup<kMode>& L)
+        : L(L), wt(a.w[t], L), gy(a.y[t]), x(a.x[t]), gx(a.g[t]) {
+        inv_d = 1.0f / static_cast<float>(a.D);
+        eps = a.eps;
+        lanes = a.lanes;
+        norm = a.norm;
+        vec = kMode != kAnywhere || a.vec != 0;
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+#pragma unroll
+            for (int i = 0; i < kE / 2; ++i) gw[c][i] = 0;
+    }
+    __device__ __forceinline__ At at(int64_t token, int64_t head) const {
+        return {static_cast<const T*>(gy.p) + token * gy.st + head * gy.sh + L.e0[0],
+                static_cast<const T*>(x.p) + token * x.st + head * x.sh + L.e0[0],
+                static_cast<T*>(gx.p) + token * gx.st + head * gx.sh + L.e0[0]};
+    }
+    __device__ __forceinline__ void advance_in(At& p, int heads) const {
+        p.g += heads * gy.sh;
+        p.x += heads * x.sh;
+    }
+    __device__ __forceinline__ void advance_out(At& p, int heads) const { p.out += heads * gx.sh; }
+    __device__ __forceinline__ void fetch(Buffers& b, const At& p, bool live) const {
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+            if (live && L.on[c]) {
+                b.g[c].load(p.g + (L.e0[c] - L.e0[0]), vec);
+                if (norm) b.x[c].load(p.x + (L.e0[c] - L.e0[0]), vec);
+            }
+    }
+    template <typename F>
+    __device__ __forceinline__ void work(Buffers& b, const At& at, bool live, const Turns<kMode>& turns, float* row,
+                                         F next) {
+        uint64_t g[kC][kE / 2], v[kC][kE / 2], o[kC][kE / 2];
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            b.g[c].widen(o[c]);
+            if (norm) b.x[c].widen(v[c]);
+        }
+        next();
+        turns.turn(o, L, row);
+        if (norm) {
+            // o = the gradient rotated back; v the head
+            uint64_t q = 0, d = 0;
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+                wt.w[c].widen(g[c]);
+#pragma unroll
+                for (int i = 0; i < kE / 2; ++i) {
+                    q = fma2(v[c][i], v[c][i], q);
+                    g[c][i] = mul2(o[c][i], g[c][i]);
+                    d = fma2(g[c][i], v[c][i], d);
+                }
+            }
+            const float ss = row_sum(sum2(q), lanes), dot = row_sum(sum2(d), lanes);
+            const float r = rsqrtf(fmaf(ss, inv_d, eps));
+            const float mean = dot * r * inv_d;  // mean(g w n)
+            const uint64_t r2 = pack2(r, r), m2 = pack2(-mean, -mean);
+#pragma unroll
+            for (int c = 0; c < kC; ++c)
+#pragma unroll
+                for (int i = 0; i < kE / 2; ++i) {
+                    const uint64_t n = mul2(v[c][i], r2);
+                    if (live) gw[c][i] = fma2(o[c][i], n, gw[c][i]);
+                    o[c][i] = mul2(r2, fma2(n, m2, g[c][i]));
+                }
+        }
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+            if (live && L.on[c]) {
+                Pack<T> y;
+                y.round(o[c]);
+                y.store(at.out + (L.e0[c] - L.e0[0]), vec);
+            }
+    }
+};
 
-    const int64_t units = static_cast<int64_t>(a.tokens) * a.parts;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps;
-    // rows of a token per unit, whole warps' worth
-    const int share = ((a.rows + a.parts * L.rows_per_warp - 1) / (a.parts * L.rows_per_warp)) * L.rows_per_warp;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); u < units; u += stride) {
-        const int token = static_cast<int>(u / a.parts), part = static_cast<int>(u % a.parts);
-        const int r0 = part * share, r1 = min(r0 + share, a.rows);
-        if (r0 >= r1) continue;
-        bool turned = false;
-#pragma unroll 1
-        for (int t = 0; t < 2; ++t) {
-            int h0, h1;
-            part_rows(a, t, r0, r1, h0, h1);
+// All rows of q (t 0) or k (t 1), by warp `warp` of `warps`. Heads enough for
+// the warp's lane groups: a warp takes a token's heads (or a `parts`-th of
+// them), so many passes ahead in flight. Fewer: the lane groups take several
+// tokens' heads at once, the next blocks of tokens in flight.
+template <int kMode, typename Op>
+__device__ __forceinline__ void all_rows(const RotaryArgs& a, int heads, const LaneSetup<kMode>& L, Op& op,
+                                         const PairFreq* table, WarpSmem<kMode>& w, int64_t warp, int64_t warps) {
+    constexpr int kAhead = Op::kAhead;
+    typename Op::Buffers buf[kAhead];
+    int which = 0;
+    const int rpw = L.rows_per_warp;
+    if (heads * 2 > rpw) {
+        const int64_t units = static_cast<int64_t>(a.tokens) * a.parts;
+        const int share = ((heads + a.parts * rpw - 1) / (a.parts * rpw)) * rpw;  // whole warps' worth
+        for (int64_t u = warp; u < units; u += warps) {
+            const int token = static_cast<int>(u / a.parts), part = static_cast<int>(u % a.parts);
+            const int h0 = part * share, h1 = min(h0 + share, heads);
             if (h0 >= h1) continue;
-            const T* in = static_cast<const T*>(a.x[t].p) + static_cast<int64_t>(token) * a.x[t].st;
-            T* out = static_cast<T*>(a.y[t].p) + static_cast<int64_t>(token) * a.y[t].st;
-            const int64_t in_h = a.x[t].sh, out_h = a.y[t].sh;
-            // the next rows' loads are in flight while a row is worked on
-            constexpr int kAhead = sizeof(T) == 4 ? 2 : (kMode == kAnywhere ? 4 : 3);
-            Pack<T> own[kAhead][kC];
-            auto fetch = [&](int k, int h) {
+            typename Op::At ahead = op.at(token, h0 + L.row_in_warp), here = ahead;
 #pragma unroll
-                for (int c = 0; c < kC; ++c)
-                    if (L.on[c] && h < h1) own[k][c].load(in + h * in_h + L.e0[c], vec);
-            };
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) fetch(k, h0 + k * L.rows_per_warp + L.row_in_warp);
-            const Weights<T, kMode> wt(a.w[t], L);
-            if (!turned) turn_pairs(a, token, table, w, L.lane);
-            turned = true;
-            const Turns<kMode> turns(a, L, w, 1.0f);
-            int which = 0;
-            for (int hb = h0; hb < h1; hb += kAhead * L.rows_per_warp) {
+            for (int k = 0; k < kAhead; ++k) {
+                op.fetch(buf[k], ahead, h0 + k * rpw + L.row_in_warp < h1);
+                op.advance_in(ahead, rpw);
+            }
+            turn_pairs(a, token, 1, table, w, L.lane);
+            const Turns<kMode> turns(a, L, w.cs, Op::kDirection);
+            for (int hb = h0; hb < h1; hb += kAhead * rpw) {
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k) {
-                    const int first = hb + k * L.rows_per_warp;
+                    const int first = hb + k * rpw;
                     if (first >= h1) break;
                     const int h = first + L.row_in_warp;
-                    uint64_t x[kC][kE / 2];
-#pragma unroll
-                    for (int c = 0; c < kC; ++c) {
-                        if (!L.on[c] || h >= h1) own[k][c].clear();
-                        own[k][c].widen(x[c]);
-                    }
-                    fetch(k, h + kAhead * L.rows_per_warp);
-                    float r = 1.0f;
-                    if (a.norm) {
-                        uint64_t q = 0;
-#pragma unroll
-                        for (int c = 0; c < kC; ++c)
-#pragma unroll
-                            for (int i = 0; i < kE / 2; ++i) q = fma2(x[c][i], x[c][i], q);
-                        r = rsqrtf(fmaf(row_sum(sum2(q), a.lanes), inv_d, a.eps));
-                        wt.apply(x, x);
-                    }
-                    turns.turn(x, L, w.row[which]);
+                    op.work(buf[k], here, h < h1, turns, w.row[which], [&] {
+                        op.fetch(buf[k], ahead, h + kAhead * rpw < h1);
+                        op.advance_in(ahead, rpw);
+                    });
+                    op.advance_out(here, rpw);
                     which ^= 1;
-                    const uint64_t r2 = pack2(r, r);
-#pragma unroll
-                    for (int c = 0; c < kC; ++c)
-                        if (L.on[c] && h < h1) {
-                            // the norm's factor, common to the row, comes last
-#pragma unroll
-                            for (int i = 0; i < kE / 2; ++i) x[c][i] = mul2(x[c][i], r2);
-                            Pack<T> o;
-                            o.round(x[c]);
-                            o.store(out + h * out_h + L.e0[c], vec);
-                        }
                 }
+            }
+        }
+    } else if (heads > 0) {
+        const int n = rpw / heads;  // tokens at once
+        const int mine = L.row_in_warp / heads, h = L.row_in_warp - mine * heads;
+        const int64_t blocks = (static_cast<int64_t>(a.tokens) + n - 1) / n;
+        // this lane's token of block b, and whether there is one
+        auto token_of = [&](int64_t b) { return static_cast<int>(b * n) + mine; };
+        auto there = [&](int64_t b) { return b < blocks && mine < n && b * n + mine < a.tokens; };
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) op.fetch(buf[k], op.at(token_of(warp + k * warps), h), there(warp + k * warps));
+        for (int64_t b0 = warp; b0 < blocks; b0 += kAhead * warps) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int64_t b = b0 + k * warps, bn = b + kAhead * warps;
+                if (b >= blocks) break;
+                const int first = static_cast<int>(b * n);
+                turn_pairs(a, first, min(n, a.tokens - first), table, w, L.lane);
+                const Turns<kMode> turns(a, L, w.cs + (mine < n ? mine : 0) * a.pairs, Op::kDirection);
+                op.work(buf[k], op.at(token_of(b), h), there(b), turns, w.row[which],
+                        [&] { op.fetch(buf[k], op.at(token_of(bn), h), there(bn)); });
+                which ^= 1;
             }
         }
     }
 }
 
-// First all heads of q, then all of k, so that one weight's sums and values
-// are live at a time: 12 warps to an SM with 168 registers, two rows of each in
-// flight (8 warps of 4 groups, or 16 with half the elements a lane, spill or
-// issue more instructions than the bytes leave time for).
+// Grid: (blocks, 2): q and k by blocks of their own.
+template <typename T, int kMode>
+__global__ void __launch_bounds__(kThreads, 2) rotary_forward_kernel(const __grid_constant__ RotaryArgs a) {
+    __shared__ WarpSmem<kMode> smem[kWarps];
+    __shared__ PairFreq table[kMaxD / 2];
+    const LaneSetup<kMode> L(a);
+    fill_freqs(a, table);
+    const int t = blockIdx.y;
+    Forward<T, kMode> op(a, t, L);
+    all_rows<kMode>(a, t ? a.rows - a.hq : a.hq, L, op, table, smem[threadIdx.x >> 5],
+                    static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5),
+                    static_cast<int64_t>(gridDim.x) * kWarps);
+}
+
+// 12 warps to an SM with 168 registers each, two rows of gradients and heads
+// in flight: with 16 warps the registers spill.
 template <typename T, int kMode>
 __global__ void __launch_bounds__(kBwdThreads, 3) rotary_backward_kernel(const __grid_constant__ RotaryArgs a) {
     constexpr int kC = LaneSetup<kMode>::kC;
     __shared__ WarpSmem<kMode> smem[kBwdWarps];
     __shared__ PairFreq table[kMaxD / 2];
     __shared__ float sums[kBwdWarps][kMaxD];
-    WarpSmem<kMode>& w = smem[threadIdx.x >> 5];
     const LaneSetup<kMode> L(a);
-    const bool vec = kMode != kAnywhere || a.vec != 0;
-    const float inv_d = 1.0f / static_cast<float>(a.D);
     fill_freqs(a, table);
-
-    const int64_t units = static_cast<int64_t>(a.tokens) * a.parts;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * kBwdWarps;
-#pragma unroll 1
-    for (int t = 0; t < 2; ++t) {
-        const int heads = t ? a.rows - a.hq : a.hq;
-        const int share = ((heads + a.parts * L.rows_per_warp - 1) / (a.parts * L.rows_per_warp)) * L.rows_per_warp;
-        const int64_t g_h = a.y[t].sh, x_h = a.x[t].sh, out_h = a.g[t].sh;
-        uint64_t gw[kC][kE / 2];
-        const Weights<T, kMode> wt(a.w[t], L);
+    const int t = blockIdx.y;
+    Backward<T, kMode> op(a, t, L);
+    all_rows<kMode>(a, t ? a.rows - a.hq : a.hq, L, op, table, smem[threadIdx.x >> 5],
+                    static_cast<int64_t>(blockIdx.x) * kBwdWarps + (threadIdx.x >> 5),
+                    static_cast<int64_t>(gridDim.x) * kBwdWarps);
+    if (!a.part) return;
+    // the block's partial sums, warps and row groups added in order
+    for (int g = 0; g < L.rows_per_warp; ++g) {
+        if (L.row_in_warp == g) {
 #pragma unroll
-        for (int c = 0; c < kC; ++c)
+            for (int c = 0; c < kC; ++c)
+                if (L.on[c]) {
 #pragma unroll
-            for (int i = 0; i < kE / 2; ++i) gw[c][i] = 0;
-        for (int64_t u = static_cast<int64_t>(blockIdx.x) * kBwdWarps + (threadIdx.x >> 5); u < units; u += stride) {
-            const int token = static_cast<int>(u / a.parts), part = static_cast<int>(u % a.parts);
-            const int h0 = part * share, h1 = min(h0 + share, heads);
-            if (h0 >= h1) continue;
-            const T* gin = static_cast<const T*>(a.y[t].p) + static_cast<int64_t>(token) * a.y[t].st;
-            const T* xin = static_cast<const T*>(a.x[t].p) + static_cast<int64_t>(token) * a.x[t].st;
-            T* out = static_cast<T*>(a.g[t].p) + static_cast<int64_t>(token) * a.g[t].st;
-            constexpr int kAhead = sizeof(T) == 4 ? 1 : 2;
-            Pack<T> own[kAhead][kC], val[kAhead][kC];
-            auto fetch = [&](int k, int h) {
-#pragma unroll
-                for (int c = 0; c < kC; ++c)
-                    if (L.on[c] && h < h1) {
-                        own[k][c].load(gin + h * g_h + L.e0[c], vec);
-                        if (a.norm) val[k][c].load(xin + h * x_h + L.e0[c], vec);
+                    for (int i = 0; i < kE / 2; ++i) {
+                        float lo, hi;
+                        unpack2(op.gw[c][i], lo, hi);
+                        float* at = &sums[threadIdx.x >> 5][L.e0[c] + 2 * i];
+                        at[0] = g ? at[0] + lo : lo;
+                        at[1] = g ? at[1] + hi : hi;
                     }
-            };
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) fetch(k, h0 + k * L.rows_per_warp + L.row_in_warp);
-            turn_pairs(a, token, table, w, L.lane);
-            const Turns<kMode> turns(a, L, w, -1.0f);
-            int which = 0;
-            for (int hb = h0; hb < h1; hb += kAhead * L.rows_per_warp) {
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) {
-                    const int first = hb + k * L.rows_per_warp;
-                    if (first >= h1) break;
-                    const int h = first + L.row_in_warp;
-                    uint64_t g[kC][kE / 2], x[kC][kE / 2], o[kC][kE / 2];
-#pragma unroll
-                    for (int c = 0; c < kC; ++c) {
-                        if (!L.on[c] || h >= h1) {
-                            own[k][c].clear();
-                            val[k][c].clear();
-                        }
-                        own[k][c].widen(o[c]);
-                        if (a.norm) val[k][c].widen(x[c]);
-                    }
-                    fetch(k, h + kAhead * L.rows_per_warp);
-                    turns.turn(o, L, w.row[which]);
-                    which ^= 1;
-                    if (a.norm) {
-                        // o = the gradient rotated back; x the head
-                        uint64_t q = 0, d = 0;
-                        wt.apply(g, o);
-#pragma unroll
-                        for (int c = 0; c < kC; ++c)
-#pragma unroll
-                            for (int i = 0; i < kE / 2; ++i) {
-                                q = fma2(x[c][i], x[c][i], q);
-                                d = fma2(g[c][i], x[c][i], d);
-                            }
-                        const float ss = row_sum(sum2(q), a.lanes), dot = row_sum(sum2(d), a.lanes);
-                        const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
-                        const float mean = dot * r * inv_d;  // mean(g w n)
-                        const uint64_t r2 = pack2(r, r), m2 = pack2(-mean, -mean);
-#pragma unroll
-                        for (int c = 0; c < kC; ++c)
-#pragma unroll
-                            for (int i = 0; i < kE / 2; ++i) {
-                                const uint64_t n = mul2(x[c][i], r2);
-                                gw[c][i] = fma2(o[c][i], n, gw[c][i]);
-                                o[c][i] = mul2(r2, fma2(n, m2, g[c][i]));
-                            }
-                    }
-#pragma unroll
-                    for (int c = 0; c < kC; ++c)
-                        if (L.on[c] && h < h1) {
-                            Pack<T> y;
-                            y.round(o[c]);
-                            y.store(out + h * out_h + L.e0[c], vec);
-                        }
                 }
-            }
         }
-        if (!a.part) continue;
-        // the block's partial sums, warps and row groups added in order
-        for (int g = 0; g < L.rows_per_warp; ++g) {
-            if (L.row_in_warp == g) {
-#pragma unroll
-                for (int c = 0; c < kC; ++c)
-                    if (L.on[c]) {
-#pragma unroll
-                        for (int i = 0; i < kE / 2; ++i) {
-                            float lo, hi;
-                            unpack2(gw[c][i], lo, hi);
-                            float* at = &sums[threadIdx.x >> 5][L.e0[c] + 2 * i];
-                            at[0] = g ? at[0] + lo : lo;
-                            at[1] = g ? at[1] + hi : hi;
-                        }
-                    }
-            }
-            __syncwarp();
-        }
-        __syncthreads();
-        for (int e = threadIdx.x; e < a.D; e += kBwdThreads) {
-            float sum = 0.0f;
-            for (int v = 0; v < kBwdWarps; ++v) sum += sums[v][e];
-            a.part[(static_cast<int64_t>(blockIdx.x) * 2 + t) * a.D + e] = sum;
-        }
-        __syncthreads();
+        __syncwarp();
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.D; e += kBwdThreads) {
+        float sum = 0.0f;
+        for (int v = 0; v < kBwdWarps; ++v) sum += sums[v][e];
+        a.part[(static_cast<int64_t>(blockIdx.x) * 2 + t) * a.D + e] = sum;
     }
 }
 
@@ -645,7 +736,7 @@ int64_t blocks_for(const RotaryArgs& a, int warps) {
 
 template <typename T>
 cudaError_t forward_t(const RotaryArgs& a, RotaryMode mode, int64_t grid, cudaStream_t st) {
-    const unsigned g = static_cast<unsigned>(grid);
+    const dim3 g(static_cast<unsigned>(grid), a.rows > a.hq ? 2u : 1u);
     if (mode == kBeside)
         rotary_forward_kernel<T, kBeside><<<g, kThreads, 0, st>>>(a);
     else if (mode == kChunks)
@@ -657,7 +748,7 @@ cudaError_t forward_t(const RotaryArgs& a, RotaryMode mode, int64_t grid, cudaSt
 
 template <typename T>
 cudaError_t backward_t(const RotaryArgs& a, RotaryMode mode, int64_t grid, void* gqw, void* gkw, cudaStream_t st) {
-    const unsigned g = static_cast<unsigned>(grid);
+    const dim3 g(static_cast<unsigned>(grid), a.rows > a.hq ? 2u : 1u);
     if (mode == kBeside)
         rotary_backward_kernel<T, kBeside><<<g, kBwdThreads, 0, st>>>(a);
     else if (mode == kChunks)
@@ -685,7 +776,7 @@ cudaError_t backward_t(const RotaryArgs& a, RotaryMode mode, int64_t grid, void*
 cudaError_t launch_rotary_forward(int dtype, RotaryArgs a, int sms, cudaStream_t st) {
     const RotaryMode mode = plan_lanes(&a, sms);
     int64_t grid = blocks_for(a, kWarps);
-    if (grid > static_cast<int64_t>(sms) * 16) grid = static_cast<int64_t>(sms) * 16;
+    if (grid > static_cast<int64_t>(sms) * 2) grid = static_cast<int64_t>(sms) * 2;  // one wave
     if (dtype == kF32) return forward_t<float>(a, mode, grid, st);
     if (dtype == kF16) return forward_t<__half>(a, mode, grid, st);
     return forward_t<__nv_bfloat16>(a, mode, grid, st);

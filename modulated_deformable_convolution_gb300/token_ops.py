@@ -33,6 +33,11 @@ _attention_attrs = struct.Struct("=if").pack
 _attention_dims = struct.Struct("=22q").pack
 
 
+def _new(t):
+    """A new contiguous tensor like t (None: none)."""
+    return None if t is None else torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _dtype_of(t):
     try:
         return _DTYPES[t.dtype]
@@ -180,9 +185,9 @@ def rotary(q, k, positions, inv_freq, sections, layout="half", norm=False, q_wei
     axes]: axis a turns sections[a] pairs of elements, with the float32
     frequencies inv_freq. Returns (q_out, k_out), which may be q and k."""
     if q_out is None:
-        q_out = q.new_empty(q.shape)
+        q_out = _new(q)
     if k_out is None and k is not None:
-        k_out = k.new_empty(k.shape)
+        k_out = _new(k)
     mdcn_rotary_forward(q, k, positions, inv_freq, sections, q_out, k_out, layout, norm, q_weight, k_weight, eps)
     return q_out, k_out
 
@@ -234,10 +239,7 @@ def rotary_backward(grad_q_out, grad_k_out, q, k, positions, inv_freq, sections,
     """Gradients of sum(grad_q_out * q_out) + sum(grad_k_out * k_out) for
     (q_out, k_out) = rotary(q, k, ...). Returns a dict with q, k, q_weight and
     k_weight (None for what was not given)."""
-    g = {"q": grad_q_out.new_empty(grad_q_out.shape),
-         "k": None if grad_k_out is None else grad_k_out.new_empty(grad_k_out.shape),
-         "q_weight": None if q_weight is None else q_weight.new_empty(q_weight.shape),
-         "k_weight": None if k_weight is None else k_weight.new_empty(k_weight.shape)}
+    g = {"q": _new(grad_q_out), "k": _new(grad_k_out), "q_weight": _new(q_weight), "k_weight": _new(k_weight)}
     if q_weight is not None or k_weight is not None:
         need = mdcn_rotary_backward_workspace_size(grad_q_out, grad_k_out, positions, inv_freq, sections, layout, norm,
                                                    eps)
@@ -328,14 +330,14 @@ def attention(q, k, v, q_starts, k_starts, k_lengths=None, causal=False, scale=N
     p = _Attention(q, k, v, q_starts, k_starts, k_lengths, causal, scale)
     shape = p.q_shape
     if out is None:
-        out = q.new_empty(shape)
+        out = _new(q)
     if lse is None:
-        lse = q.new_empty((shape[1], shape[0]), dtype=torch.float32)
+        lse = torch.empty((shape[1], shape[0]), dtype=torch.float32, device=q.device)
     o = p.like_q("out", out)
     dims = p.dims(o)
     need = _size("mdcn_attention_workspace_size", p.attrs, dims, p.code)
     if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = q.new_empty(need, dtype=torch.uint8)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     _forward(p, dims, o, lse, workspace, None)
     return out, lse
 
@@ -372,10 +374,10 @@ def attention_backward(grad_out, q, k, v, out, lse, q_starts, k_starts, k_length
     """Gradients of sum(grad_out * out) for (out, lse) = attention(q, k, v,
     ...), as a dict with q, k and v."""
     p = _Attention(q, k, v, q_starts, k_starts, k_lengths, causal, scale)
-    g = {"q": q.new_empty(p.q_shape), "k": k.new_empty(p.k_shape), "v": v.new_empty(p.k_shape)}
+    g = {"q": _new(q), "k": _new(k), "v": _new(v)}
     dims, inputs, outputs = _backward_dims(p, grad_out, out, g["q"], g["k"], g["v"])
     need = _size("mdcn_attention_backward_workspace_size", p.attrs, dims, p.code)
     if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = q.new_empty(need, dtype=torch.uint8)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     _backward(p, dims, inputs, lse, outputs, workspace, None)
     return g

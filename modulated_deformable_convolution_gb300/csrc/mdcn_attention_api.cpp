@@ -134,29 +134,47 @@ mdcn_status attn_check(const mdcn_attention_attrs* at, const mdcn_attention_dims
 }
 
 // The forward's plan: row tiles, and between how many blocks a tile's keys are
-// shared out. More than one only where the tiles leave most of the GPU's SMs
-// idle; then as many as fill it twice, each with at least two key tiles of
-// the average sequence.
+// shared out. Estimated in steps (one key tile of a row tile): an item of n
+// steps costs n + kItemSteps. Sequences that fill their rows: as many waves of
+// items as the SMs need, each as long as an item. Sequences of any length up to
+// their rows (k_lengths): half the steps on average, taken as they come, and
+// one item's length at the end. The join of the shares costs a launch and the
+// partial results' way to memory and back.
 struct AttnPlan {
     int64_t tiles, splits;
     size_t off_out, off_lse, bytes;
 };
 
-AttnPlan attn_plan(const mdcn_attention_dims& d, mdcn_dtype dtype) {
-    constexpr int64_t kSms = 152;
+AttnPlan attn_plan(const mdcn_attention_attrs& at, const mdcn_attention_dims& d, mdcn_dtype dtype, bool lengths) {
+    constexpr int64_t kSms = 152, kMaxSplits = 32;
+    constexpr double kItemSteps = 2.0, kJoinSteps = 4.0, kStepBytes = 4.0e6;
     AttnPlan p{};
     const int64_t group = d.q_heads / d.k_heads;
     const bool tc = dtype != MDCN_F32;
     const int64_t tokens = tc ? 2 * (mdcn::kAttnTcBlockRows / group) : mdcn::kAttnSimtRows / group;
     const int64_t keys = tc ? 128 : 64;
     p.tiles = mdcn::attn_tiles(d.q_tokens, d.batch, tokens);
-    const int64_t blocks = p.tiles * d.k_heads;
     p.splits = 1;
-    if (blocks > 0 && blocks * 2 <= kSms) {
-        const int64_t key_tiles = (d.k_tokens / d.batch + keys - 1) / keys;
-        p.splits = 2 * kSms / blocks;
-        if (p.splits > key_tiles / 2) p.splits = key_tiles / 2;
-        if (p.splits < 1) p.splits = 1;
+    const int64_t blocks = p.tiles * d.k_heads;
+    if (blocks > 0) {
+        const double mean = static_cast<double>(d.k_tokens) / static_cast<double>(d.batch);
+        const double own = at.causal ? static_cast<double>(d.q_tokens) / static_cast<double>(d.batch) / 2 : 0.0;
+        const double seen = mean > own ? mean - own : mean / 2;
+        const int64_t steps = static_cast<int64_t>(seen / static_cast<double>(keys)) + 1;
+        const double rows = static_cast<double>(d.q_tokens) * static_cast<double>(d.q_heads) *
+                            static_cast<double>(d.head_dim) * 8.0;
+        double best = 0.0;
+        for (int64_t s = 1; s <= kMaxSplits && s <= steps; ++s) {
+            const double item = static_cast<double>((steps + s - 1) / s);
+            double cost = lengths ? (static_cast<double>(blocks) * (static_cast<double>(steps) / 2 + kItemSteps * s)) /
+                                            static_cast<double>(kSms) + item
+                                  : static_cast<double>((blocks * s + kSms - 1) / kSms) * (item + kItemSteps);
+            if (s > 1) cost += kJoinSteps + rows * static_cast<double>(s) / kStepBytes;
+            if (s == 1 || cost < best) {
+                best = cost;
+                p.splits = s;
+            }
+        }
     }
     size_t off = mdcn::kAttnHeaderBytes;
     if (p.splits > 1) {
@@ -319,7 +337,9 @@ mdcn_status mdcn_attention_workspace_size(const mdcn_attention_attrs* attrs, con
     if (!bytes) return MDCN_ERR_NULL;
     const mdcn_status s = attn_check(attrs, dims, dtype, false);
     if (s != MDCN_OK) return s;
-    *bytes = attn_plan(*dims, dtype).bytes;
+    // whether the call has k_lengths is not known here: room for either plan
+    const size_t with = attn_plan(*attrs, *dims, dtype, true).bytes, without = attn_plan(*attrs, *dims, dtype, false).bytes;
+    *bytes = with > without ? with : without;
     return MDCN_OK;
 }
 
@@ -335,8 +355,8 @@ mdcn_status mdcn_attention_forward(const mdcn_attention_attrs* attrs, const mdcn
     const void* al[] = {q, k, v, q_starts, k_starts, k_lengths_or_null, out, lse, workspace};
     for (const void* p : al)
         if (!aligned16(p)) return MDCN_ERR_ALIGN;
-    const AttnPlan p = attn_plan(*dims, dtype);
-    if (p.tiles * p.splits > kI31) return MDCN_ERR_UNSUPPORTED;
+    const AttnPlan p = attn_plan(*attrs, *dims, dtype, k_lengths_or_null != nullptr);
+    if (p.tiles > kI31 / p.splits / dims->k_heads) return MDCN_ERR_UNSUPPORTED;
     if (workspace_bytes < p.bytes) return MDCN_ERR_WORKSPACE;
     s = mdcn::api_check_device(nullptr);
     if (s != MDCN_OK) return s;

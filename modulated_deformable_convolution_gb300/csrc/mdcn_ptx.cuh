@@ -398,6 +398,37 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         : "memory");
 }
 
+// ---------------------------------------------------------------- work stealing
+// Asks for the index of a block of this launch that has not started, which
+// then never starts: 16 bytes at dst, signalled on the mbarrier (one thread;
+// the barrier expects 16 bytes). Not to be asked again once it was refused.
+__device__ __forceinline__ void steal_block(uint32_t dst, uint32_t bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+        "r"(bar)
+        : "memory");
+}
+
+// The answer at src: the block's x index, or -1 when none was left.
+__device__ __forceinline__ int32_t stolen_block(uint32_t src) {
+    uint32_t got, x;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t.reg .b32 y, z, u;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, u}, r;\n\t}"
+        : "=r"(got), "=r"(x)
+        : "r"(src)
+        : "memory");
+    return got ? static_cast<int32_t>(x) : -1;
+}
+
+__device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
 // 32 lanes x 32 bits, 16 consecutive columns: thread t of the warp gets TMEM
 // lane (taddr.lane + t), columns taddr.col .. +15.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {

@@ -1,27 +1,30 @@
 // Attention over packed sequences on the tensor cores (float16, bfloat16):
 // the forward.
 //
-// A CTA takes two row tiles of 128 rows (row = token and query head of one key
-// head) and runs over the key tiles of 128 keys that they see:
+// A work item is two row tiles of 128 rows (row = token and query head of one
+// key head) over the key tiles of 128 keys that they see:
 //   S = Q K^T (fp32, tensor memory), P = exp2(scale' S - m) rounded to the
 //   type of v, written over S in tensor memory, O += P V (fp32, tensor memory).
 // Warps 0-3 and 4-7 hold one row per thread of the first and second tile (a
 // tensor-memory lane each, so row maxima and sums need no exchange), warp 8
-// loads tiles by TMA into a ring, warp 9 issues the MMAs: the products of one
-// tile run while the other tile's probabilities are computed. O is rescaled
-// only when a row's maximum has grown by more than 2^8 since it was last
-// taken (P then stays below 2^8, exact in the sums: the result does not
-// depend on which maximum is used beyond rounding); by the row's own warp,
-// which knows the previous O += P V finished because the S it waits for was
-// issued after it.
+// loads tiles by TMA into a ring, warp 9 issues the MMAs, warp 10 gets items.
+// The steps of the two row tiles alternate, and the products of one run while
+// the other's probabilities are computed. Heads of at most 64 elements leave
+// room for three S in tensor memory, so that a row tile's next S is ready when
+// its probabilities are done; with two, S follows the step's O += P V.
+// O is rescaled only when a row's maximum has grown by more than 2^8 since it
+// was last taken (P then stays below 2^8, exact in the sums: the result does
+// not depend on which maximum is used beyond rounding), by the row's own warp.
 //
 // Bound by the tensor cores for long rows: per key tile and row tile two
-// 128 x 128 x D products, 4 * 128 * 128 * D operations; next by the exponentials.
+// 128 x 128 x D products, 4 * 128 * 128 * D operations; at D = 64 by a row
+// tile's chain of score, probabilities, sum.
 // Shared memory: Q once, K and V in a ring of 128-row tiles, 227 KB in all.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "mdcn_attention_tc.cuh"
 #include "mdcn_plan.h"
@@ -31,16 +34,35 @@ namespace mdcn {
 namespace {
 
 constexpr int kTcThreads = 384;
-constexpr int kWarpLoad = 8, kWarpIssue = 9, kWarpServe = 10;
+constexpr int kWarpLoad = 8, kWarpIssue = 9, kWarpServe = 10, kWarpClear = 11;
 constexpr int kRegsRow = 216, kRegsCtl = 72;  // of 168 a thread at launch
 static_assert(2 * kRegsRow + kRegsCtl <= 3 * 168, "register split must fit the launch's");
 constexpr int kKeys = 128;
 constexpr float kRescaleLog2 = 8.0f;
+using Zero = std::integral_constant<int, 0>;
+using One = std::integral_constant<int, 1>;
 
 // Stages of the ring: as many 128-row tiles as fit beside Q.
 __host__ __device__ constexpr int stages_of(int atoms) { return atoms == 2 ? 5 : 8; }
 __host__ __device__ constexpr int smem_of(int atoms) {
-    return 1024 + (2 + stages_of(atoms)) * atoms * static_cast<int>(kAtomBytes) + 512;
+    return 1024 + (2 + stages_of(atoms)) * atoms * static_cast<int>(kAtomBytes) + 768;
+}
+
+// S buffers in tensor memory, which the steps of both row tiles use in turn.
+__host__ __device__ constexpr int scores_of(int atoms) { return atoms == 2 ? 2 : 3; }
+
+// Which S buffer row tile t's key tile j goes to, in an item with n0 and n1 key
+// tiles: with three, the next in turn (j by j, tile 0 first; `before`: S of
+// earlier items); with two, one for each row tile, or both in turn where only
+// one row tile has keys.
+template <int kAtoms>
+__device__ __forceinline__ uint32_t score_buffer(int t, int32_t j, int32_t n0, int32_t n1, uint32_t before) {
+    if constexpr (scores_of(kAtoms) == 3) {
+        const int32_t i = t ? min(j + 1, n0) + j : j + min(j, n1);
+        return (before + static_cast<uint32_t>(i)) % 3u;
+    } else {
+        return n0 == 0 || n1 == 0 ? static_cast<uint32_t>(j & 1) : static_cast<uint32_t>(t);
+    }
 }
 
 // kAtoms: 64-element atoms of a head (head_dim <= 64: 1, else 2).
@@ -50,6 +72,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                            const __grid_constant__ CUtensorMap mv, const __grid_constant__ AttnArgs a) {
     constexpr uint32_t S = stages_of(kAtoms);
     constexpr uint32_t kTile = kAtoms * kAtomBytes;
+    constexpr uint32_t NB = scores_of(kAtoms);
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -59,14 +82,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     auto full = [&](uint32_t s) { return bars + 8u * s; };
     auto empty = [&](uint32_t s) { return bars + 8u * (S + s); };
     const uint32_t rest = bars + 16u * S;
-    auto s_full = [&](int t) { return rest + 8u * t; };
-    auto p_full = [&](int t) { return rest + 16u + 8u * t; };
-    auto o_full = [&](int t) { return rest + 32u + 8u * t; };
-    auto o_read = [&](int t) { return rest + 48u + 8u * t; };
-    auto q_full = [&](int t) { return rest + 64u + 8u * t; };
-    auto q_empty = [&](int t) { return rest + 80u + 8u * t; };
-    const uint32_t drain = rest + 96u;
-    const uint32_t slot_off = rest + 104u - raw;
+    // A row tile's i-th S signals barrier i % NB of that tile, its i-th P likewise: a barrier's next
+    // use waits for what follows step i, so none gets two phases ahead of who waits for it, however
+    // far either side lags (up to NB steps of a tile are under way)
+    const uint32_t s_full0 = rest, p_full0 = rest + 48u, o_done0 = rest + 96u;
+    auto s_full = [&](int t, uint32_t i) { return s_full0 + 24u * t + 8u * (i % NB); };
+    auto p_full = [&](int t, uint32_t i) { return p_full0 + 24u * t + 8u * (i % NB); };
+    auto o_done = [&](int t, uint32_t i) { return o_done0 + 24u * t + 8u * (i % NB); };  // O += P V of a step
+    auto o_read = [&](int t) { return rest + 144u + 8u * t; };                           // an item's O
+    auto q_full = [&](int t) { return rest + 160u + 8u * t; };
+    auto q_empty = [&](int t) { return rest + 176u + 8u * t; };
+    const uint32_t drain = rest + 192u, cleared = rest + 200u, to_clear = rest + 208u;
+    const uint32_t slot_off = rest + 216u - raw;
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem_raw + slot_off);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem_raw + slot_off + 4);
 
@@ -78,15 +105,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(empty(i), 1);
         }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(s_full(t), 1);
-            mbar_init(p_full(t), 4);
-            mbar_init(o_full(t), 1);
+            for (uint32_t i = 0; i < NB; ++i) {
+                mbar_init(s_full(t, i), 1);
+                mbar_init(p_full(t, i), 4);
+                mbar_init(o_done(t, i), 1);
+            }
             mbar_init(o_read(t), 4);
             mbar_init(q_full(t), 1);
             mbar_init(q_empty(t), 1);
         }
         mbar_init(drain, 1);
-        queue.init(10);
+        queue.init(11);
+        mbar_init(cleared, 1);
+        mbar_init(to_clear, 1);
         *abort_flag = 0;
         fence_mbarrier_init();
         tma_prefetch_desc(&mq);
@@ -101,9 +132,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // tensor memory: S of tile 0 and 1 (128 columns each, P over the first 64), O of tile 0 and 1
-    auto s_col = [&](int t) { return tmem + 128u * t; };
-    auto o_col = [&](int t) { return tmem + 256u + 64u * kAtoms * t; };
+    // tensor memory: the S buffers (128 columns each, P over the first 64), O of row tile 0 and 1
+    auto s_col = [&](uint32_t b) { return tmem + 128u * b; };
+    auto o_col = [&](int t) { return tmem + 128u * NB + 64u * kAtoms * t; };
     const int tpt = kAttnTcRows / a.group;
 
     if (warp >= 8) {
@@ -176,75 +207,153 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
         } else if (warp == kWarpIssue) {
             // ------------------------------------------------------------ MMAs
-            const uint32_t fmt = kBf ? 1u : 0u;
-            const uint32_t nd = static_cast<uint32_t>((a.D + 15) & ~15);
-            const uint32_t id_s = make_idesc(fmt, 128u, kKeys), id_o = make_idesc(fmt, 128u, nd) | (1u << 16);
-            const int ksteps = (a.D + 15) / 16;
-            auto wait = [&](uint32_t bar, uint32_t parity) {
-                return warp_wait2(bar, 0u, parity, abort_flag, a.status, kSiteMmaFull);
-            };
-            uint32_t e = 0;                          // ring entries used up by earlier items
-            uint32_t items[2] = {0, 0}, ps[2] = {0, 0};  // items and probability tiles of each row tile so far
+            // One thread. The tensor pipe holds a few products; what this thread does between two
+            // groups of them has to be shorter than those take, so stages, phases, buffers and
+            // descriptors advance by additions, and no other lane is waited for.
+            if (elect_lane()) {
+                const uint32_t fmt = kBf ? 1u : 0u;
+                const uint32_t nd = static_cast<uint32_t>((a.D + 15) & ~15);
+                const uint32_t id_s = make_idesc(fmt, 128u, kKeys), id_o = make_idesc(fmt, 128u, nd) | (1u << 16);
+                const int ksteps = (a.D + 15) / 16;
+                const uint64_t dq0 = desc_sw128(q_s, 16u, 1024u), dk0 = desc_sw128(ring, 16u, 1024u);
+                const uint64_t dv0 = desc_sw128(ring, kAtomBytes, 1024u);
+                auto wait = [&](uint32_t bar, uint32_t parity) {
+                    return mbar_wait_bounded(bar, parity, abort_flag, a.status, kSiteMmaFull);
+                };
+                uint32_t ks = 0, kp = 0, vs = 1, vp = 0;     // stage and phase of the next K and V
+                auto next2 = [&](uint32_t& st, uint32_t& ph) {
+                    st += 2;
+                    if (st >= S) {
+                        st -= S;
+                        ph ^= 1u;
+                    }
+                };
+                uint32_t sb = 0, pb = 0;                     // buffer of the next S and of the next P
+                uint32_t si0 = 0, si1 = 0;                   // barrier of a row tile's next S
+                uint32_t pi0 = 0, pi1 = 0, pp0 = 0, pp1 = 0; // barrier and phase of its next P
+                uint32_t it0 = 0, it1 = 0, zeroed = 0;       // parities: items of a row tile, cleared tiles
+                for_items_one(queue, abort_flag, a.status, [&](const AttnItem& it) {
+                    const int32_t n0 = it.n0, n1 = it.n1, nmax = max(n0, n1);
+                    if (nmax == 0) return true;
+                    const bool solo = NB == 2 && (n0 == 0 || n1 == 0);
+                    if (NB == 2) sb = pb = 0;
+                    const bool partial = it.lk - (it.j0 + nmax - 1) * kKeys < kKeys;
+                    // S of row tile T from the K in stage ks
+                    auto scores = [&](auto T, bool last) {
+                        constexpr int t = decltype(T)::value;
+                        uint32_t& si = t ? si1 : si0;
+                        const uint32_t d = s_col(NB == 3 || solo ? sb : t);
+                        const uint64_t dq = dq0 + t * (kTile >> 4), dk = dk0 + ks * (kTile >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < 4 * kAtoms; ++kk) {
+                            const uint32_t off = (static_cast<uint32_t>(kk >> 2) * kAtomBytes + 32u * (kk & 3)) >> 4;
+                            if (kk < ksteps) mma_f16(d, dq + off, dk + off, id_s, kk > 0);
+                        }
+                        mma_commit(s_full0 + 24u * t + 8u * si);
+                        if (last) mma_commit(q_empty(t));
+                        si = si + 1 == NB ? 0 : si + 1;
+                        sb = sb + 1 == NB ? 0 : sb + 1;
+                    };
+                    bool have = false;      // the K in stage ks has been waited for
+                    bool clearing = false;  // V's rows past the last key are being cleared
+                    auto key = [&] {
+                        if (!have && !wait(full(ks), kp)) return false;
+                        have = true;
+                        tc_fence_after();
+                        return true;
+                    };
+                    auto begin = [&](auto T) {
+                        constexpr int t = decltype(T)::value;
+                        const int32_t n = t ? n1 : n0;
+                        if (n == 0) return true;
+                        if (!key() || !wait(q_full(t), t ? it1 : it0)) return false;
+                        tc_fence_after();
+                        scores(T, n == 1);
+                        return true;
+                    };
+                    // step j of row tile T: O += P V, and the next S
+                    auto step = [&](auto T, int32_t j) {
+                        constexpr int t = decltype(T)::value;
+                        const int32_t n = t ? n1 : n0;
+                        if (j >= n) return true;
+                        const bool more = j + 1 < n;
+                        // a free S buffer: the next S goes ahead of this step's sum
+                        if (more && (NB == 3 || solo)) {
+                            if (!key()) return false;
+                            scores(T, j + 2 == n);
+                        }
+                        uint32_t& pi = t ? pi1 : pi0;
+                        uint32_t& pp = t ? pp1 : pp0;
+                        const uint32_t p = s_col(NB == 3 || solo ? pb : t);
+                        const uint64_t dv = dv0 + vs * (kTile >> 4);
+                        if (j == 0 && !wait(o_read(t), (t ? it1 : it0) ^ 1u)) return false;
+                        if (clearing) {
+                            if (!wait(cleared, zeroed)) return false;
+                            zeroed ^= 1u;
+                            clearing = false;
+                        }
+                        if (!wait(p_full0 + 24u * t + 8u * pi, pp)) return false;
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < kKeys / 16; ++kk)
+                            mma_f16_ts(o_col(t), p + 8u * kk, dv + 128u * kk, id_o, j > 0 || kk > 0);
+                        mma_commit(o_done0 + 24u * t + 8u * pi);
+                        if (++pi == NB) {
+                            pi = 0;
+                            pp ^= 1u;
+                        }
+                        pb = pb + 1 == NB ? 0 : pb + 1;
+                        if (more && NB == 2 && !solo) {
+                            if (!key()) return false;
+                            scores(T, j + 2 == n);
+                        }
+                        return true;
+                    };
+                    if (!begin(Zero{}) || !begin(One{})) return false;
+                    mma_commit(empty(ks));
+                    next2(ks, kp);
+                    for (int32_t j = 0; j < nmax; ++j) {
+                        have = false;
+                        if (!wait(full(vs), vp)) return false;
+                        if (partial && j + 1 == nmax) {
+                            mbar_arrive(to_clear);
+                            clearing = true;
+                        }
+                        if (!step(Zero{}, j) || !step(One{}, j)) return false;
+                        mma_commit(empty(vs));
+                        next2(vs, vp);
+                        if (j + 1 < nmax) {
+                            mma_commit(empty(ks));
+                            next2(ks, kp);
+                        }
+                    }
+                    it0 ^= n0 > 0 ? 1u : 0u;
+                    it1 ^= n1 > 0 ? 1u : 0u;
+                    return true;
+                });
+                // every MMA issued has completed before tensor memory is released
+                mma_commit(drain);
+                volatile int never = 0;
+                mbar_wait_bounded(drain, 0, &never, a.status, kSiteDrain, 200000000ull);
+            }
+            __syncwarp();
+        } else if (warp == kWarpClear) {
+            // ------------------------------------------------------------ values past the last key
+            uint32_t e = 0, turn = 0;  // ring entries of earlier items; tiles cleared
             for_items(queue, abort_flag, a.status, [&](const AttnItem& it) {
                 const int32_t nmax = max(it.n0, it.n1);
                 if (nmax == 0) return true;
-                const int32_t n[2] = {it.n0, it.n1};
-                // S of row tile t and key tile j
-                auto scores = [&](int t, uint32_t k_s, int32_t j) {
-                    for (int kk = 0; kk < ksteps; ++kk) {
-                        const uint32_t off = static_cast<uint32_t>(kk >> 2) * kAtomBytes + 32u * (kk & 3);
-                        mma_f16_elect(s_col(t), desc_sw128(q_s + t * kTile + off, 16u, 1024u),
-                                      desc_sw128(k_s + off, 16u, 1024u), id_s, kk > 0);
-                    }
-                    mma_commit_elect(s_full(t));
-                    if (j + 1 == n[t]) mma_commit_elect(q_empty(t));
-                };
-                if (!wait(full(e % S), (e / S) & 1u)) return false;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (n[t] == 0) continue;
-                    if (!wait(q_full(t), items[t] & 1u)) return false;
-                    tc_fence_after();
-                    scores(t, ring + (e % S) * kTile, 0);
-                }
-                mma_commit_elect(empty(e % S));
-                for (int32_t j = 0; j < nmax; ++j) {
-                    const uint32_t ev = e + 2 * j + 1, ek = ev + 1;  // V_j, K_{j+1}
-                    const uint32_t sv = ev % S, sk = ek % S;
-                    const uint32_t v_s = ring + sv * kTile;
-                    if (!wait(full(sv), (ev / S) & 1u)) return false;
-                    const int32_t valid = it.lk - (it.j0 + j) * kKeys;
-                    if (valid < kKeys) zero_rows(v_s, kAtoms, kAtomBytes, valid, kKeys);
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (j >= n[t]) continue;
-                        if (j == 0 && !wait(o_read(t), (items[t] & 1u) ^ 1u)) return false;
-                        if (!wait(p_full(t), ps[t] & 1u)) return false;
-                        ++ps[t];
-                        tc_fence_after();
-                        for (int kk = 0; kk < kKeys / 16; ++kk)
-                            mma_f16_ts_elect(o_col(t), s_col(t) + 8u * kk,
-                                             desc_sw128(v_s + 2048u * kk, kAtomBytes, 1024u), id_o, j > 0 || kk > 0);
-                        if (j + 1 < n[t]) {
-                            if (!wait(full(sk), (ek / S) & 1u)) return false;
-                            tc_fence_after();
-                            scores(t, ring + sk * kTile, j + 1);
-                        } else {
-                            mma_commit_elect(o_full(t));
-                        }
-                    }
-                    mma_commit_elect(empty(sv));
-                    if (j + 1 < nmax) mma_commit_elect(empty(sk));
-                }
-                e += 2 * nmax;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) items[t] += n[t] > 0 ? 1u : 0u;
+                const int32_t valid = it.lk - (it.j0 + nmax - 1) * kKeys;
+                const uint32_t st = (e + 2u * nmax - 1u) % S;
+                e += 2u * nmax;
+                if (valid >= kKeys) return true;
+                // the issuing thread has seen the tile arrive
+                if (!warp_wait2(to_clear, 0u, turn, abort_flag, a.status, kSiteTmaEmpty)) return false;
+                turn ^= 1u;
+                zero_rows(ring + st * kTile, kAtoms, kAtomBytes, valid, kKeys);
+                if (lane == 0) mbar_arrive(cleared);
                 return true;
             });
-            // every MMA issued has completed before tensor memory is released
-            mma_commit_elect(drain);
-            volatile int never = 0;
-            warp_wait2(drain, 0u, 0, &never, a.status, kSiteDrain, 200000000ull);
         }
     } else {
         setmaxnreg_inc<kRegsRow>();
@@ -255,8 +364,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int tk = r / a.group, sub = r - tk * a.group;
         const float sc = fmaxf(fabsf(a.scale), 1e-30f) * kLog2e;
         const bool neg = a.scale < 0.0f;
-        const uint32_t scol = s_col(t) + lanes, ocol = o_col(t) + lanes;
-        uint32_t ss = 0, items = 0;  // score tiles and items of this row tile so far
+        const uint32_t ocol = o_col(t) + lanes;
+        uint32_t g = 0, done = 0;  // steps of earlier items; steps of this row tile so far
         for_items(queue, abort_flag, a.status, [&](const AttnItem& it) {
             const int32_t tokt = it.first + t * tpt;
             const int rows = max(0, min(tpt, it.lq - tokt)) * a.group;
@@ -269,9 +378,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             float m = -INFINITY, l = 0.0f;
             const int nt = t ? it.n1 : it.n0;
             for (int32_t j = 0; j < nt; ++j) {
-                if (!warp_wait2(s_full(t), 0u, ss & 1u, abort_flag, a.status, kSiteGatherEmpty)) return false;
-                ++ss;
+                if (!warp_wait2(s_full(t, done), 0u, (done / NB) & 1u, abort_flag, a.status, kSiteGatherEmpty))
+                    return false;
                 tc_fence_after();
+                const uint32_t scol = s_col(score_buffer<kAtoms>(t, j, it.n0, it.n1, g)) + lanes;
                 uint32_t x[4][32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32_async(scol + 32u * c, x[c]);
@@ -285,12 +395,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         for (int i = 0; i < 32; ++i) x[c][i] ^= 0x80000000u;
                 }
                 if (seen_all < (j + 1) * kKeys) {
-                    const int32_t left = seen - j * kKeys;  // of this tile's keys
+                    const int32_t left = seen - j * kKeys, left_all = seen_all - j * kKeys;  // of this tile's keys
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 4; ++c) {
+                        if (left_all >= 32 * (c + 1)) continue;
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (32 * c + i >= left) x[c][i] = 0xff800000u;  // -infinity
+                    }
                 }
                 float best[4];
 #pragma unroll
@@ -308,6 +420,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (grow) m = top;
                     l *= corr;
                     if (j > 0) {
+                        // the sum before this step has been added
+                        if (!warp_wait2(o_done(t, done - 1u), 0u, ((done - 1u) / NB) & 1u, abort_flag, a.status,
+                                        kSiteGatherEmpty))
+                            return false;
+                        tc_fence_after();
                         const uint64_t c2 = pack2(corr, corr);
 #pragma unroll 1
                         for (int c = 0; c < 2 * kAtoms; ++c) {
@@ -347,7 +464,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_full(t));
+                if (lane == 0) mbar_arrive(p_full(t, done));
+                ++done;
                 float u, w;
                 unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), u, w);
                 l += u + w;
@@ -357,8 +475,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int h = it.kh * a.group + sub;
             const bool any = nt > 0;
             if (any) {
-                if (!warp_wait2(o_full(t), 0u, items & 1u, abort_flag, a.status, kSiteEpilogue)) return false;
-                ++items;
+                if (!warp_wait2(o_done(t, done - 1u), 0u, ((done - 1u) / NB) & 1u, abort_flag, a.status, kSiteEpilogue))
+                    return false;
                 tc_fence_after();
             }
             const bool some = any && l != 0.0f;  // the row saw a key
@@ -398,6 +516,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(o_read(t));
             }
+            g += static_cast<uint32_t>(it.n0 + it.n1);
             return true;
         });
     }

@@ -137,6 +137,24 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, int32_t a, int32_t b
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+__device__ __forceinline__ AttnItem read_item(uint32_t slot) {
+    const uint4 a = ld_shared_v4(slot), b = ld_shared_v4(slot + 16u), c = ld_shared_v4(slot + 32u);
+    AttnItem it;
+    it.go = static_cast<int32_t>(a.x);
+    it.kh = static_cast<int32_t>(a.y);
+    it.split = static_cast<int32_t>(a.z);
+    it.q0 = static_cast<int32_t>(a.w);
+    it.k0 = static_cast<int32_t>(b.x);
+    it.lq = static_cast<int32_t>(b.y);
+    it.lk = static_cast<int32_t>(b.z);
+    it.room = static_cast<int32_t>(b.w);
+    it.first = static_cast<int32_t>(c.x);
+    it.n0 = static_cast<int32_t>(c.y);
+    it.n1 = static_cast<int32_t>(c.z);
+    it.j0 = static_cast<int32_t>(c.w);
+    return it;
+}
+
 // A warp's turn through the items: each item to `body` (which returns false to
 // stop). The reader frees the slot as soon as it has copied the item.
 template <typename F>
@@ -144,22 +162,21 @@ __device__ __forceinline__ void for_items(const ItemQueue& q, volatile int* abor
     for (uint32_t i = 0;; ++i) {
         const uint32_t s = i & 1u;
         if (!warp_wait2(q.full(s), 0u, (i >> 1) & 1u, abort_flag, status, kSiteEpilogue)) return;
-        AttnItem it;
-        const uint4 a = ld_shared_v4(q.slot(s)), b = ld_shared_v4(q.slot(s) + 16u), c = ld_shared_v4(q.slot(s) + 32u);
-        it.go = static_cast<int32_t>(a.x);
-        it.kh = static_cast<int32_t>(a.y);
-        it.split = static_cast<int32_t>(a.z);
-        it.q0 = static_cast<int32_t>(a.w);
-        it.k0 = static_cast<int32_t>(b.x);
-        it.lq = static_cast<int32_t>(b.y);
-        it.lk = static_cast<int32_t>(b.z);
-        it.room = static_cast<int32_t>(b.w);
-        it.first = static_cast<int32_t>(c.x);
-        it.n0 = static_cast<int32_t>(c.y);
-        it.n1 = static_cast<int32_t>(c.z);
-        it.j0 = static_cast<int32_t>(c.w);
+        const AttnItem it = read_item(q.slot(s));
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(q.empty(s));
+        if (!it.go || !body(it)) return;
+    }
+}
+
+// The same for a role that one thread plays.
+template <typename F>
+__device__ __forceinline__ void for_items_one(const ItemQueue& q, volatile int* abort_flag, uint32_t* status, F body) {
+    for (uint32_t i = 0;; ++i) {
+        const uint32_t s = i & 1u;
+        if (!mbar_wait_bounded(q.full(s), (i >> 1) & 1u, abort_flag, status, kSiteEpilogue)) return;
+        const AttnItem it = read_item(q.slot(s));
+        mbar_arrive(q.empty(s));
         if (!it.go || !body(it)) return;
     }
 }

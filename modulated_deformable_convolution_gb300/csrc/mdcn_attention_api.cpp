@@ -410,7 +410,8 @@ mdcn_status mdcn_attention_backward(const mdcn_attention_attrs* attrs, const mdc
         if (!aligned16(p)) return MDCN_ERR_ALIGN;
     const int64_t tiles = mdcn::attn_tiles(dims->q_tokens, dims->batch,
                                            mdcn::kAttnSimtRows / (dims->q_heads / dims->k_heads));
-    if (tiles > kI31) return MDCN_ERR_UNSUPPORTED;
+    if (tiles > kI31 / dims->k_heads || mdcn::attn_tiles(dims->k_tokens, dims->batch, 64) > kI31 / dims->k_heads)
+        return MDCN_ERR_UNSUPPORTED;
     if (workspace_bytes < attn_bwd_bytes(*dims)) return MDCN_ERR_WORKSPACE;
     s = mdcn::api_check_device(nullptr);
     if (s != MDCN_OK) return s;

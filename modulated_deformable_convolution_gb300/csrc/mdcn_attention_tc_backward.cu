@@ -32,7 +32,7 @@ namespace mdcn {
 namespace {
 
 constexpr int kTcThreads = 384;
-constexpr int kWarpLoad = 8, kWarpIssue = 9, kWarpStats = 10;
+constexpr int kWarpLoad = 8, kWarpIssue = 9, kWarpServe = 10, kWarpAid = 11;
 constexpr int kRegsRow = 216, kRegsCtl = 72;  // of 168 a thread at launch
 static_assert(2 * kRegsRow + kRegsCtl <= 3 * 168, "register split must fit the launch's");
 constexpr int kKeys = 128;
@@ -79,9 +79,19 @@ __device__ __forceinline__ void store_row(uint32_t col, uint8_t* p, int c0, int 
     }
 }
 
+// d (+)= rows of x times rows of y over the head, both K-major; one thread.
+template <int kAtoms>
+__device__ __forceinline__ void head_product(uint32_t d, uint64_t x, uint64_t y, uint32_t idesc, int ksteps) {
+#pragma unroll
+    for (int kk = 0; kk < 4 * kAtoms; ++kk) {
+        const uint32_t off = (static_cast<uint32_t>(kk >> 2) * kAtomBytes + 32u * (kk & 3)) >> 4;
+        if (kk < ksteps) mma_f16(d, x + off, y + off, idesc, kk > 0);
+    }
+}
+
 __host__ __device__ constexpr int stages_of(int atoms) { return atoms == 2 ? 5 : 8; }
 __host__ __device__ constexpr int smem_q(int atoms) {
-    return 1024 + (2 + stages_of(atoms)) * atoms * static_cast<int>(kAtomBytes) + 256;
+    return 1024 + (2 + stages_of(atoms)) * atoms * static_cast<int>(kAtomBytes) + 512;
 }
 
 // ---------------------------------------------------------------- grad_q
@@ -96,37 +106,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
-    const uint32_t q_s = base, g_s = base + kTile, ring = base + 2 * kTile, bars = ring + S * kTile;
+    const uint32_t q_s = base, g_s = base + kTile, ring = base + 2 * kTile;
+    const ItemQueue queue{ring + S * kTile};
+    const uint32_t bars = queue.base + ItemQueue::kBytes;
     auto full = [&](uint32_t s) { return bars + 8u * s; };
     auto empty = [&](uint32_t s) { return bars + 8u * (S + s); };
     const uint32_t rest = bars + 16u * S;
-    const uint32_t q_full = rest, drain = rest + 8, s_full = rest + 16, p_full = rest + 24, s_read = rest + 32,
-                   dp_read = rest + 40, ds_full = rest + 48, dq_done = rest + 56;
-    const uint32_t slot_off = rest + 64 - raw;
+    const uint32_t q_full = rest, q_empty = rest + 8, s_full = rest + 16, dp_full = rest + 24, s_read = rest + 32,
+                   dp_read = rest + 40, ds_full = rest + 48, dq_done = rest + 56, dq_read = rest + 64,
+                   drain = rest + 72, cleared = rest + 80, to_clear = rest + 88;
+    const uint32_t slot_off = rest + 96 - raw;
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem_raw + slot_off);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem_raw + slot_off + 4);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tpt = kAttnTcRows / a.group;
-    const AttnSeq s = attn_find(a, false, tpt, blockIdx.x);
-    if (s.tile < 0) return;
-    const int kh = blockIdx.y;
-    const int32_t tok0 = s.tile * tpt, ntok = min(tpt, s.lq - tok0);
-    const int32_t n = (attn_seen(a, s, tok0 + ntok - 1) + kKeys - 1) / kKeys;
-
     if (warp == kWarpLoad && lane == 0) {
         for (uint32_t i = 0; i < S; ++i) {
             mbar_init(full(i), 1);
             mbar_init(empty(i), 1);
         }
-        mbar_init(q_full, 1);
-        mbar_init(drain, 1);
-        mbar_init(s_full, 1);
-        mbar_init(p_full, 1);
-        mbar_init(s_read, 8);
-        mbar_init(dp_read, 8);
-        mbar_init(ds_full, 8);
-        mbar_init(dq_done, 1);
+        const uint32_t ones[] = {q_full, q_empty, s_full, dp_full, dq_done, drain, cleared, to_clear};
+        for (uint32_t b : ones) mbar_init(b, 1);
+        const uint32_t eights[] = {s_read, dp_read, ds_full, dq_read};
+        for (uint32_t b : eights) mbar_init(b, 8);
+        queue.init(11);
         *abort_flag = 0;
         fence_mbarrier_init();
         tma_prefetch_desc(&mq);
@@ -143,156 +146,223 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const uint32_t c_s = tmem, c_dp = tmem + 128u, c_ds = tmem + 256u, c_dq = tmem + 320u;
+    const int tpt = kAttnTcRows / a.group;
 
     if (warp >= 8) {
         setmaxnreg_dec<kRegsCtl>();
-        if (warp == kWarpLoad && n > 0) {
-            mbar_arrive_expect_tx_elect(q_full, 2u * kAtoms * static_cast<uint32_t>(tpt * a.group) * 128u);
-            for (int at = 0; at < kAtoms; ++at) {
-                tma_load_4d_elect(q_s + at * kAtomBytes, &mq, 64 * at, 0, kh, s.q0 + tok0, q_full);
-                tma_load_4d_elect(g_s + at * kAtomBytes, &mg, 64 * at, 0, kh, s.q0 + tok0, q_full);
-            }
-            bool ok = true;
-            uint32_t st = 0, ph = 0, issued = 0;
-            for (int32_t j = 0; j < n && ok; ++j) {
-                for (int kv = 0; kv < 2; ++kv) {
-                    if (!warp_wait_bounded(empty(st), ph ^ 1u, abort_flag, a.status, kSiteTmaEmpty)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_arrive_expect_tx_elect(full(st), kTile);
-                    for (int at = 0; at < kAtoms; ++at)
-                        tma_load_3d_elect(ring + st * kTile + at * kAtomBytes, kv ? &mv : &mk, 64 * at, kh,
-                                          s.k0 + j * kKeys, full(st));
-                    ++issued;
-                    if (++st == S) {
-                        st = 0;
-                        ph ^= 1u;
+        if (warp == kWarpServe) {
+            // ------------------------------------------------------------ items
+            serve_items(queue, abort_flag, a.status, [&](int32_t index, AttnItem& it) {
+                it.kh = index % a.hk;
+                const AttnSeq s = attn_find(a, false, tpt, index / a.hk);
+                if (s.tile < 0) return false;
+                it.q0 = s.q0;
+                it.k0 = s.k0;
+                it.lq = s.lq;
+                it.lk = s.lk;
+                it.first = s.tile * tpt;
+                it.n0 = (attn_seen(a, s, it.first + min(tpt, s.lq - it.first) - 1) + kKeys - 1) / kKeys;
+                return true;
+            });
+        } else if (warp == kWarpLoad) {
+            // ------------------------------------------------------------ loads
+            uint32_t issued = 0, rows = 0;
+            for_items(queue, abort_flag, a.status, [&](const AttnItem& it) {
+                if (it.n0 == 0) return true;
+                if (!warp_wait_bounded(q_empty, (rows & 1u) ^ 1u, abort_flag, a.status, kSiteTmaEmpty)) return false;
+                mbar_arrive_expect_tx_elect(q_full, 2u * kAtoms * static_cast<uint32_t>(tpt * a.group) * 128u);
+                for (int at = 0; at < kAtoms; ++at) {
+                    tma_load_4d_elect(q_s + at * kAtomBytes, &mq, 64 * at, 0, it.kh, it.q0 + it.first, q_full);
+                    tma_load_4d_elect(g_s + at * kAtomBytes, &mg, 64 * at, 0, it.kh, it.q0 + it.first, q_full);
+                }
+                ++rows;
+                for (int32_t j = 0; j < it.n0; ++j) {
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const uint32_t st = issued % S;
+                        if (!warp_wait_bounded(empty(st), ((issued / S) & 1u) ^ 1u, abort_flag, a.status, kSiteTmaEmpty))
+                            return false;
+                        mbar_arrive_expect_tx_elect(full(st), kTile);
+                        for (int at = 0; at < kAtoms; ++at)
+                            tma_load_3d_elect(ring + st * kTile + at * kAtomBytes, kv ? &mv : &mk, 64 * at, it.kh,
+                                              it.k0 + j * kKeys, full(st));
+                        ++issued;
                     }
                 }
-            }
-            if (!ok) {  // the copies already issued land before the CTA exits
+                return true;
+            });
+            if (*abort_flag) {  // the copies already issued land before the CTA exits
                 volatile int never = 0;
-                warp_wait_bounded(q_full, 0, &never, a.status, kSiteDrain, 200000000ull);
-                const uint32_t first = issued > S ? issued - S : 0;
-                for (uint32_t i = first; i < issued; ++i)
+                if (rows) warp_wait_bounded(q_full, (rows - 1) & 1u, &never, a.status, kSiteDrain, 200000000ull);
+                for (uint32_t i = issued > S ? issued - S : 0; i < issued; ++i)
                     warp_wait_bounded(full(i % S), (i / S) & 1, &never, a.status, kSiteDrain, 200000000ull);
             }
-        } else if (warp == kWarpIssue && n > 0) {
-            const uint32_t fmt = kBf ? 1u : 0u;
-            const uint32_t nd = static_cast<uint32_t>((a.D + 15) & ~15);
-            const uint32_t id_s = make_idesc(fmt, 128u, kKeys), id_q = make_idesc(fmt, 128u, nd) | (1u << 16);
-            const int ksteps = (a.D + 15) / 16;
-            auto wait = [&](uint32_t bar, uint32_t parity) {
-                return warp_wait2(bar, 0u, parity, abort_flag, a.status, kSiteMmaFull);
-            };
-            auto product = [&](uint32_t d, uint32_t x, uint32_t y) {
-                for (int kk = 0; kk < ksteps; ++kk) {
-                    const uint32_t off = static_cast<uint32_t>(kk >> 2) * kAtomBytes + 32u * (kk & 3);
-                    mma_f16_elect(d, desc_sw128(x + off, 16u, 1024u), desc_sw128(y + off, 16u, 1024u), id_s, kk > 0);
-                }
-            };
-            // S and dP of key tile j, into the buffers whose previous values have been read
-            auto scores = [&](int32_t j) {
-                const uint32_t e = 2u * j, sk = e % S, sv = (e + 1) % S;
-                if (!wait(full(sk), (e / S) & 1)) return false;
-                // dQ += dS K multiplies the rows past the last key by 0
-                const int32_t valid = s.lk - j * kKeys;
-                if (valid < kKeys) zero_rows(ring + sk * kTile, kAtoms, kAtomBytes, valid, kKeys);
-                if (j > 0 && !wait(s_read, (j - 1) & 1)) return false;
-                tc_fence_after();
-                product(c_s, q_s, ring + sk * kTile);
-                mma_commit_elect(s_full);
-                if (!wait(full(sv), ((e + 1) / S) & 1)) return false;
-                if (j > 0 && !wait(dp_read, (j - 1) & 1)) return false;
-                tc_fence_after();
-                product(c_dp, g_s, ring + sv * kTile);
-                mma_commit_elect(p_full);
-                mma_commit_elect(empty(sv));
+        } else if (warp == kWarpAid) {
+            // ------------------------------------------------------------ keys past the last one
+            uint32_t e = 0, turn = 0;
+            for_items(queue, abort_flag, a.status, [&](const AttnItem& it) {
+                if (it.n0 == 0) return true;
+                const int32_t valid = it.lk - (it.n0 - 1) * kKeys;
+                const uint32_t st = (e + 2u * it.n0 - 2u) % S;
+                e += 2u * it.n0;
+                if (valid >= kKeys) return true;
+                // the issuing thread has seen the tile arrive
+                if (!warp_wait2(to_clear, 0u, turn, abort_flag, a.status, kSiteTmaEmpty)) return false;
+                turn ^= 1u;
+                zero_rows(ring + st * kTile, kAtoms, kAtomBytes, valid, kKeys);
+                if (lane == 0) mbar_arrive(cleared);
                 return true;
-            };
-            bool ok = wait(q_full, 0) && scores(0);
-            for (int32_t j = 0; j < n && ok; ++j) {
-                if (j + 1 < n && !(ok = scores(j + 1))) break;
-                if (!(ok = wait(ds_full, j & 1))) break;
-                tc_fence_after();
-                const uint32_t sk = (2u * j) % S;
-                for (int kk = 0; kk < kKeys / 16; ++kk)
-                    mma_f16_ts_elect(c_dq, c_ds + 8u * kk, desc_sw128(ring + sk * kTile + 2048u * kk, kAtomBytes, 1024u),
-                                     id_q, j > 0 || kk > 0);
-                mma_commit_elect(empty(sk));
-                mma_commit_elect(dq_done);
+            });
+        } else {
+            // ------------------------------------------------------------ MMAs, one thread
+            if (elect_lane()) {
+                const uint32_t fmt = kBf ? 1u : 0u;
+                const uint32_t nd = static_cast<uint32_t>((a.D + 15) & ~15);
+                const uint32_t id_s = make_idesc(fmt, 128u, kKeys), id_q = make_idesc(fmt, 128u, nd) | (1u << 16);
+                const int ksteps = (a.D + 15) / 16;
+                const uint64_t dq0 = desc_sw128(q_s, 16u, 1024u), dg0 = desc_sw128(g_s, 16u, 1024u);
+                const uint64_t dk0 = desc_sw128(ring, 16u, 1024u), dm0 = desc_sw128(ring, kAtomBytes, 1024u);
+                auto wait = [&](uint32_t bar, uint32_t parity) {
+                    return mbar_wait_bounded(bar, parity, abort_flag, a.status, kSiteMmaFull);
+                };
+                uint32_t st = 0, ph = 0;        // stage and phase of the next tile to arrive
+                uint32_t ks = 0;                // stage of the next K to be summed
+                uint32_t read = 1, ds = 0;      // parities: S and dP read, dS written
+                uint32_t items = 0, clear = 0;  // parities
+                auto next = [&](uint32_t& s) {
+                    const bool wrap = ++s == S;
+                    if (wrap) s = 0;
+                    return wrap;
+                };
+                for_items_one(queue, abort_flag, a.status, [&](const AttnItem& it) {
+                    const int32_t n = it.n0;
+                    if (n == 0) return true;
+                    const bool partial = it.lk - (n - 1) * kKeys < kKeys;
+                    // S and dP of the next key tile, into the buffers whose previous values have been read
+                    auto scores = [&](bool last) {
+                        if (!wait(full(st), ph) || !wait(s_read, read)) return false;
+                        if (last && partial) mbar_arrive(to_clear);
+                        tc_fence_after();
+                        head_product<kAtoms>(c_s, dq0, dk0 + st * (kTile >> 4), id_s, ksteps);
+                        mma_commit(s_full);
+                        if (next(st)) ph ^= 1u;
+                        if (!wait(full(st), ph) || !wait(dp_read, read)) return false;
+                        tc_fence_after();
+                        head_product<kAtoms>(c_dp, dg0, dk0 + st * (kTile >> 4), id_s, ksteps);
+                        mma_commit(dp_full);
+                        mma_commit(empty(st));
+                        if (last) mma_commit(q_empty);
+                        if (next(st)) ph ^= 1u;
+                        read ^= 1u;
+                        return true;
+                    };
+                    if (!wait(q_full, items) || !scores(n == 1)) return false;
+                    for (int32_t j = 0; j < n; ++j) {
+                        if (j + 1 < n && !scores(j + 2 == n)) return false;
+                        if (j == 0 && !wait(dq_read, items ^ 1u)) return false;
+                        // dQ += dS K multiplies the rows past the last key by 0
+                        if (j + 1 == n && partial) {
+                            if (!wait(cleared, clear)) return false;
+                            clear ^= 1u;
+                        }
+                        const uint64_t dm = dm0 + ks * (kTile >> 4);
+                        if (!wait(ds_full, ds)) return false;
+                        ds ^= 1u;
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < kKeys / 16; ++kk)
+                            mma_f16_ts(c_dq, c_ds + 8u * kk, dm + 128u * kk, id_q, j > 0 || kk > 0);
+                        mma_commit(dq_done);
+                        mma_commit(empty(ks));
+                        next(ks);
+                        next(ks);
+                    }
+                    items ^= 1u;
+                    return true;
+                });
+                mma_commit(drain);
+                volatile int never = 0;
+                mbar_wait_bounded(drain, 0, &never, a.status, kSiteDrain, 200000000ull);
             }
-            mma_commit_elect(drain);
-            volatile int never = 0;
-            warp_wait2(drain, 0u, 0, &never, a.status, kSiteDrain, 200000000ull);
+            __syncwarp();
         }
     } else {
         setmaxnreg_inc<kRegsRow>();
         const int half = warp >> 2;  // columns [64 half, 64 half + 64) of each tile
         const int r = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const bool live = r < ntok * a.group;
-        const int tk = r / a.group, h = kh * a.group + (r - tk * a.group);
-        const int64_t tok = s.q0 + tok0 + tk;
-        const int32_t seen = live ? attn_seen(a, s, tok0 + tk) : 0;
-        const int32_t seen_all = __reduce_min_sync(0xffffffffu, live ? seen : 0x7fffffff);
+        const int tk = r / a.group, sub = r - tk * a.group;
         const float sc = a.scale * kLog2e;
-        const float lse = live ? a.lse[static_cast<int64_t>(h) * a.tq + tok] * kLog2e : 0.0f;
-        const float delta = live ? a.delta[static_cast<int64_t>(h) * a.tq + tok] * kUnshift : 0.0f;
-        const uint64_t sc2 = pack2(sc, sc), l2 = pack2(kShift - lse, kShift - lse), d2 = pack2(-delta, -delta);
-        bool ok = true;
-        for (int32_t j = 0; j < n; ++j) {
-            if (!(ok = warp_wait2(s_full, 0u, j & 1, abort_flag, a.status, kSiteGatherEmpty))) break;
-            tc_fence_after();
-            uint32_t x[2][32];
-            load_half(c_s + lanes + 64u * half, x);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(s_read);
-            const int32_t first = j * kKeys + 64 * half;
-            const bool masked = seen_all < first + 64;
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    float u, w;
-                    unpack2(fma2(pack2(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])), sc2, l2), u, w);
-                    x[c][i] = __float_as_uint(attn_exp2(u));
-                    x[c][i + 1] = __float_as_uint(attn_exp2(w));
-                }
-            if (!(ok = warp_wait2(p_full, 0u, j & 1, abort_flag, a.status, kSiteGatherEmpty))) break;
-            tc_fence_after();
-            uint32_t dp[2][32], ds[32];
-            load_half(c_dp + lanes + 64u * half, dp);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(dp_read);
-            if (masked) {
-                const int32_t left = seen - first;
+        const uint64_t sc2 = pack2(sc, sc);
+        uint32_t g = 0;  // steps so far
+        for_items(queue, abort_flag, a.status, [&](const AttnItem& it) {
+            const int32_t n = it.n0;
+            const bool live = r < min(tpt, it.lq - it.first) * a.group;
+            const int h = it.kh * a.group + sub;
+            const int64_t tok = it.q0 + it.first + tk;
+            int32_t seen = it.lk;
+            if (a.causal) seen = min(max(it.first + tk + 1 + it.lk - it.lq, 0), it.lk);
+            if (!live) seen = 0;
+            const int32_t seen_all = __reduce_min_sync(0xffffffffu, live ? seen : 0x7fffffff);
+            const float lse = live ? a.lse[static_cast<int64_t>(h) * a.tq + tok] * kLog2e : 0.0f;
+            const float delta = live ? a.delta[static_cast<int64_t>(h) * a.tq + tok] * kUnshift : 0.0f;
+            const uint64_t l2 = pack2(kShift - lse, kShift - lse), d2 = pack2(-delta, -delta);
+            for (int32_t j = 0; j < n; ++j, ++g) {
+                if (!warp_wait2(s_full, 0u, g & 1u, abort_flag, a.status, kSiteGatherEmpty)) return false;
+                tc_fence_after();
+                uint32_t x[2][32];
+                load_half(c_s + lanes + 64u * half, x);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(s_read);
+                const int32_t first = j * kKeys + 64 * half;
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (32 * c + i >= left) x[c][i] = dp[c][i] = 0u;
+                    for (int i = 0; i < 32; i += 2) {
+                        float u, w;
+                        unpack2(fma2(pack2(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])), sc2, l2), u, w);
+                        x[c][i] = __float_as_uint(attn_exp2(u));
+                        x[c][i + 1] = __float_as_uint(attn_exp2(w));
+                    }
+                if (!warp_wait2(dp_full, 0u, g & 1u, abort_flag, a.status, kSiteGatherEmpty)) return false;
+                tc_fence_after();
+                uint32_t dp[2][32], ds[32];
+                load_half(c_dp + lanes + 64u * half, dp);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(dp_read);
+                if (seen_all < first + 64) {
+                    const int32_t left = seen - first;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (32 * c + i >= left) x[c][i] = dp[c][i] = 0u;
+                }
+                score_grads<kBf>(x, dp, [&](int) { return d2; }, ds);
+                // the sum before this step has read dS
+                if (j > 0 && !warp_wait2(dq_done, 0u, (g - 1u) & 1u, abort_flag, a.status, kSiteGatherEmpty))
+                    return false;
+                tc_fence_after();
+                tmem_st32(c_ds + lanes + 32u * half, ds);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ds_full);
             }
-            score_grads<kBf>(x, dp, [&](int) { return d2; }, ds);
-            if (j > 0 && !(ok = warp_wait2(dq_done, 0u, (j - 1) & 1, abort_flag, a.status, kSiteGatherEmpty))) break;
-            tc_fence_after();
-            tmem_st32(c_ds + lanes + 32u * half, ds);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(ds_full);
-        }
-        const bool any = n > 0;
-        if (any && ok) ok = warp_wait2(dq_done, 0u, (n - 1) & 1, abort_flag, a.status, kSiteEpilogue);
-        if (ok && *abort_flag == 0) {
+            const bool any = n > 0;
+            if (any && !warp_wait2(dq_done, 0u, (g - 1u) & 1u, abort_flag, a.status, kSiteEpilogue)) return false;
             tc_fence_after();
             uint8_t* p = static_cast<uint8_t*>(a.gq.p) + 2 * (tok * a.gq.st + h * a.gq.sh);
             const int mid = min(32 * kAtoms, a.D);
             store_row<kBf>(c_dq + lanes, p, half ? mid : 0, half ? a.D : mid, a.scale, any, live);
-        }
+            if (any) {  // the next item's first sum may overwrite dQ
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(dq_read);
+            }
+            return true;
+        });
     }
     tc_fence_before();
     __syncthreads();
@@ -310,7 +380,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // what the other still reads.
 __host__ __device__ constexpr uint32_t kv_stages(int atoms) { return atoms == 2 ? 2 : 4; }
 __host__ __device__ constexpr int smem_kv(int atoms) {
-    return 1024 + static_cast<int>((2 + 2 * kv_stages(atoms)) * atoms * kAtomBytes + kv_stages(atoms) * 1024u) + 512;
+    return 1024 + static_cast<int>((2 + 2 * kv_stages(atoms)) * atoms * kAtomBytes + kv_stages(atoms) * 1024u) + 768;
 }
 
 template <int kAtoms, bool kBf>
@@ -325,7 +395,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t base = (raw + 1023u) & ~1023u;
     const uint32_t k_s = base, v_s = base + kTile, q_ring = base + 2 * kTile, g_ring = q_ring + S * kTile;
     const uint32_t stats = g_ring + S * kTile;  // per stage: 128 x (8 - lse'), 128 x (-delta 2^-8)
-    const uint32_t bars = stats + S * 1024u;
+    const ItemQueue queue{stats + S * 1024u};
+    const uint32_t bars = queue.base + ItemQueue::kBytes;
     auto bar = [&](uint32_t kind, uint32_t s) { return bars + 8u * (kind * S + s); };
     auto q_full = [&](uint32_t s) { return bar(0, s); };
     auto q_empty = [&](uint32_t s) { return bar(1, s); };
@@ -334,40 +405,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     auto t_full = [&](uint32_t s) { return bar(4, s); };
     auto t_empty = [&](uint32_t s) { return bar(5, s); };
     const uint32_t rest = bars + 48u * S;
-    const uint32_t kv_full = rest, drain = rest + 8, s_full = rest + 16, dp_full = rest + 24, p_ready = rest + 32,
-                   ds_ready = rest + 40, done = rest + 48;
-    const uint32_t slot_off = rest + 56 - raw;
+    const uint32_t kv_full = rest, kv_empty = rest + 8, s_full = rest + 16, dp_full = rest + 24, p_ready = rest + 32,
+                   ds_ready = rest + 40, done = rest + 48, acc_read = rest + 56, drain = rest + 64,
+                   cleared = rest + 72, to_clear = rest + 80;
+    const uint32_t slot_off = rest + 88 - raw;
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem_raw + slot_off);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem_raw + slot_off + 4);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int tpt = kAttnTcRows / a.group;
-    const AttnSeq s = attn_find(a, true, kKeys, blockIdx.x);
-    if (s.tile < 0) return;
-    const int kh = blockIdx.y;
-    const int32_t j0 = s.tile * kKeys;
-    // the blocks of query rows that see key j0 and later ones
-    const int32_t shift = s.lk - s.lq;
-    int32_t b0 = a.causal ? max(0, j0 - shift) / tpt : 0;
-    const int32_t b1 = j0 < s.lk ? (s.lq + tpt - 1) / tpt : 0;
-    const int32_t n = max(0, b1 - b0);
-
+    const int tpt = kAttnTcRows / a.group, most = tpt * a.group;  // rows of a full block
     if (warp == kWarpLoad && lane == 0) {
         for (uint32_t i = 0; i < S; ++i) {
-            mbar_init(q_full(i), 1);
-            mbar_init(q_empty(i), 1);
-            mbar_init(g_full(i), 1);
-            mbar_init(g_empty(i), 1);
-            mbar_init(t_full(i), 1);
+            for (uint32_t kind = 0; kind < 5; ++kind) mbar_init(bar(kind, i), 1);
             mbar_init(t_empty(i), 8);
         }
-        mbar_init(kv_full, 1);
-        mbar_init(drain, 1);
-        mbar_init(s_full, 1);
-        mbar_init(dp_full, 1);
-        mbar_init(p_ready, 8);
-        mbar_init(ds_ready, 8);
-        mbar_init(done, 1);
+        const uint32_t ones[] = {kv_full, kv_empty, s_full, dp_full, done, drain, cleared, to_clear};
+        for (uint32_t b : ones) mbar_init(b, 1);
+        const uint32_t eights[] = {p_ready, ds_ready, acc_read};
+        for (uint32_t b : eights) mbar_init(b, 8);
+        queue.init(11);
         *abort_flag = 0;
         fence_mbarrier_init();
         tma_prefetch_desc(&mq);
@@ -379,6 +435,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tmem_alloc(smem_u32(const_cast<uint32_t*>(tmem_slot)), 512);
         tmem_relinquish();
     }
+    if (warp == kWarpAid && most < kAttnTcRows) {
+        // rows that no copy ever writes (a group that does not divide the tile): zero for good, since
+        // the sums multiply them by 0
+        for (uint32_t i = 0; i < 2 * S; ++i) zero_rows(q_ring + i * kTile, kAtoms, kAtomBytes, most, kAttnTcRows);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -387,123 +448,178 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     if (warp >= 8) {
         setmaxnreg_dec<kRegsCtl>();
-        if (warp == kWarpLoad && n > 0) {
+        if (warp == kWarpServe) {
+            // ------------------------------------------------------------ items
+            serve_items(queue, abort_flag, a.status, [&](int32_t index, AttnItem& it) {
+                it.kh = index % a.hk;
+                const AttnSeq s = attn_find(a, true, kKeys, index / a.hk);
+                if (s.tile < 0) return false;
+                it.q0 = s.q0;
+                it.k0 = s.k0;
+                it.lq = s.lq;
+                it.lk = s.lk;
+                it.room = s.room;
+                it.first = s.tile * kKeys;
+                // the blocks of query rows that see the tile's first key, or later ones
+                it.j0 = a.causal ? max(0, it.first + s.lq - s.lk) / tpt : 0;
+                it.n0 = it.first < s.lk ? max(0, (s.lq + tpt - 1) / tpt - it.j0) : 0;
+                return true;
+            });
+        } else if (warp == kWarpLoad) {
             // ------------------------------------------------------------ loads
-            mbar_arrive_expect_tx_elect(kv_full, 2u * kTile);
-            for (int at = 0; at < kAtoms; ++at) {
-                tma_load_3d_elect(k_s + at * kAtomBytes, &mk, 64 * at, kh, s.k0 + j0, kv_full);
-                tma_load_3d_elect(v_s + at * kAtomBytes, &mv, 64 * at, kh, s.k0 + j0, kv_full);
-            }
-            const uint32_t bytes = static_cast<uint32_t>(kAtoms * tpt * a.group) * 128u;
-            bool ok = true;
-            uint32_t qi = 0, gi = 0;
-            for (int32_t i = 0; i < n && ok; ++i) {
-                const uint32_t st = static_cast<uint32_t>(i) % S, ph = (static_cast<uint32_t>(i) / S) & 1u;
-                const int32_t row = s.q0 + (b0 + i) * tpt;
-                if (!(ok = warp_wait_bounded(q_empty(st), ph ^ 1u, abort_flag, a.status, kSiteTmaEmpty))) break;
-                mbar_arrive_expect_tx_elect(q_full(st), bytes);
-                for (int at = 0; at < kAtoms; ++at)
-                    tma_load_4d_elect(q_ring + st * kTile + at * kAtomBytes, &mq, 64 * at, 0, kh, row, q_full(st));
-                ++qi;
-                if (!(ok = warp_wait_bounded(g_empty(st), ph ^ 1u, abort_flag, a.status, kSiteTmaEmpty))) break;
-                mbar_arrive_expect_tx_elect(g_full(st), bytes);
-                for (int at = 0; at < kAtoms; ++at)
-                    tma_load_4d_elect(g_ring + st * kTile + at * kAtomBytes, &mg, 64 * at, 0, kh, row, g_full(st));
-                ++gi;
-            }
-            if (!ok) {  // the copies already issued land before the CTA exits
+            const uint32_t bytes = static_cast<uint32_t>(kAtoms * most) * 128u;
+            uint32_t qi = 0, gi = 0, tiles = 0;
+            for_items(queue, abort_flag, a.status, [&](const AttnItem& it) {
+                if (it.n0 == 0) return true;
+                if (!warp_wait_bounded(kv_empty, (tiles & 1u) ^ 1u, abort_flag, a.status, kSiteTmaEmpty)) return false;
+                mbar_arrive_expect_tx_elect(kv_full, 2u * kTile);
+                for (int at = 0; at < kAtoms; ++at) {
+                    tma_load_3d_elect(k_s + at * kAtomBytes, &mk, 64 * at, it.kh, it.k0 + it.first, kv_full);
+                    tma_load_3d_elect(v_s + at * kAtomBytes, &mv, 64 * at, it.kh, it.k0 + it.first, kv_full);
+                }
+                ++tiles;
+                for (int32_t i = 0; i < it.n0; ++i) {
+                    const int32_t row = it.q0 + (it.j0 + i) * tpt;
+                    const uint32_t st = qi % S, ph = (qi / S) & 1u;
+                    if (!warp_wait_bounded(q_empty(st), ph ^ 1u, abort_flag, a.status, kSiteTmaEmpty)) return false;
+                    mbar_arrive_expect_tx_elect(q_full(st), bytes);
+                    for (int at = 0; at < kAtoms; ++at)
+                        tma_load_4d_elect(q_ring + st * kTile + at * kAtomBytes, &mq, 64 * at, 0, it.kh, row, q_full(st));
+                    ++qi;
+                    if (!warp_wait_bounded(g_empty(st), ph ^ 1u, abort_flag, a.status, kSiteTmaEmpty)) return false;
+                    mbar_arrive_expect_tx_elect(g_full(st), bytes);
+                    for (int at = 0; at < kAtoms; ++at)
+                        tma_load_4d_elect(g_ring + st * kTile + at * kAtomBytes, &mg, 64 * at, 0, it.kh, row, g_full(st));
+                    ++gi;
+                }
+                return true;
+            });
+            if (*abort_flag) {  // the copies already issued land before the CTA exits
                 volatile int never = 0;
-                warp_wait_bounded(kv_full, 0, &never, a.status, kSiteDrain, 200000000ull);
+                if (tiles) warp_wait_bounded(kv_full, (tiles - 1) & 1u, &never, a.status, kSiteDrain, 200000000ull);
                 for (uint32_t i = qi > S ? qi - S : 0; i < qi; ++i)
                     warp_wait_bounded(q_full(i % S), (i / S) & 1, &never, a.status, kSiteDrain, 200000000ull);
                 for (uint32_t i = gi > S ? gi - S : 0; i < gi; ++i)
                     warp_wait_bounded(g_full(i % S), (i / S) & 1, &never, a.status, kSiteDrain, 200000000ull);
             }
-        } else if (warp == kWarpStats && n > 0) {
+        } else if (warp == kWarpAid) {
             // ------------------------------------------------------------ lse and delta of a block's rows
-            for (int32_t i = 0; i < n; ++i) {
-                const uint32_t st = static_cast<uint32_t>(i) % S, ph = (static_cast<uint32_t>(i) / S) & 1u;
-                const int32_t tok0 = (b0 + i) * tpt, rows = min(tpt, s.lq - tok0) * a.group;
-                float l[4], d[4];
+            uint32_t b = 0, turn = 0;  // blocks so far
+            for_items(queue, abort_flag, a.status, [&](const AttnItem& it) {
+                for (int32_t i = 0; i < it.n0; ++i, ++b) {
+                    const uint32_t st = b % S, ph = (b / S) & 1u;
+                    const int32_t tok0 = (it.j0 + i) * tpt, rows = min(tpt, it.lq - tok0) * a.group;
+                    float l[4], d[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int r = lane + 32 * k;
-                    l[k] = d[k] = 0.0f;
-                    if (r < rows) {
-                        const int64_t at = static_cast<int64_t>(kh * a.group + r % a.group) * a.tq + s.q0 + tok0 + r / a.group;
-                        l[k] = a.lse[at];
-                        d[k] = a.delta[at];
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = lane + 32 * k;
+                        l[k] = d[k] = 0.0f;
+                        if (r < rows) {
+                            const int64_t at =
+                                static_cast<int64_t>(it.kh * a.group + r % a.group) * a.tq + it.q0 + tok0 + r / a.group;
+                            l[k] = a.lse[at];
+                            d[k] = a.delta[at];
+                        }
+                    }
+                    if (!warp_wait_bounded(t_empty(st), ph ^ 1u, abort_flag, a.status, kSiteTmaEmpty)) return false;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        st_shared_f32(stats + st * 1024u + 4u * (lane + 32 * k), fmaf(-kLog2e, l[k], kShift));
+                        st_shared_f32(stats + st * 1024u + 512u + 4u * (lane + 32 * k), -d[k] * kUnshift);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(t_full(st));
+                    if (i + 1 == it.n0 && rows < most) {
+                        // the sequence's last block: another's rows behind its own, multiplied by 0 (the
+                        // issuing thread has seen both tiles arrive)
+                        if (!warp_wait2(to_clear, 0u, turn, abort_flag, a.status, kSiteTmaEmpty)) return false;
+                        turn ^= 1u;
+                        zero_rows(q_ring + st * kTile, kAtoms, kAtomBytes, rows, kAttnTcRows);
+                        zero_rows(g_ring + st * kTile, kAtoms, kAtomBytes, rows, kAttnTcRows);
+                        if (lane == 0) mbar_arrive(cleared);
                     }
                 }
-                if (!warp_wait_bounded(t_empty(st), ph ^ 1u, abort_flag, a.status, kSiteTmaEmpty)) break;
+                return true;
+            });
+        } else {
+            // ------------------------------------------------------------ MMAs, one thread
+            if (elect_lane()) {
+                const uint32_t fmt = kBf ? 1u : 0u;
+                const uint32_t nd = static_cast<uint32_t>((a.D + 15) & ~15);
+                const uint32_t id_s = make_idesc(fmt, 128u, 128u), id_o = make_idesc(fmt, 128u, nd) | (1u << 16);
+                const int ksteps = (a.D + 15) / 16;
+                const uint64_t dk0 = desc_sw128(k_s, 16u, 1024u), dv0 = desc_sw128(v_s, 16u, 1024u);
+                const uint64_t dq0 = desc_sw128(q_ring, 16u, 1024u), dg0 = desc_sw128(g_ring, 16u, 1024u);
+                const uint64_t mq0 = desc_sw128(q_ring, kAtomBytes, 1024u), mg0 = desc_sw128(g_ring, kAtomBytes, 1024u);
+                auto wait = [&](uint32_t b, uint32_t parity) {
+                    return mbar_wait_bounded(b, parity, abort_flag, a.status, kSiteMmaFull);
+                };
+                // d (+)= the rounded values at x times the rows at y, over the block's 128 rows
+                auto sums = [&](uint32_t d, uint32_t x, uint64_t y, bool more) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    st_shared_f32(stats + st * 1024u + 4u * (lane + 32 * k), fmaf(-kLog2e, l[k], kShift));
-                    st_shared_f32(stats + st * 1024u + 512u + 4u * (lane + 32 * k), -d[k] * kUnshift);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(t_full(st));
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_f16_ts(d, x + 8u * kk + (kk >= 4 ? 32u : 0u), y + 128u * kk, id_o, more || kk > 0);
+                };
+                uint32_t sq = 0, pq = 0, sg = 0, pg = 0;  // stage and phase of the next Q and G to arrive
+                uint32_t st = 0;                          // stage of the next sums
+                uint32_t step = 0, items = 0, clear = 0;  // parities
+                auto next = [&](uint32_t& s) {
+                    const bool wrap = ++s == S;
+                    if (wrap) s = 0;
+                    return wrap;
+                };
+                for_items_one(queue, abort_flag, a.status, [&](const AttnItem& it) {
+                    const int32_t n = it.n0;
+                    if (n == 0) return true;
+                    const bool partial = (it.lq - (it.j0 + n - 1) * tpt) * a.group < most;
+                    auto scores = [&]() {
+                        if (!wait(q_full(sq), pq)) return false;
+                        tc_fence_after();
+                        head_product<kAtoms>(c_s, dk0, dq0 + sq * (kTile >> 4), id_s, ksteps);
+                        mma_commit(s_full);
+                        if (next(sq)) pq ^= 1u;
+                        return true;
+                    };
+                    auto grads = [&](bool last) {
+                        if (!wait(g_full(sg), pg)) return false;
+                        if (last && partial) mbar_arrive(to_clear);  // this block's Q came before
+                        tc_fence_after();
+                        head_product<kAtoms>(c_dp, dv0, dg0 + sg * (kTile >> 4), id_s, ksteps);
+                        mma_commit(dp_full);
+                        if (last) mma_commit(kv_empty);
+                        if (next(sg)) pg ^= 1u;
+                        return true;
+                    };
+                    if (!wait(kv_full, items) || !scores() || !grads(n == 1)) return false;
+                    for (int32_t i = 0; i < n; ++i) {
+                        const uint64_t yq = mq0 + st * (kTile >> 4), yg = mg0 + st * (kTile >> 4);
+                        if (i == 0 && !wait(acc_read, items ^ 1u)) return false;
+                        if (i + 1 == n && partial) {
+                            if (!wait(cleared, clear)) return false;
+                            clear ^= 1u;
+                        }
+                        if (!wait(p_ready, step)) return false;
+                        tc_fence_after();
+                        sums(c_dv, c_s, yg, i > 0);
+                        mma_commit(g_empty(st));
+                        if (i + 1 < n && !scores()) return false;
+                        if (!wait(ds_ready, step)) return false;
+                        tc_fence_after();
+                        sums(c_dk, c_dp, yq, i > 0);
+                        mma_commit(q_empty(st));
+                        if (i + 1 < n && !grads(i + 2 == n)) return false;
+                        next(st);
+                        step ^= 1u;
+                    }
+                    mma_commit(done);
+                    items ^= 1u;
+                    return true;
+                });
+                mma_commit(drain);
+                volatile int never = 0;
+                mbar_wait_bounded(drain, 0, &never, a.status, kSiteDrain, 200000000ull);
             }
-        } else if (warp == kWarpIssue && n > 0) {
-            // ------------------------------------------------------------ MMAs
-            const uint32_t fmt = kBf ? 1u : 0u;
-            const uint32_t nd = static_cast<uint32_t>((a.D + 15) & ~15);
-            const uint32_t id_s = make_idesc(fmt, 128u, 128u), id_o = make_idesc(fmt, 128u, nd) | (1u << 16);
-            const int ksteps = (a.D + 15) / 16;
-            auto wait = [&](uint32_t b, uint32_t parity) {
-                return warp_wait2(b, 0u, parity, abort_flag, a.status, kSiteMmaFull);
-            };
-            auto product = [&](uint32_t d, uint32_t x, uint32_t y) {
-                for (int kk = 0; kk < ksteps; ++kk) {
-                    const uint32_t off = static_cast<uint32_t>(kk >> 2) * kAtomBytes + 32u * (kk & 3);
-                    mma_f16_elect(d, desc_sw128(x + off, 16u, 1024u), desc_sw128(y + off, 16u, 1024u), id_s, kk > 0);
-                }
-            };
-            auto sums = [&](uint32_t d, uint32_t x, uint32_t y, bool more) {
-                for (int kk = 0; kk < 8; ++kk)
-                    mma_f16_ts_elect(d, x + 8u * kk + (kk >= 4 ? 32u : 0u), desc_sw128(y + 2048u * kk, kAtomBytes, 1024u),
-                                     id_o, more || kk > 0);
-            };
-            // a block's rows past its last (another sequence's, or none) are multiplied by 0
-            auto arrived = [&](uint32_t b, uint32_t tile, int32_t i) {
-                if (!wait(b, (static_cast<uint32_t>(i) / S) & 1u)) return false;
-                const int32_t rows = min(tpt, s.lq - (b0 + i) * tpt) * a.group;
-                if (rows < kAttnTcRows) zero_rows(tile, kAtoms, kAtomBytes, rows, kAttnTcRows);
-                tc_fence_after();
-                return true;
-            };
-            auto scores = [&](int32_t i) {
-                const uint32_t st = static_cast<uint32_t>(i) % S;
-                if (!arrived(q_full(st), q_ring + st * kTile, i)) return false;
-                product(c_s, k_s, q_ring + st * kTile);
-                mma_commit_elect(s_full);
-                return true;
-            };
-            auto grads = [&](int32_t i) {
-                const uint32_t st = static_cast<uint32_t>(i) % S;
-                if (!arrived(g_full(st), g_ring + st * kTile, i)) return false;
-                product(c_dp, v_s, g_ring + st * kTile);
-                mma_commit_elect(dp_full);
-                return true;
-            };
-            bool ok = wait(kv_full, 0) && scores(0) && grads(0);
-            for (int32_t i = 0; i < n && ok; ++i) {
-                const uint32_t st = static_cast<uint32_t>(i) % S;
-                if (!(ok = wait(p_ready, i & 1))) break;
-                tc_fence_after();
-                sums(c_dv, c_s, g_ring + st * kTile, i > 0);
-                mma_commit_elect(g_empty(st));
-                if (i + 1 < n && !(ok = scores(i + 1))) break;
-                if (!(ok = wait(ds_ready, i & 1))) break;
-                tc_fence_after();
-                sums(c_dk, c_dp, q_ring + st * kTile, i > 0);
-                mma_commit_elect(q_empty(st));
-                if (i + 1 < n && !(ok = grads(i + 1))) break;
-            }
-            mma_commit_elect(done);
-            mma_commit_elect(drain);
-            volatile int never = 0;
-            warp_wait2(drain, 0u, 0, &never, a.status, kSiteDrain, 200000000ull);
+            __syncwarp();
         }
     } else {
         setmaxnreg_inc<kRegsRow>();
@@ -511,99 +627,103 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int half = warp >> 2;  // columns (query rows) [64 half, 64 half + 64) of each block
         const int r = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const int32_t key = j0 + r;
         const float sc = a.scale * kLog2e;
         const uint64_t sc2 = pack2(sc, sc);
-        bool ok = true;
-        for (int32_t i = 0; i < n; ++i) {
-            const uint32_t st = static_cast<uint32_t>(i) % S, ph = (static_cast<uint32_t>(i) / S) & 1u;
-            const int32_t tok0 = (b0 + i) * tpt, rows = min(tpt, s.lq - tok0) * a.group;
-            // this key is seen by the block's rows from `from` on
-            const int32_t from = a.causal ? min(max(0, key - shift - tok0), tpt) * a.group : 0;
-            const bool masked = __any_sync(0xffffffffu, from > 64 * half) || rows < 64 * half + 64;
-            const uint32_t lse_s = stats + st * 1024u + 256u * half, delta_s = lse_s + 512u;
-            if (!(ok = warp_wait2(t_full(st), 0u, ph, abort_flag, a.status, kSiteGatherEmpty))) break;
-            if (!(ok = warp_wait2(s_full, 0u, i & 1, abort_flag, a.status, kSiteGatherEmpty))) break;
-            tc_fence_after();
-            uint32_t x[2][32], out[32];
-            load_half(c_s + lanes + 64u * half, x);
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int k = 0; k < 32; k += 4) {
-                    const uint4 l = ld_shared_v4(lse_s + 4u * (32 * c + k));
-                    float u, w;
-                    unpack2(fma2(pack2(__uint_as_float(x[c][k]), __uint_as_float(x[c][k + 1])), sc2,
-                                 pack2(__uint_as_float(l.x), __uint_as_float(l.y))),
-                            u, w);
-                    x[c][k] = __float_as_uint(attn_exp2(u));
-                    x[c][k + 1] = __float_as_uint(attn_exp2(w));
-                    unpack2(fma2(pack2(__uint_as_float(x[c][k + 2]), __uint_as_float(x[c][k + 3])), sc2,
-                                 pack2(__uint_as_float(l.z), __uint_as_float(l.w))),
-                            u, w);
-                    x[c][k + 2] = __float_as_uint(attn_exp2(u));
-                    x[c][k + 3] = __float_as_uint(attn_exp2(w));
-                }
-            if (masked) {
-                const int32_t lo = from - 64 * half, hi = rows - 64 * half;
+        uint32_t b = 0, items = 0;  // blocks, and items with any, so far
+        for_items(queue, abort_flag, a.status, [&](const AttnItem& it) {
+            const int32_t key = it.first + r, shift = it.lk - it.lq, n = it.n0;
+            for (int32_t i = 0; i < n; ++i, ++b) {
+                const uint32_t st = b % S, ph = (b / S) & 1u;
+                const int32_t tok0 = (it.j0 + i) * tpt, rows = min(tpt, it.lq - tok0) * a.group;
+                // this key is seen by the block's rows from `from` on
+                const int32_t from = a.causal ? min(max(0, key - shift - tok0), tpt) * a.group : 0;
+                const bool masked = __any_sync(0xffffffffu, from > 64 * half) || rows < 64 * half + 64;
+                const uint32_t lse_s = stats + st * 1024u + 256u * half, delta_s = lse_s + 512u;
+                if (!warp_wait2(t_full(st), 0u, ph, abort_flag, a.status, kSiteGatherEmpty)) return false;
+                if (!warp_wait2(s_full, 0u, b & 1u, abort_flag, a.status, kSiteGatherEmpty)) return false;
+                tc_fence_after();
+                uint32_t x[2][32], out[32];
+                load_half(c_s + lanes + 64u * half, x);
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (32 * c + k < lo || 32 * c + k >= hi) x[c][k] = 0u;
-            }
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-                out[k] = round2<kBf>(__uint_as_float(x[k >> 4][2 * (k & 15)]), __uint_as_float(x[k >> 4][2 * (k & 15) + 1]));
-            tmem_st32(c_s + lanes + 64u * half, out);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(p_ready);
-
-            if (!(ok = warp_wait2(dp_full, 0u, i & 1, abort_flag, a.status, kSiteGatherEmpty))) break;
-            tc_fence_after();
-            uint32_t dp[2][32];
-            load_half(c_dp + lanes + 64u * half, dp);
-            if (masked) {
-                const int32_t lo = from - 64 * half, hi = rows - 64 * half;
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (32 * c + k < lo || 32 * c + k >= hi) dp[c][k] = 0u;
-            }
-            uint64_t d2[2];
-            score_grads<kBf>(
-                x, dp,
-                [&](int k) {
-                    if ((k & 2) == 0) {
-                        const uint4 d = ld_shared_v4(delta_s + 4u * k);
-                        d2[0] = pack2(__uint_as_float(d.x), __uint_as_float(d.y));
-                        d2[1] = pack2(__uint_as_float(d.z), __uint_as_float(d.w));
+                    for (int k = 0; k < 32; k += 4) {
+                        const uint4 l = ld_shared_v4(lse_s + 4u * (32 * c + k));
+                        float u, w;
+                        unpack2(fma2(pack2(__uint_as_float(x[c][k]), __uint_as_float(x[c][k + 1])), sc2,
+                                     pack2(__uint_as_float(l.x), __uint_as_float(l.y))),
+                                u, w);
+                        x[c][k] = __float_as_uint(attn_exp2(u));
+                        x[c][k + 1] = __float_as_uint(attn_exp2(w));
+                        unpack2(fma2(pack2(__uint_as_float(x[c][k + 2]), __uint_as_float(x[c][k + 3])), sc2,
+                                     pack2(__uint_as_float(l.z), __uint_as_float(l.w))),
+                                u, w);
+                        x[c][k + 2] = __float_as_uint(attn_exp2(u));
+                        x[c][k + 3] = __float_as_uint(attn_exp2(w));
                     }
-                    return d2[(k >> 1) & 1];
-                },
-                out);
-            tmem_st32(c_dp + lanes + 64u * half, out);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(ds_ready);
-                mbar_arrive(t_empty(st));
+                if (masked) {
+                    const int32_t lo = from - 64 * half, hi = rows - 64 * half;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (32 * c + k < lo || 32 * c + k >= hi) x[c][k] = 0u;
+                }
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    out[k] =
+                        round2<kBf>(__uint_as_float(x[k >> 4][2 * (k & 15)]), __uint_as_float(x[k >> 4][2 * (k & 15) + 1]));
+                tmem_st32(c_s + lanes + 64u * half, out);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_ready);
+
+                if (!warp_wait2(dp_full, 0u, b & 1u, abort_flag, a.status, kSiteGatherEmpty)) return false;
+                tc_fence_after();
+                uint32_t dp[2][32];
+                load_half(c_dp + lanes + 64u * half, dp);
+                if (masked) {
+                    const int32_t lo = from - 64 * half, hi = rows - 64 * half;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (32 * c + k < lo || 32 * c + k >= hi) dp[c][k] = 0u;
+                }
+                uint64_t d2[2];
+                score_grads<kBf>(
+                    x, dp,
+                    [&](int k) {
+                        if ((k & 2) == 0) {
+                            const uint4 d = ld_shared_v4(delta_s + 4u * k);
+                            d2[0] = pack2(__uint_as_float(d.x), __uint_as_float(d.y));
+                            d2[1] = pack2(__uint_as_float(d.z), __uint_as_float(d.w));
+                        }
+                        return d2[(k >> 1) & 1];
+                    },
+                    out);
+                tmem_st32(c_dp + lanes + 64u * half, out);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(ds_ready);
+                    mbar_arrive(t_empty(st));
+                }
             }
-        }
-        const bool any = n > 0;
-        if (any && ok) ok = warp_wait2(done, 0u, 0, abort_flag, a.status, kSiteEpilogue);
-        if (ok && *abort_flag == 0) {
-            tc_fence_after();
+            const bool any = n > 0;
+            if (any) {
+                if (!warp_wait2(done, 0u, items & 1u, abort_flag, a.status, kSiteEpilogue)) return false;
+                ++items;
+                tc_fence_after();
+            }
             const AttnTensor& t = half ? a.gk : a.gv;
-            uint8_t* p = static_cast<uint8_t*>(t.p) + 2 * (static_cast<int64_t>(s.k0 + key) * t.st + kh * t.sh);
+            uint8_t* p = static_cast<uint8_t*>(t.p) + 2 * (static_cast<int64_t>(it.k0 + key) * t.st + it.kh * t.sh);
             // keys past the last in use see nothing: their rows hold zeros
-            const bool used = any && key < s.lk;
+            const bool used = any && key < it.lk;
             const float f = used ? (half ? a.scale : kUnshift) : 0.0f;
-            const bool live = key < s.room;
+            const bool live = key < it.room;
             const bool wide = (reinterpret_cast<uintptr_t>(p) & 31u) == 0;
 #pragma unroll 1
             for (int c = 0; c < a.D; c += 16) {
@@ -614,7 +734,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int i = 0; i < 16; ++i) v[i] = used ? v[i] * f : 0.0f;
                 store16<kBf>(p + 2 * c, v, a.D - c, wide);
             }
-        }
+            if (any) {  // the next item's first sums may overwrite dV and dK
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(acc_read);
+            }
+            return true;
+        });
     }
     tc_fence_before();
     __syncthreads();
@@ -640,7 +766,7 @@ cudaError_t launch_backward(int dtype, const AttnArgs& a, cudaStream_t st) {
         static_assert(smem <= 227 * 1024, "shared memory");
         if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
         const unsigned tiles = static_cast<unsigned>(attn_tiles(a.tq, a.batch, tpt));
-        kern<<<dim3(tiles, hk), kTcThreads, smem, st>>>(mq, mg, mk, mv, a);
+        kern<<<tiles * hk, kTcThreads, smem, st>>>(mq, mg, mk, mv, a);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     if (a.tk > 0) {
@@ -649,7 +775,7 @@ cudaError_t launch_backward(int dtype, const AttnArgs& a, cudaStream_t st) {
         static_assert(smem <= 227 * 1024, "shared memory");
         if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
         const unsigned tiles = static_cast<unsigned>(attn_tiles(a.tk, a.batch, kKeys));
-        kern<<<dim3(tiles, hk), kTcThreads, smem, st>>>(mq, mg, mk, mv, a);
+        kern<<<tiles * hk, kTcThreads, smem, st>>>(mq, mg, mk, mv, a);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     return cudaSuccess;

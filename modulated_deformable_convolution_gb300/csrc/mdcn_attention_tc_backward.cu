@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 };
                 uint32_t st = 0, ph = 0;        // stage and phase of the next tile to arrive
                 uint32_t ks = 0;                // stage of the next K to be summed
-                uint32_t read = 1, ds = 0;      // parities: S and dP read, dS written
+                uint32_t read_s = 1, read_dp = 1, ds = 0;  // parities: S and dP read, dS written
                 uint32_t items = 0, clear = 0;  // parities
                 auto next = [&](uint32_t& s) {
                     const bool wrap = ++s == S;
@@ -237,30 +237,38 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const int32_t n = it.n0;
                     if (n == 0) return true;
                     const bool partial = it.lk - (n - 1) * kKeys < kKeys;
-                    // S and dP of the next key tile, into the buffers whose previous values have been read
+                    // S, then dP, of the next key tile, into the buffer whose previous values have been read
                     auto scores = [&](bool last) {
-                        if (!wait(full(st), ph) || !wait(s_read, read)) return false;
+                        if (!wait(full(st), ph) || !wait(s_read, read_s)) return false;
                         if (last && partial) mbar_arrive(to_clear);
                         tc_fence_after();
                         head_product<kAtoms>(c_s, dq0, dk0 + st * (kTile >> 4), id_s, ksteps);
                         mma_commit(s_full);
                         if (next(st)) ph ^= 1u;
-                        if (!wait(full(st), ph) || !wait(dp_read, read)) return false;
+                        read_s ^= 1u;
+                        return true;
+                    };
+                    auto grads = [&](bool last) {
+                        if (!wait(full(st), ph) || !wait(dp_read, read_dp)) return false;
                         tc_fence_after();
                         head_product<kAtoms>(c_dp, dg0, dk0 + st * (kTile >> 4), id_s, ksteps);
                         mma_commit(dp_full);
                         mma_commit(empty(st));
                         if (last) mma_commit(q_empty);
                         if (next(st)) ph ^= 1u;
-                        read ^= 1u;
+                        read_dp ^= 1u;
                         return true;
                     };
-                    if (!wait(q_full, items) || !scores(n == 1)) return false;
+                    if (!wait(q_full, items) || !scores(n == 1) || !grads(n == 1)) return false;
                     for (int32_t j = 0; j < n; ++j) {
-                        if (j + 1 < n && !scores(j + 2 == n)) return false;
+                        const bool more = j + 1 < n, last = j + 2 == n;
+                        if (more && !scores(last)) return false;
+                        // The ring of five 128-element tiles has no room for the next V before this K is
+                        // summed and freed; that of eight 64-element tiles does
+                        if (more && kAtoms == 1 && !grads(last)) return false;
                         if (j == 0 && !wait(dq_read, items ^ 1u)) return false;
                         // dQ += dS K multiplies the rows past the last key by 0
-                        if (j + 1 == n && partial) {
+                        if (!more && partial) {
                             if (!wait(cleared, clear)) return false;
                             clear ^= 1u;
                         }
@@ -275,6 +283,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         mma_commit(empty(ks));
                         next(ks);
                         next(ks);
+                        if (more && kAtoms == 2 && !grads(last)) return false;
                     }
                     items ^= 1u;
                     return true;
@@ -374,13 +383,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 // ---------------------------------------------------------------- grad_k, grad_v
-// Tensor memory: S^T [0, 128) with P^T over it, dP^T [128, 256) with dS^T over
-// it, dV [256, 256 + D), dK [384, 384 + D). Each half of the columns keeps its
-// rounded values in its own half (at 0 and 64), so neither warpgroup overwrites
-// what the other still reads.
-__host__ __device__ constexpr uint32_t kv_stages(int atoms) { return atoms == 2 ? 2 : 4; }
+// Tensor memory: S^T with P^T over it, dP^T with dS^T over it (128 columns
+// each), dV, dK. Each half of the columns keeps its rounded values in its own
+// half (at 0 and 64), so neither warpgroup overwrites what the other still
+// reads. Heads of at most 64 elements leave room for a second S^T, so that a
+// block's S is there when the elementwise step of the one before ends.
+// Shared memory: K, V, rings of Q (whose tiles are held longest, from S to dK)
+// and of G, and the rows' lse and delta. At D = 128 it is used to the last
+// kilobyte: a third Q tile is worth more than any slack.
+__host__ __device__ constexpr uint32_t kv_q_stages(int atoms) { return atoms == 2 ? 3 : 5; }
+__host__ __device__ constexpr uint32_t kv_g_stages(int atoms) { return atoms == 2 ? 2 : 4; }
+constexpr uint32_t kStatStages = 2;
 __host__ __device__ constexpr int smem_kv(int atoms) {
-    return 1024 + static_cast<int>((2 + 2 * kv_stages(atoms)) * atoms * kAtomBytes + kv_stages(atoms) * 1024u) + 768;
+    return static_cast<int>((2 + kv_q_stages(atoms) + kv_g_stages(atoms)) * atoms * kAtomBytes + kStatStages * 1024u) + 1024;
 }
 
 template <int kAtoms, bool kBf>
@@ -388,40 +403,47 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     attn_grad_kv_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg,
                            const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                            const __grid_constant__ AttnArgs a) {
-    constexpr uint32_t S = kv_stages(kAtoms);
+    constexpr uint32_t SQ = kv_q_stages(kAtoms), SG = kv_g_stages(kAtoms), ST = kStatStages;
+    constexpr uint32_t NS = kAtoms == 2 ? 1 : 2;  // S^T buffers
     constexpr uint32_t kTile = kAtoms * kAtomBytes;
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
-    const uint32_t k_s = base, v_s = base + kTile, q_ring = base + 2 * kTile, g_ring = q_ring + S * kTile;
-    const uint32_t stats = g_ring + S * kTile;  // per stage: 128 x (8 - lse'), 128 x (-delta 2^-8)
-    const ItemQueue queue{stats + S * 1024u};
+    if (raw & 1023u) {  // the tiles' swizzle needs the alignment asked for above
+        if (threadIdx.x == 0) atomicOr(a.status, kStatusTimeout | kSiteSelftest);
+        return;
+    }
+    const uint32_t k_s = raw, v_s = raw + kTile, q_ring = raw + 2 * kTile, g_ring = q_ring + SQ * kTile;
+    const uint32_t stats = g_ring + SG * kTile;  // per stage: 128 x (8 - lse'), 128 x (-delta 2^-8)
+    const ItemQueue queue{stats + ST * 1024u};
     const uint32_t bars = queue.base + ItemQueue::kBytes;
-    auto bar = [&](uint32_t kind, uint32_t s) { return bars + 8u * (kind * S + s); };
-    auto q_full = [&](uint32_t s) { return bar(0, s); };
-    auto q_empty = [&](uint32_t s) { return bar(1, s); };
-    auto g_full = [&](uint32_t s) { return bar(2, s); };
-    auto g_empty = [&](uint32_t s) { return bar(3, s); };
-    auto t_full = [&](uint32_t s) { return bar(4, s); };
-    auto t_empty = [&](uint32_t s) { return bar(5, s); };
-    const uint32_t rest = bars + 48u * S;
-    const uint32_t kv_full = rest, kv_empty = rest + 8, s_full = rest + 16, dp_full = rest + 24, p_ready = rest + 32,
-                   ds_ready = rest + 40, done = rest + 48, acc_read = rest + 56, drain = rest + 64,
-                   cleared = rest + 72, to_clear = rest + 80;
-    const uint32_t slot_off = rest + 88 - raw;
+    auto q_full = [&](uint32_t s) { return bars + 8u * s; };
+    auto q_empty = [&](uint32_t s) { return bars + 8u * (SQ + s); };
+    const uint32_t bars_g = bars + 16u * SQ, bars_t = bars_g + 16u * SG, rest = bars_t + 16u * ST;
+    auto g_full = [&](uint32_t s) { return bars_g + 8u * s; };
+    auto g_empty = [&](uint32_t s) { return bars_g + 8u * (SG + s); };
+    auto t_full = [&](uint32_t s) { return bars_t + 8u * s; };
+    auto t_empty = [&](uint32_t s) { return bars_t + 8u * (ST + s); };
+    // a block's S and P signal by its buffer: either side may be one block ahead of the other
+    auto s_full = [&](uint32_t b) { return rest + 8u * b; };
+    auto p_ready = [&](uint32_t b) { return rest + 16u + 8u * b; };
+    const uint32_t kv_full = rest + 32, kv_empty = rest + 40, dp_full = rest + 48, ds_ready = rest + 56,
+                   done = rest + 64, acc_read = rest + 72, drain = rest + 80, cleared = rest + 88, to_clear = rest + 96;
+    const uint32_t slot_off = rest + 104 - raw;
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem_raw + slot_off);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem_raw + slot_off + 4);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tpt = kAttnTcRows / a.group, most = tpt * a.group;  // rows of a full block
     if (warp == kWarpLoad && lane == 0) {
-        for (uint32_t i = 0; i < S; ++i) {
-            for (uint32_t kind = 0; kind < 5; ++kind) mbar_init(bar(kind, i), 1);
+        for (uint32_t i = 0; i < 2 * SQ; ++i) mbar_init(bars + 8u * i, 1);
+        for (uint32_t i = 0; i < 2 * SG; ++i) mbar_init(bars_g + 8u * i, 1);
+        for (uint32_t i = 0; i < ST; ++i) {
+            mbar_init(t_full(i), 1);
             mbar_init(t_empty(i), 8);
         }
-        const uint32_t ones[] = {kv_full, kv_empty, s_full, dp_full, done, drain, cleared, to_clear};
+        const uint32_t ones[] = {s_full(0), s_full(1), kv_full, kv_empty, dp_full, done, drain, cleared, to_clear};
         for (uint32_t b : ones) mbar_init(b, 1);
-        const uint32_t eights[] = {p_ready, ds_ready, acc_read};
+        const uint32_t eights[] = {p_ready(0), p_ready(1), ds_ready, acc_read};
         for (uint32_t b : eights) mbar_init(b, 8);
         queue.init(11);
         *abort_flag = 0;
@@ -438,13 +460,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (warp == kWarpAid && most < kAttnTcRows) {
         // rows that no copy ever writes (a group that does not divide the tile): zero for good, since
         // the sums multiply them by 0
-        for (uint32_t i = 0; i < 2 * S; ++i) zero_rows(q_ring + i * kTile, kAtoms, kAtomBytes, most, kAttnTcRows);
+        for (uint32_t i = 0; i < SQ + SG; ++i) zero_rows(q_ring + i * kTile, kAtoms, kAtomBytes, most, kAttnTcRows);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const uint32_t c_s = tmem, c_dp = tmem + 128u, c_dv = tmem + 256u, c_dk = tmem + 384u;
+    const uint32_t c_dp = tmem + 128u * NS, c_dv = c_dp + 128u, c_dk = c_dv + 64u * kAtoms;
+    auto c_s = [&](uint32_t b) { return tmem + 128u * b; };
 
     if (warp >= 8) {
         setmaxnreg_dec<kRegsCtl>();
@@ -480,16 +503,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 ++tiles;
                 for (int32_t i = 0; i < it.n0; ++i) {
                     const int32_t row = it.q0 + (it.j0 + i) * tpt;
-                    const uint32_t st = qi % S, ph = (qi / S) & 1u;
-                    if (!warp_wait_bounded(q_empty(st), ph ^ 1u, abort_flag, a.status, kSiteTmaEmpty)) return false;
-                    mbar_arrive_expect_tx_elect(q_full(st), bytes);
+                    const uint32_t sq = qi % SQ, sg = gi % SG;
+                    if (!warp_wait_bounded(q_empty(sq), ((qi / SQ) & 1u) ^ 1u, abort_flag, a.status, kSiteTmaEmpty))
+                        return false;
+                    mbar_arrive_expect_tx_elect(q_full(sq), bytes);
                     for (int at = 0; at < kAtoms; ++at)
-                        tma_load_4d_elect(q_ring + st * kTile + at * kAtomBytes, &mq, 64 * at, 0, it.kh, row, q_full(st));
+                        tma_load_4d_elect(q_ring + sq * kTile + at * kAtomBytes, &mq, 64 * at, 0, it.kh, row, q_full(sq));
                     ++qi;
-                    if (!warp_wait_bounded(g_empty(st), ph ^ 1u, abort_flag, a.status, kSiteTmaEmpty)) return false;
-                    mbar_arrive_expect_tx_elect(g_full(st), bytes);
+                    if (!warp_wait_bounded(g_empty(sg), ((gi / SG) & 1u) ^ 1u, abort_flag, a.status, kSiteTmaEmpty))
+                        return false;
+                    mbar_arrive_expect_tx_elect(g_full(sg), bytes);
                     for (int at = 0; at < kAtoms; ++at)
-                        tma_load_4d_elect(g_ring + st * kTile + at * kAtomBytes, &mg, 64 * at, 0, it.kh, row, g_full(st));
+                        tma_load_4d_elect(g_ring + sg * kTile + at * kAtomBytes, &mg, 64 * at, 0, it.kh, row, g_full(sg));
                     ++gi;
                 }
                 return true;
@@ -497,17 +522,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (*abort_flag) {  // the copies already issued land before the CTA exits
                 volatile int never = 0;
                 if (tiles) warp_wait_bounded(kv_full, (tiles - 1) & 1u, &never, a.status, kSiteDrain, 200000000ull);
-                for (uint32_t i = qi > S ? qi - S : 0; i < qi; ++i)
-                    warp_wait_bounded(q_full(i % S), (i / S) & 1, &never, a.status, kSiteDrain, 200000000ull);
-                for (uint32_t i = gi > S ? gi - S : 0; i < gi; ++i)
-                    warp_wait_bounded(g_full(i % S), (i / S) & 1, &never, a.status, kSiteDrain, 200000000ull);
+                for (uint32_t i = qi > SQ ? qi - SQ : 0; i < qi; ++i)
+                    warp_wait_bounded(q_full(i % SQ), (i / SQ) & 1, &never, a.status, kSiteDrain, 200000000ull);
+                for (uint32_t i = gi > SG ? gi - SG : 0; i < gi; ++i)
+                    warp_wait_bounded(g_full(i % SG), (i / SG) & 1, &never, a.status, kSiteDrain, 200000000ull);
             }
         } else if (warp == kWarpAid) {
             // ------------------------------------------------------------ lse and delta of a block's rows
             uint32_t b = 0, turn = 0;  // blocks so far
             for_items(queue, abort_flag, a.status, [&](const AttnItem& it) {
                 for (int32_t i = 0; i < it.n0; ++i, ++b) {
-                    const uint32_t st = b % S, ph = (b / S) & 1u;
+                    const uint32_t st = b % ST, ph = (b / ST) & 1u;
                     const int32_t tok0 = (it.j0 + i) * tpt, rows = min(tpt, it.lq - tok0) * a.group;
                     float l[4], d[4];
 #pragma unroll
@@ -534,8 +559,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         // issuing thread has seen both tiles arrive)
                         if (!warp_wait2(to_clear, 0u, turn, abort_flag, a.status, kSiteTmaEmpty)) return false;
                         turn ^= 1u;
-                        zero_rows(q_ring + st * kTile, kAtoms, kAtomBytes, rows, kAttnTcRows);
-                        zero_rows(g_ring + st * kTile, kAtoms, kAtomBytes, rows, kAttnTcRows);
+                        zero_rows(q_ring + (b % SQ) * kTile, kAtoms, kAtomBytes, rows, kAttnTcRows);
+                        zero_rows(g_ring + (b % SG) * kTile, kAtoms, kAtomBytes, rows, kAttnTcRows);
                         if (lane == 0) mbar_arrive(cleared);
                     }
                 }
@@ -561,10 +586,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         mma_f16_ts(d, x + 8u * kk + (kk >= 4 ? 32u : 0u), y + 128u * kk, id_o, more || kk > 0);
                 };
                 uint32_t sq = 0, pq = 0, sg = 0, pg = 0;  // stage and phase of the next Q and G to arrive
-                uint32_t st = 0;                          // stage of the next sums
-                uint32_t step = 0, items = 0, clear = 0;  // parities
-                auto next = [&](uint32_t& s) {
-                    const bool wrap = ++s == S;
+                uint32_t tq = 0, tg = 0;                  // stages of the next sums
+                uint32_t bs = 0;                          // blocks whose S has been issued
+                uint32_t b = 0;                           // blocks summed
+                uint32_t items = 0, clear = 0;            // parities
+                auto next = [](uint32_t& s, uint32_t n) {
+                    const bool wrap = ++s == n;
                     if (wrap) s = 0;
                     return wrap;
                 };
@@ -575,9 +602,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     auto scores = [&]() {
                         if (!wait(q_full(sq), pq)) return false;
                         tc_fence_after();
-                        head_product<kAtoms>(c_s, dk0, dq0 + sq * (kTile >> 4), id_s, ksteps);
-                        mma_commit(s_full);
-                        if (next(sq)) pq ^= 1u;
+                        head_product<kAtoms>(c_s(bs % NS), dk0, dq0 + sq * (kTile >> 4), id_s, ksteps);
+                        mma_commit(s_full(bs % NS));
+                        ++bs;
+                        if (next(sq, SQ)) pq ^= 1u;
                         return true;
                     };
                     auto grads = [&](bool last) {
@@ -587,29 +615,31 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         head_product<kAtoms>(c_dp, dv0, dg0 + sg * (kTile >> 4), id_s, ksteps);
                         mma_commit(dp_full);
                         if (last) mma_commit(kv_empty);
-                        if (next(sg)) pg ^= 1u;
+                        if (next(sg, SG)) pg ^= 1u;
                         return true;
                     };
                     if (!wait(kv_full, items) || !scores() || !grads(n == 1)) return false;
-                    for (int32_t i = 0; i < n; ++i) {
-                        const uint64_t yq = mq0 + st * (kTile >> 4), yg = mg0 + st * (kTile >> 4);
+                    for (int32_t i = 0; i < n; ++i, ++b) {
+                        const uint64_t yq = mq0 + tq * (kTile >> 4), yg = mg0 + tg * (kTile >> 4);
+                        // a second S^T: the next block's goes ahead of this one's sums
+                        if (NS == 2 && i + 1 < n && !scores()) return false;
                         if (i == 0 && !wait(acc_read, items ^ 1u)) return false;
                         if (i + 1 == n && partial) {
                             if (!wait(cleared, clear)) return false;
                             clear ^= 1u;
                         }
-                        if (!wait(p_ready, step)) return false;
+                        if (!wait(p_ready(b % NS), (b / NS) & 1u)) return false;
                         tc_fence_after();
-                        sums(c_dv, c_s, yg, i > 0);
-                        mma_commit(g_empty(st));
-                        if (i + 1 < n && !scores()) return false;
-                        if (!wait(ds_ready, step)) return false;
+                        sums(c_dv, c_s(b % NS), yg, i > 0);
+                        mma_commit(g_empty(tg));
+                        if (NS == 1 && i + 1 < n && !scores()) return false;
+                        if (!wait(ds_ready, b & 1u)) return false;
                         tc_fence_after();
                         sums(c_dk, c_dp, yq, i > 0);
-                        mma_commit(q_empty(st));
+                        mma_commit(q_empty(tq));
                         if (i + 1 < n && !grads(i + 2 == n)) return false;
-                        next(st);
-                        step ^= 1u;
+                        next(tq, SQ);
+                        next(tg, SG);
                     }
                     mma_commit(done);
                     items ^= 1u;
@@ -633,17 +663,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for_items(queue, abort_flag, a.status, [&](const AttnItem& it) {
             const int32_t key = it.first + r, shift = it.lk - it.lq, n = it.n0;
             for (int32_t i = 0; i < n; ++i, ++b) {
-                const uint32_t st = b % S, ph = (b / S) & 1u;
+                const uint32_t st = b % ST, ph = (b / ST) & 1u, scol = c_s(b % NS) + lanes + 64u * half;
                 const int32_t tok0 = (it.j0 + i) * tpt, rows = min(tpt, it.lq - tok0) * a.group;
                 // this key is seen by the block's rows from `from` on
                 const int32_t from = a.causal ? min(max(0, key - shift - tok0), tpt) * a.group : 0;
                 const bool masked = __any_sync(0xffffffffu, from > 64 * half) || rows < 64 * half + 64;
                 const uint32_t lse_s = stats + st * 1024u + 256u * half, delta_s = lse_s + 512u;
                 if (!warp_wait2(t_full(st), 0u, ph, abort_flag, a.status, kSiteGatherEmpty)) return false;
-                if (!warp_wait2(s_full, 0u, b & 1u, abort_flag, a.status, kSiteGatherEmpty)) return false;
+                if (!warp_wait2(s_full(b % NS), 0u, (b / NS) & 1u, abort_flag, a.status, kSiteGatherEmpty)) return false;
                 tc_fence_after();
                 uint32_t x[2][32], out[32];
-                load_half(c_s + lanes + 64u * half, x);
+                load_half(scol, x);
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -673,11 +703,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int k = 0; k < 32; ++k)
                     out[k] =
                         round2<kBf>(__uint_as_float(x[k >> 4][2 * (k & 15)]), __uint_as_float(x[k >> 4][2 * (k & 15) + 1]));
-                tmem_st32(c_s + lanes + 64u * half, out);
+                tmem_st32(scol, out);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_ready);
+                if (lane == 0) mbar_arrive(p_ready(b % NS));
 
                 if (!warp_wait2(dp_full, 0u, b & 1u, abort_flag, a.status, kSiteGatherEmpty)) return false;
                 tc_fence_after();

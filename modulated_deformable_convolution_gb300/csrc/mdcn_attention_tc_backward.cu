@@ -529,23 +529,40 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
         } else if (warp == kWarpAid) {
             // ------------------------------------------------------------ lse and delta of a block's rows
+            // A lane's four rows of a block are the same in every block: their places are taken apart
+            // once, and the next block's values are on their way while this one's are handed over.
             uint32_t b = 0, turn = 0;  // blocks so far
+            int64_t place[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = lane + 32 * k;
+                place[k] = static_cast<int64_t>(r % a.group) * a.tq + r / a.group;
+            }
             for_items(queue, abort_flag, a.status, [&](const AttnItem& it) {
+                const int64_t head = static_cast<int64_t>(it.kh) * a.group * a.tq + it.q0;
+                float nl[4], nd[4];
+                auto fetch = [&](int32_t i) {
+                    const int32_t tok0 = (it.j0 + i) * tpt, rows = i < it.n0 ? min(tpt, it.lq - tok0) * a.group : 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        nl[k] = nd[k] = 0.0f;
+                        if (lane + 32 * k < rows) {
+                            nl[k] = a.lse[head + tok0 + place[k]];
+                            nd[k] = a.delta[head + tok0 + place[k]];
+                        }
+                    }
+                };
+                fetch(0);
                 for (int32_t i = 0; i < it.n0; ++i, ++b) {
                     const uint32_t st = b % ST, ph = (b / ST) & 1u;
-                    const int32_t tok0 = (it.j0 + i) * tpt, rows = min(tpt, it.lq - tok0) * a.group;
+                    const int32_t rows = min(tpt, it.lq - (it.j0 + i) * tpt) * a.group;
                     float l[4], d[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int r = lane + 32 * k;
-                        l[k] = d[k] = 0.0f;
-                        if (r < rows) {
-                            const int64_t at =
-                                static_cast<int64_t>(it.kh * a.group + r % a.group) * a.tq + it.q0 + tok0 + r / a.group;
-                            l[k] = a.lse[at];
-                            d[k] = a.delta[at];
-                        }
+                        l[k] = nl[k];
+                        d[k] = nd[k];
                     }
+                    fetch(i + 1);
                     if (!warp_wait_bounded(t_empty(st), ph ^ 1u, abort_flag, a.status, kSiteTmaEmpty)) return false;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {

@@ -188,8 +188,35 @@ AttnPlan attn_plan(const mdcn_attention_attrs& at, const mdcn_attention_dims& d,
     return p;
 }
 
-size_t attn_bwd_bytes(const mdcn_attention_dims& d) {
-    return align256(mdcn::kAttnHeaderBytes + static_cast<size_t>(d.q_tokens) * static_cast<size_t>(d.q_heads) * 4);
+// The backward's plan: where delta lies, and in float32 between how many blocks
+// the rows that see a key tile are shared out (the row tiles' own blocks run
+// beside them): as many as fill the SMs twice, each with two row tiles at least.
+struct AttnBwdPlan {
+    int64_t tiles, kv_splits;
+    size_t off_kv, bytes;
+};
+
+AttnBwdPlan attn_bwd_plan(const mdcn_attention_dims& d, mdcn_dtype dtype) {
+    constexpr int64_t kSms = 152, kMaxSplits = 16;
+    AttnBwdPlan p{};
+    const int64_t tokens = mdcn::kAttnSimtRows / (d.q_heads / d.k_heads);
+    p.tiles = mdcn::attn_tiles(d.q_tokens, d.batch, tokens);
+    p.kv_splits = 1;
+    size_t off = align256(mdcn::kAttnHeaderBytes + static_cast<size_t>(d.q_tokens) * static_cast<size_t>(d.q_heads) * 4);
+    const int64_t kv = mdcn::attn_tiles(d.k_tokens, d.batch, 64) * d.k_heads;
+    if (dtype == MDCN_F32 && kv > 0) {
+        int64_t s = 2 * kSms / kv;
+        const int64_t row_tiles = (d.q_tokens / d.batch + tokens - 1) / tokens;
+        if (s > row_tiles / 2) s = row_tiles / 2;
+        p.kv_splits = s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s;
+        if (p.kv_splits > 1) {
+            p.off_kv = off;
+            off = align256(off + static_cast<size_t>(p.kv_splits) * 2 * static_cast<size_t>(d.k_tokens) *
+                                     static_cast<size_t>(d.k_heads) * static_cast<size_t>(d.head_dim) * 4);
+        }
+    }
+    p.bytes = off;
+    return p;
 }
 
 mdcn::AttnTensor atensor(const void* p, const mdcn_strides& s, int64_t tokens, int64_t heads) {
@@ -386,7 +413,7 @@ mdcn_status mdcn_attention_backward_workspace_size(const mdcn_attention_attrs* a
     if (!bytes) return MDCN_ERR_NULL;
     const mdcn_status s = attn_check(attrs, dims, dtype, true);
     if (s != MDCN_OK) return s;
-    *bytes = attn_bwd_bytes(*dims);
+    *bytes = attn_bwd_plan(*dims, dtype).bytes;
     return MDCN_OK;
 }
 
@@ -408,11 +435,11 @@ mdcn_status mdcn_attention_backward(const mdcn_attention_attrs* attrs, const mdc
                         workspace};
     for (const void* p : al)
         if (!aligned16(p)) return MDCN_ERR_ALIGN;
-    const int64_t tiles = mdcn::attn_tiles(dims->q_tokens, dims->batch,
-                                           mdcn::kAttnSimtRows / (dims->q_heads / dims->k_heads));
-    if (tiles > kI31 / dims->k_heads || mdcn::attn_tiles(dims->k_tokens, dims->batch, 64) > kI31 / dims->k_heads)
+    const AttnBwdPlan p = attn_bwd_plan(*dims, dtype);
+    if (p.tiles > kI31 / dims->k_heads ||
+        mdcn::attn_tiles(dims->k_tokens, dims->batch, 64) + p.tiles > kI31 / dims->k_heads / p.kv_splits)
         return MDCN_ERR_UNSUPPORTED;
-    if (workspace_bytes < attn_bwd_bytes(*dims)) return MDCN_ERR_WORKSPACE;
+    if (workspace_bytes < p.bytes) return MDCN_ERR_WORKSPACE;
     s = mdcn::api_check_device(nullptr);
     if (s != MDCN_OK) return s;
     mdcn::AttnArgs a = attn_args(*attrs, *dims, q, k, v, out, lse, q_starts, k_starts, k_lengths_or_null);
@@ -424,7 +451,9 @@ mdcn_status mdcn_attention_backward(const mdcn_attention_attrs* attrs, const mdc
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     a.status = reinterpret_cast<uint32_t*>(ws);
     a.delta = reinterpret_cast<float*>(ws + mdcn::kAttnHeaderBytes);
-    a.tiles = static_cast<int32_t>(tiles);
+    a.tiles = static_cast<int32_t>(p.tiles);
+    a.kv_splits = static_cast<int32_t>(p.kv_splits);
+    if (p.kv_splits > 1) a.part_kv = reinterpret_cast<float*>(ws + p.off_kv);
     cudaError_t e = mdcn::launch_attention_delta(dtype, a, st);
     if (e == cudaSuccess)
         e = dtype == MDCN_F32 ? mdcn::launch_attention_simt_backward(a, st)

@@ -1,17 +1,21 @@
-// Attention over packed sequences on the CUDA cores (fp32 products), and the
-// small kernels that both forms of the attention use.
+// Attention over packed sequences in float32, on the CUDA cores, and the small
+// kernels that both forms of the attention use.
 //
 // Forward, per row: running maximum m and sum l of exp(scale q.k - m) over
 // 64-key tiles, accumulator rescaled by exp(m_old - m) when m grows; out =
 // acc / l, lse = m + log l. Backward from lse: p = exp(scale q.k - lse), ds =
-// p (g.v - delta) scale; one kernel sums ds k over the keys of 64 rows, the
-// other p^T g and ds^T q over the rows that see 64 keys.
+// p (g.v - delta) scale; some blocks sum ds k over the keys of 64 rows, the
+// others p^T g and ds^T q over the rows that see 64 keys, in one launch.
 //
 // Bound by fp32 multiply-adds. 256 threads hold a 64 x 64 score tile as 4 x 4
 // each and a 64 x D accumulator as 4 rows x 4-element pieces; operands come
 // from shared memory as 16-byte vectors (rows padded by 4 words, so that the
 // 16 rows a warp reads at once fall into different banks), 64 multiply-adds
-// for 8 vectors.
+// for 8 vectors. Tiles are copied to shared memory asynchronously, each as
+// soon as the one before it has been used, and two blocks share an SM where
+// their tiles fit, so that one computes while the other waits. Tensor cores
+// would need three products of reduced precision for one of fp32 (or six
+// with 16-bit parts), each with its own copy of the operands.
 #include <cfloat>
 #include <cstdint>
 
@@ -36,37 +40,51 @@ __device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
     return fmaf(a.w, b.w, c);
 }
 
+// 16 bytes to shared memory, asynchronously; zeros where `there` is false.
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "r"(there ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the latest n groups of this thread's copies have arrived.
+template <int n>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+}
+
 // Rows of a packed row tile into shared memory: row r = (token r / group, head
-// r % group) of key head kh, zero past the sequence's end.
-template <typename T>
+// r % group) of key head kh, zero past the sequence's end. One group of copies.
 __device__ __forceinline__ void load_rows(float* dst, int pitch, const AttnTensor& t, const AttnArgs& a,
                                           const AttnSeq& s, int32_t tok0, int32_t ntok, int kh) {
     const int v4 = a.D / 4, rows = ntok * a.group;
     for (int i = threadIdx.x; i < kR * v4; i += kT) {
         const int r = i / v4, c = (i - r * v4) * 4;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < rows) {
-            const int tk = r / a.group, h = kh * a.group + (r - tk * a.group);
-            x = attn_load4(static_cast<const T*>(t.p) + static_cast<int64_t>(s.q0 + tok0 + tk) * t.st +
-                           static_cast<int64_t>(h) * t.sh + c);
-        }
-        *reinterpret_cast<float4*>(dst + r * pitch + c) = x;
+        const bool there = r < rows;
+        const int tk = there ? r / a.group : 0, h = kh * a.group + (there ? r - tk * a.group : 0);
+        copy16(dst + r * pitch + c,
+               static_cast<const float*>(t.p) + static_cast<int64_t>(s.q0 + tok0 + tk) * t.st +
+                   static_cast<int64_t>(h) * t.sh + c,
+               there);
     }
+    copies_end();
 }
 
-// Keys (or values) [j0, j0 + 64) of the sequence, zero past its last key.
-template <typename T>
+// Keys (or values) [j0, j0 + 64) of the sequence, zero past its last key. One
+// group of copies.
 __device__ __forceinline__ void load_keys(float* dst, int pitch, const AttnTensor& t, const AttnArgs& a,
                                           const AttnSeq& s, int32_t j0, int kh) {
     const int v4 = a.D / 4;
     for (int i = threadIdx.x; i < kC * v4; i += kT) {
         const int r = i / v4, c = (i - r * v4) * 4;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (j0 + r < s.lk)
-            x = attn_load4(static_cast<const T*>(t.p) + static_cast<int64_t>(s.k0 + j0 + r) * t.st +
-                           static_cast<int64_t>(kh) * t.sh + c);
-        *reinterpret_cast<float4*>(dst + r * pitch + c) = x;
+        const bool there = j0 + r < s.lk;
+        copy16(dst + r * pitch + c,
+               static_cast<const float*>(t.p) + static_cast<int64_t>(there ? s.k0 + j0 + r : 0) * t.st +
+                   static_cast<int64_t>(kh) * t.sh + c,
+               there);
     }
+    copies_end();
 }
 
 // acc[i][j] = row (ty + 16 i) of x . row (tx + 16 j) of y
@@ -129,8 +147,7 @@ __device__ __forceinline__ float sum16(float v) {
 
 // Grid: (tiles * splits, key heads). Block x takes tile x / splits and the
 // (x % splits)-th share of the key tiles that the tile's rows see.
-template <typename T>
-__global__ void __launch_bounds__(kT) attn_forward_simt_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kT, 2) attn_forward_simt_kernel(const __grid_constant__ AttnArgs a) {
     extern __shared__ float sm[];
     if (a.status && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.status = 0;
     const int tpt = kR / a.group;
@@ -139,11 +156,16 @@ __global__ void __launch_bounds__(kT) attn_forward_simt_kernel(const __grid_cons
     const int kh = blockIdx.y, split = blockIdx.x % a.splits;
     const int pitch = a.D + 4;
     float* qs = sm;
-    float* ks = qs + kR * pitch;  // keys, then values
-    float* ps = ks + kC * pitch;
+    float* ks = qs + kR * pitch;
+    float* vs = ks + kC * pitch;
+    float* ps = vs + kC * pitch;
     const int32_t tok0 = s.tile * tpt, ntok = min(tpt, s.lq - tok0);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    load_rows<T>(qs, pitch, a.q, a, s, tok0, ntok, kh);
+    const int32_t most = attn_seen(a, s, tok0 + ntok - 1);
+    const int32_t ktiles = (most + kC - 1) / kC, per = (ktiles + a.splits - 1) / a.splits;
+    const int32_t t0 = min(split * per, ktiles), t1 = min(t0 + per, ktiles);
+    load_rows(qs, pitch, a.q, a, s, tok0, ntok, kh);
+    if (t0 < t1) load_keys(ks, pitch, a.k, a, s, t0 * kC, kh);
 
     int32_t seen[4];
     float m[4], l[4];
@@ -157,16 +179,18 @@ __global__ void __launch_bounds__(kT) attn_forward_simt_kernel(const __grid_cons
 #pragma unroll
         for (int c = 0; c < kAcc; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    const int32_t most = attn_seen(a, s, tok0 + ntok - 1);
-    const int32_t ktiles = (most + kC - 1) / kC, per = (ktiles + a.splits - 1) / a.splits;
-    const int32_t t0 = min(split * per, ktiles), t1 = min(t0 + per, ktiles);
     const float to_log2 = a.scale * kLog2e;
     for (int32_t t = t0; t < t1; ++t) {
-        __syncthreads();
-        load_keys<T>(ks, pitch, a.k, a, s, t * kC, kh);
+        load_keys(vs, pitch, a.v, a, s, t * kC, kh);
+        copies_wait<1>();  // the keys
         __syncthreads();
         float x[4][4];
         products(x, qs, ks, pitch, a.D, tx, ty);
+        __syncthreads();
+        if (t + 1 < t1)
+            load_keys(ks, pitch, a.k, a, s, (t + 1) * kC, kh);
+        else
+            copies_end();
         float corr[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -196,11 +220,12 @@ __global__ void __launch_bounds__(kT) attn_forward_simt_kernel(const __grid_cons
                 o[i][c].w *= corr[i];
             }
         }
+        copies_wait<1>();  // the values
         __syncthreads();
-        load_keys<T>(ks, pitch, a.v, a, s, t * kC, kh);
+        accumulate(o, ps, vs, pitch, a.D, tx, ty);
         __syncthreads();
-        accumulate(o, ps, ks, pitch, a.D, tx, ty);
     }
+    copies_wait<0>();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = ty + 16 * i;
@@ -217,7 +242,7 @@ __global__ void __launch_bounds__(kT) attn_forward_simt_kernel(const __grid_cons
             if (a.splits > 1)
                 *reinterpret_cast<float4*>(a.part_out + ((static_cast<int64_t>(split) * a.tq + tok) * a.hq + h) * a.D + d) = v;
             else
-                attn_store4(static_cast<T*>(a.out.p) + tok * a.out.st + h * a.out.sh + d, v);
+                *reinterpret_cast<float4*>(static_cast<float*>(a.out.p) + tok * a.out.st + h * a.out.sh + d) = v;
         }
         if (tx == 0) {
             if (a.splits > 1)
@@ -228,14 +253,12 @@ __global__ void __launch_bounds__(kT) attn_forward_simt_kernel(const __grid_cons
     }
 }
 
-// grad_q of one row tile. Grid: (tiles, key heads).
-template <typename T>
-__global__ void __launch_bounds__(kT) attn_grad_q_simt_kernel(const __grid_constant__ AttnArgs a) {
-    extern __shared__ float sm[];
+// grad_q of one row tile.
+__device__ __forceinline__ void grad_q_block(const AttnArgs& a, float* sm, int32_t index, int kh) {
     const int tpt = kR / a.group;
-    const AttnSeq s = attn_find(a, false, tpt, blockIdx.x);
+    const AttnSeq s = attn_find(a, false, tpt, index);
     if (s.tile < 0) return;
-    const int kh = blockIdx.y, pitch = a.D + 4;
+    const int pitch = a.D + 4;
     float* qs = sm;
     float* gs = qs + kR * pitch;
     float* ks = gs + kR * pitch;
@@ -243,8 +266,13 @@ __global__ void __launch_bounds__(kT) attn_grad_q_simt_kernel(const __grid_const
     float* ps = vs + kC * pitch;
     const int32_t tok0 = s.tile * tpt, ntok = min(tpt, s.lq - tok0);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    load_rows<T>(qs, pitch, a.q, a, s, tok0, ntok, kh);
-    load_rows<T>(gs, pitch, a.g, a, s, tok0, ntok, kh);
+    const int32_t ktiles = (attn_seen(a, s, tok0 + ntok - 1) + kC - 1) / kC;
+    load_rows(qs, pitch, a.q, a, s, tok0, ntok, kh);
+    load_rows(gs, pitch, a.g, a, s, tok0, ntok, kh);
+    if (ktiles > 0) {
+        load_keys(ks, pitch, a.k, a, s, 0, kh);
+        load_keys(vs, pitch, a.v, a, s, 0, kh);
+    }
     int32_t seen[4];
     float lse[4], delta[4];
     float4 o[4][kAcc];
@@ -259,26 +287,32 @@ __global__ void __launch_bounds__(kT) attn_grad_q_simt_kernel(const __grid_const
 #pragma unroll
         for (int c = 0; c < kAcc; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    const int32_t ktiles = (attn_seen(a, s, tok0 + ntok - 1) + kC - 1) / kC;
     for (int32_t t = 0; t < ktiles; ++t) {
-        __syncthreads();
-        load_keys<T>(ks, pitch, a.k, a, s, t * kC, kh);
-        load_keys<T>(vs, pitch, a.v, a, s, t * kC, kh);
+        copies_wait<1>();  // the keys
         __syncthreads();
         float x[4][4], dp[4][4];
         products(x, qs, ks, pitch, a.D, tx, ty);
+        copies_wait<0>();  // the values
+        __syncthreads();
         products(dp, gs, vs, pitch, a.D, tx, ty);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const bool on = t * kC + tx + 16 * j < seen[i];
+                // s - lse is rounded once, before the small difference is scaled
                 const float p = on ? exp2f(fmaf(x[i][j], a.scale, -lse[i]) * kLog2e) : 0.0f;
                 ps[(ty + 16 * i) * kPP + tx + 16 * j] = on ? p * (dp[i][j] - delta[i]) : 0.0f;
             }
         __syncthreads();
         accumulate(o, ps, ks, pitch, a.D, tx, ty);
+        __syncthreads();
+        if (t + 1 < ktiles) {
+            load_keys(ks, pitch, a.k, a, s, (t + 1) * kC, kh);
+            load_keys(vs, pitch, a.v, a, s, (t + 1) * kC, kh);
+        }
     }
+    copies_wait<0>();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = ty + 16 * i;
@@ -289,8 +323,8 @@ __global__ void __launch_bounds__(kT) attn_grad_q_simt_kernel(const __grid_const
         for (int c = 0; c < kAcc; ++c) {
             const int d = tx * 4 + 64 * c;
             if (d < a.D)
-                attn_store4(static_cast<T*>(a.gq.p) + tok * a.gq.st + h * a.gq.sh + d,
-                            make_float4(o[i][c].x * a.scale, o[i][c].y * a.scale, o[i][c].z * a.scale, o[i][c].w * a.scale));
+                *reinterpret_cast<float4*>(static_cast<float*>(a.gq.p) + tok * a.gq.st + h * a.gq.sh + d) =
+                    make_float4(o[i][c].x * a.scale, o[i][c].y * a.scale, o[i][c].z * a.scale, o[i][c].w * a.scale);
         }
     }
 }
@@ -298,7 +332,7 @@ __global__ void __launch_bounds__(kT) attn_grad_q_simt_kernel(const __grid_const
 // o[i] (row 4 ty + i) += sum over the 64 rows r of p[r][row] * y[r]
 __device__ __forceinline__ void accumulate_t(float4 (&o)[4][kAcc], const float* p, const float* y, int pitch, int D,
                                              int tx, int ty) {
-#pragma unroll 2
+#pragma unroll 4
     for (int r = 0; r < kR; ++r) {
         const float4 w = *reinterpret_cast<const float4*>(p + r * kPP + ty * 4);
         const float f[4] = {w.x, w.y, w.z, w.w};
@@ -318,59 +352,82 @@ __device__ __forceinline__ void accumulate_t(float4 (&o)[4][kAcc], const float* 
     }
 }
 
-// grad_k and grad_v of 64 keys of one key head. Grid: (key tiles, key heads).
-template <typename T>
-__global__ void __launch_bounds__(kT) attn_grad_kv_simt_kernel(const __grid_constant__ AttnArgs a) {
-    extern __shared__ float sm[];
-    const AttnSeq s = attn_find(a, true, kC, blockIdx.x);
+// grad_k and grad_v of 64 keys of one key head, or (a.kv_splits > 1) the sums
+// over a share of the row tiles that see them. P, then dS, in one buffer.
+__device__ __forceinline__ void grad_kv_block(const AttnArgs& a, float* sm, int32_t index, int32_t split, int kh) {
+    const AttnSeq s = attn_find(a, true, kC, index);
     if (s.tile < 0) return;
-    const int kh = blockIdx.y, pitch = a.D + 4, tpt = kR / a.group;
+    const int pitch = a.D + 4, tpt = kR / a.group;
     float* qs = sm;
     float* gs = qs + kR * pitch;
     float* ks = gs + kR * pitch;
     float* vs = ks + kC * pitch;
     float* ps = vs + kC * pitch;
-    float* ds = ps + kR * kPP;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int32_t j0 = s.tile * kC;
-    load_keys<T>(ks, pitch, a.k, a, s, j0, kh);
-    load_keys<T>(vs, pitch, a.v, a, s, j0, kh);
     float4 ok[4][kAcc], ov[4][kAcc];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int c = 0; c < kAcc; ++c) ok[i][c] = ov[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-    // the first query that sees key j0
-    const int32_t first = j0 >= s.lk ? s.lq : (a.causal ? max(0, j0 + s.lq - s.lk) : 0);
-    for (int32_t tok0 = first / tpt * tpt; tok0 < s.lq; tok0 += tpt) {
-        const int32_t ntok = min(tpt, s.lq - tok0);
-        __syncthreads();
-        load_rows<T>(qs, pitch, a.q, a, s, tok0, ntok, kh);
-        load_rows<T>(gs, pitch, a.g, a, s, tok0, ntok, kh);
-        __syncthreads();
-        float x[4][4], dp[4][4];
-        products(x, qs, ks, pitch, a.D, tx, ty);
-        products(dp, gs, vs, pitch, a.D, tx, ty);
+    // row tiles from the first that sees key j0
+    const int32_t first = a.causal ? max(0, j0 + s.lq - s.lk) / tpt : 0;
+    const int32_t tiles = j0 < s.lk ? max(0, (s.lq + tpt - 1) / tpt - first) : 0;
+    const int32_t per = (tiles + a.kv_splits - 1) / a.kv_splits;
+    const int32_t b0 = first + min(split * per, tiles), b1 = first + min(split * per + per, tiles);
+    if (b0 < b1) {
+        load_keys(ks, pitch, a.k, a, s, j0, kh);
+        load_keys(vs, pitch, a.v, a, s, j0, kh);
+        load_rows(qs, pitch, a.q, a, s, b0 * tpt, min(tpt, s.lq - b0 * tpt), kh);
+        load_rows(gs, pitch, a.g, a, s, b0 * tpt, min(tpt, s.lq - b0 * tpt), kh);
+    }
+    for (int32_t b = b0; b < b1; ++b) {
+        const int32_t tok0 = b * tpt, ntok = min(tpt, s.lq - tok0);
+        float lse[4], delta[4];
+        int32_t seen[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = ty + 16 * i;
             const bool live = r < ntok * a.group;
             const int64_t at =
                 live ? static_cast<int64_t>(kh * a.group + r % a.group) * a.tq + s.q0 + tok0 + r / a.group : 0;
-            const int32_t seen = live ? attn_seen(a, s, tok0 + r / a.group) : 0;
-            const float lse = live ? a.lse[at] : 0.0f, delta = live ? a.delta[at] : 0.0f;
+            seen[i] = live ? attn_seen(a, s, tok0 + r / a.group) : 0;
+            lse[i] = live ? a.lse[at] : 0.0f;
+            delta[i] = live ? a.delta[at] : 0.0f;
+        }
+        copies_wait<1>();  // the queries
+        __syncthreads();
+        float x[4][4], dp[4][4];
+        products(x, qs, ks, pitch, a.D, tx, ty);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const bool on = j0 + tx + 16 * j < seen;
-                const float p = on ? exp2f(fmaf(x[i][j], a.scale, -lse) * kLog2e) : 0.0f;  // one rounding before the small difference is scaled
-                ps[r * kPP + tx + 16 * j] = p;
-                ds[r * kPP + tx + 16 * j] = on ? p * (dp[i][j] - delta) : 0.0f;
+                const bool on = j0 + tx + 16 * j < seen[i];
+                x[i][j] = on ? exp2f(fmaf(x[i][j], a.scale, -lse[i]) * kLog2e) : 0.0f;
+                ps[(ty + 16 * i) * kPP + tx + 16 * j] = x[i][j];
             }
-        }
+        copies_wait<0>();  // the gradients
         __syncthreads();
+        products(dp, gs, vs, pitch, a.D, tx, ty);
         accumulate_t(ov, ps, gs, pitch, a.D, tx, ty);
-        accumulate_t(ok, ds, qs, pitch, a.D, tx, ty);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool on = j0 + tx + 16 * j < seen[i];
+                ps[(ty + 16 * i) * kPP + tx + 16 * j] = on ? x[i][j] * (dp[i][j] - delta[i]) : 0.0f;
+            }
+        __syncthreads();
+        accumulate_t(ok, ps, qs, pitch, a.D, tx, ty);
+        __syncthreads();
+        if (b + 1 < b1) {
+            load_rows(qs, pitch, a.q, a, s, tok0 + tpt, min(tpt, s.lq - tok0 - tpt), kh);
+            load_rows(gs, pitch, a.g, a, s, tok0 + tpt, min(tpt, s.lq - tok0 - tpt), kh);
+        }
     }
+    copies_wait<0>();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int32_t j = j0 + ty * 4 + i;
@@ -380,11 +437,56 @@ __global__ void __launch_bounds__(kT) attn_grad_kv_simt_kernel(const __grid_cons
         for (int c = 0; c < kAcc; ++c) {
             const int d = tx * 4 + 64 * c;
             if (d >= a.D) continue;
-            attn_store4(static_cast<T*>(a.gv.p) + row * a.gv.st + kh * a.gv.sh + d, ov[i][c]);
-            attn_store4(static_cast<T*>(a.gk.p) + row * a.gk.st + kh * a.gk.sh + d,
-                        make_float4(ok[i][c].x * a.scale, ok[i][c].y * a.scale, ok[i][c].z * a.scale, ok[i][c].w * a.scale));
+            const float4 k = make_float4(ok[i][c].x * a.scale, ok[i][c].y * a.scale, ok[i][c].z * a.scale, ok[i][c].w * a.scale);
+            if (a.kv_splits > 1) {
+                float* at = a.part_kv + ((static_cast<int64_t>(split) * 2 * a.tk + row) * a.hk + kh) * a.D + d;
+                *reinterpret_cast<float4*>(at) = k;
+                *reinterpret_cast<float4*>(at + static_cast<int64_t>(a.tk) * a.hk * a.D) = ov[i][c];
+            } else {
+                *reinterpret_cast<float4*>(static_cast<float*>(a.gk.p) + row * a.gk.st + kh * a.gk.sh + d) = k;
+                *reinterpret_cast<float4*>(static_cast<float*>(a.gv.p) + row * a.gv.st + kh * a.gv.sh + d) = ov[i][c];
+            }
         }
     }
+}
+
+// Grid: (key tiles * kv_splits + row tiles, key heads): the longer blocks first.
+__global__ void __launch_bounds__(kT) attn_backward_simt_kernel(const __grid_constant__ AttnArgs a, int32_t kv_blocks) {
+    extern __shared__ float sm[];
+    const int32_t b = blockIdx.x;
+    if (b < kv_blocks)
+        grad_kv_block(a, sm, b / a.kv_splits, b % a.kv_splits, blockIdx.y);
+    else
+        grad_q_block(a, sm, b - kv_blocks, blockIdx.y);
+}
+
+// grad_k (y 0) or grad_v (y 1): the shares' sums added in order, for the keys of a sequence.
+__global__ void __launch_bounds__(kT) attn_kv_sum_kernel(const __grid_constant__ AttnArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kT / 32) + (threadIdx.x >> 5);  // (key, head)
+    if (row >= static_cast<int64_t>(a.tk) * a.hk) return;
+    const int64_t key = row / a.hk;
+    const int kh = static_cast<int>(row - key * a.hk);
+    bool mine = false;  // keys of no sequence are not written
+    for (int b = lane; b < a.batch; b += 32) {
+        int32_t first, len;
+        attn_range(a.k_starts, b, a.tk, first, len);
+        mine = mine || (key >= first && key < first + len);
+    }
+    if (!__any_sync(0xffffffffu, mine) || lane * 4 >= a.D) return;
+    const int64_t one = static_cast<int64_t>(a.tk) * a.hk * a.D;
+    const float* p = a.part_kv + blockIdx.y * one + row * a.D + lane * 4;
+    float4 sum = *reinterpret_cast<const float4*>(p);
+    for (int i = 1; i < a.kv_splits; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(p + 2 * i * one);
+        sum.x += v.x;
+        sum.y += v.y;
+        sum.z += v.z;
+        sum.w += v.w;
+    }
+    const AttnTensor& t = blockIdx.y ? a.gv : a.gk;
+    *reinterpret_cast<float4*>(static_cast<float*>(t.p) + key * t.st + kh * t.sh + lane * 4) = sum;
 }
 
 // One warp per (token, head): out = sum over the splits of exp(lse_i - lse) out_i.
@@ -448,50 +550,10 @@ __global__ void __launch_bounds__(kT) attn_delta_kernel(const __grid_constant__ 
     if (live && sub == 0) a.delta[static_cast<int64_t>(h) * a.tq + tok] = sum;
 }
 
-template <typename F>
-cudaError_t with_smem(F kernel, int bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
-template <typename T>
-cudaError_t forward_t(const AttnArgs& a, cudaStream_t st) {
-    const int smem = (2 * kR * (a.D + 4) + kR * kPP) * 4;
-    cudaError_t e = with_smem(attn_forward_simt_kernel<T>, smem);
-    if (e != cudaSuccess) return e;
-    attn_forward_simt_kernel<T>
-        <<<dim3(static_cast<unsigned>(a.tiles) * a.splits, static_cast<unsigned>(a.hk)), kT, smem, st>>>(a);
-    return cudaGetLastError();
-}
-
-template <typename T>
-cudaError_t backward_t(const AttnArgs& a, cudaStream_t st) {
-    cudaError_t e;
-    if (a.tq > 0) {
-        const int smem = (4 * kR * (a.D + 4) + kR * kPP) * 4;
-        if ((e = with_smem(attn_grad_q_simt_kernel<T>, smem)) != cudaSuccess) return e;
-        attn_grad_q_simt_kernel<T><<<dim3(static_cast<unsigned>(a.tiles), static_cast<unsigned>(a.hk)), kT, smem, st>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    if (a.tk > 0) {
-        const int smem = (4 * kR * (a.D + 4) + 2 * kR * kPP) * 4;
-        if ((e = with_smem(attn_grad_kv_simt_kernel<T>, smem)) != cudaSuccess) return e;
-        const unsigned kt = static_cast<unsigned>(attn_tiles(a.tk, a.batch, kC));
-        attn_grad_kv_simt_kernel<T><<<dim3(kt, static_cast<unsigned>(a.hk)), kT, smem, st>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    }
-    return cudaSuccess;
-}
-
-}  // namespace
-
-cudaError_t launch_attention_simt_forward(const AttnArgs& a, cudaStream_t st) { return forward_t<float>(a, st); }
-
-cudaError_t launch_attention_simt_backward(const AttnArgs& a, cudaStream_t st) { return backward_t<float>(a, st); }
-
-template <typename F>
-static cudaError_t launch_after(F kernel, int64_t grid, const AttnArgs& a, cudaStream_t st) {
+template <typename F, typename... Args>
+cudaError_t launch_after(F kernel, dim3 grid, cudaStream_t st, Args... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(kT);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -499,15 +561,39 @@ static cudaError_t launch_after(F kernel, int64_t grid, const AttnArgs& a, cudaS
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
+}  // namespace
+
+cudaError_t launch_attention_simt_forward(const AttnArgs& a, cudaStream_t st) {
+    const int smem = (3 * kR * (a.D + 4) + kR * kPP) * 4;
+    cudaError_t e = cudaFuncSetAttribute(attn_forward_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    attn_forward_simt_kernel<<<dim3(static_cast<unsigned>(a.tiles) * a.splits, static_cast<unsigned>(a.hk)), kT, smem,
+                               st>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_attention_simt_backward(const AttnArgs& a, cudaStream_t st) {
+    const int smem = (4 * kR * (a.D + 4) + kR * kPP) * 4;
+    cudaError_t e = cudaFuncSetAttribute(attn_backward_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int32_t kv = static_cast<int32_t>(attn_tiles(a.tk, a.batch, kC)) * a.kv_splits;
+    const int32_t blocks = kv + (a.tq > 0 ? a.tiles : 0);
+    if (blocks == 0) return cudaSuccess;
+    attn_backward_simt_kernel<<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(a.hk)), kT, smem, st>>>(a, kv);
+    if ((e = cudaGetLastError()) != cudaSuccess || a.kv_splits == 1) return e;
+    const int64_t rows = static_cast<int64_t>(a.tk) * a.hk;
+    return launch_after(attn_kv_sum_kernel, dim3(static_cast<unsigned>((rows + kT / 32 - 1) / (kT / 32)), 2), st, a);
+}
+
 cudaError_t launch_attention_join(int dtype, const AttnArgs& a, cudaStream_t st) {
-    const int64_t grid = (static_cast<int64_t>(a.tq) * a.hq + kT / 32 - 1) / (kT / 32);
-    if (dtype == kF32) return launch_after(attn_join_kernel<float>, grid, a, st);
-    if (dtype == kF16) return launch_after(attn_join_kernel<__half>, grid, a, st);
-    return launch_after(attn_join_kernel<__nv_bfloat16>, grid, a, st);
+    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.tq) * a.hq + kT / 32 - 1) / (kT / 32)));
+    if (dtype == kF32) return launch_after(attn_join_kernel<float>, grid, st, a);
+    if (dtype == kF16) return launch_after(attn_join_kernel<__half>, grid, st, a);
+    return launch_after(attn_join_kernel<__nv_bfloat16>, grid, st, a);
 }
 
 cudaError_t launch_attention_delta(int dtype, const AttnArgs& a, cudaStream_t st) {

@@ -135,11 +135,14 @@ mdcn_status attn_check(const mdcn_attention_attrs* at, const mdcn_attention_dims
 
 // The forward's plan: row tiles, and between how many blocks a tile's keys are
 // shared out. Estimated in steps (one key tile of a row tile): an item of n
-// steps costs n + kItemSteps. Sequences that fill their rows: as many waves of
-// items as the SMs need, each as long as an item. Sequences of any length up to
-// their rows (k_lengths): half the steps on average, taken as they come, and
-// one item's length at the end. The join of the shares costs a launch and the
-// partial results' way to memory and back.
+// steps costs n + 2, or n + 4 where the steps wait for memory. Sequences that
+// fill their rows: as many waves of items as the SMs need, each as long as an
+// item. Sequences of any length up to their rows (k_lengths): half the steps on
+// average, taken as they come, and one item's length at the end. The join of
+// the shares costs a launch and the partial results' way to memory and back.
+// (Measured: 4 maps of 80 x 80, 2 heads of 64: 112 us with one share, 104 with
+// three; 16 new tokens against up to 8192 keys: 90 with one, 81 with four; a
+// prompt of 1024 tokens, 32 heads: 28 with one, 40 with two.)
 struct AttnPlan {
     int64_t tiles, splits;
     size_t off_out, off_lse, bytes;
@@ -147,7 +150,7 @@ struct AttnPlan {
 
 AttnPlan attn_plan(const mdcn_attention_attrs& at, const mdcn_attention_dims& d, mdcn_dtype dtype, bool lengths) {
     constexpr int64_t kSms = 152, kMaxSplits = 32;
-    constexpr double kItemSteps = 2.0, kJoinSteps = 4.0, kStepBytes = 4.0e6;
+    constexpr double kItemSteps = 2.0, kWaitingItemSteps = 4.0, kJoinSteps = 2.5, kStepBytes = 8.0e6;
     AttnPlan p{};
     const int64_t group = d.q_heads / d.k_heads;
     const bool tc = dtype != MDCN_F32;
@@ -166,7 +169,7 @@ AttnPlan attn_plan(const mdcn_attention_attrs& at, const mdcn_attention_dims& d,
         double best = 0.0;
         for (int64_t s = 1; s <= kMaxSplits && s <= steps; ++s) {
             const double item = static_cast<double>((steps + s - 1) / s);
-            double cost = lengths ? (static_cast<double>(blocks) * (static_cast<double>(steps) / 2 + kItemSteps * s)) /
+            double cost = lengths ? (static_cast<double>(blocks) * (static_cast<double>(steps) / 2 + kWaitingItemSteps * s)) /
                                             static_cast<double>(kSms) + item
                                   : static_cast<double>((blocks * s + kSms - 1) / kSms) * (item + kItemSteps);
             if (s > 1) cost += kJoinSteps + rows * static_cast<double>(s) / kStepBytes;

@@ -489,46 +489,58 @@ __global__ void __launch_bounds__(kT) attn_kv_sum_kernel(const __grid_constant__
     *reinterpret_cast<float4*>(static_cast<float*>(t.p) + key * t.st + kh * t.sh + lane * 4) = sum;
 }
 
-// One warp per (token, head): out = sum over the splits of exp(lse_i - lse) out_i.
+// out = sum over the shares of exp(lse_i - lse) out_i; 16 lanes per (token,
+// head), up to 8 elements each.
 template <typename T>
 __global__ void __launch_bounds__(kT) attn_join_kernel(const __grid_constant__ AttnArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int lane = threadIdx.x & 31;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kT / 32) + (threadIdx.x >> 5);
-    if (row >= static_cast<int64_t>(a.tq) * a.hq) return;
-    const int64_t tok = row / a.hq;
-    const int h = static_cast<int>(row - tok * a.hq);
+    const int sub = threadIdx.x & 15;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kT / 16) + (threadIdx.x >> 4);
+    const bool real = row < static_cast<int64_t>(a.tq) * a.hq;
+    const int64_t tok = real ? row / a.hq : 0;
+    const int h = real ? static_cast<int>(row - tok * a.hq) : 0;
     // rows of no sequence have no partial results and are not written
-    bool mine = false;
-    for (int b = lane; b < a.batch; b += 32) {
+    float mine = 0.0f;
+    for (int b = sub; b < a.batch; b += 16) {
         int32_t first, len;
         attn_range(a.q_starts, b, a.tq, first, len);
-        mine = mine || (tok >= first && tok < first + len);
+        if (real && tok >= first && tok < first + len) mine = 1.0f;
     }
-    if (!__any_sync(0xffffffffu, mine)) return;
+    const bool live = max16(mine) > 0.0f;
     float best = -INFINITY;
-    for (int i = lane; i < a.splits; i += 32) best = fmaxf(best, a.part_lse[(static_cast<int64_t>(i) * a.hq + h) * a.tq + tok]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) best = fmaxf(best, __shfl_xor_sync(0xffffffffu, best, o));
+    for (int i = sub; live && i < a.splits; i += 16)
+        best = fmaxf(best, a.part_lse[(static_cast<int64_t>(i) * a.hq + h) * a.tq + tok]);
+    best = max16(best);
+    if (!live) return;
     const float base = best == -INFINITY ? 0.0f : best;
+    const bool on = sub * 8 < a.D;
     float total = 0.0f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
+#pragma unroll 4
     for (int i = 0; i < a.splits; ++i) {
         const float w = expf(a.part_lse[(static_cast<int64_t>(i) * a.hq + h) * a.tq + tok] - base);
         total += w;
-        if (lane * 4 < a.D && w != 0.0f) {
-            const float4 v = *reinterpret_cast<const float4*>(a.part_out + ((static_cast<int64_t>(i) * a.tq + tok) * a.hq + h) * a.D + lane * 4);
-            acc.x = fmaf(w, v.x, acc.x);
-            acc.y = fmaf(w, v.y, acc.y);
-            acc.z = fmaf(w, v.z, acc.z);
-            acc.w = fmaf(w, v.w, acc.w);
+        if (on) {
+            const float* p = a.part_out + ((static_cast<int64_t>(i) * a.tq + tok) * a.hq + h) * a.D + sub * 8;
+            const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
+            // a share without a key holds zeros
+            u.x = fmaf(w, x.x, u.x);
+            u.y = fmaf(w, x.y, u.y);
+            u.z = fmaf(w, x.z, u.z);
+            u.w = fmaf(w, x.w, u.w);
+            v.x = fmaf(w, y.x, v.x);
+            v.y = fmaf(w, y.y, v.y);
+            v.z = fmaf(w, y.z, v.z);
+            v.w = fmaf(w, y.w, v.w);
         }
     }
     const float inv = total > 0.0f ? 1.0f / total : total;
-    if (lane * 4 < a.D)
-        attn_store4(static_cast<T*>(a.out.p) + tok * a.out.st + h * a.out.sh + lane * 4,
-                    make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-    if (lane == 0) a.lse[static_cast<int64_t>(h) * a.tq + tok] = total == 0.0f ? -INFINITY : base + logf(total);
+    if (on) {
+        T* o = static_cast<T*>(a.out.p) + tok * a.out.st + h * a.out.sh + sub * 8;
+        attn_store4(o, make_float4(u.x * inv, u.y * inv, u.z * inv, u.w * inv));
+        attn_store4(o + 4, make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv));
+    }
+    if (sub == 0) a.lse[static_cast<int64_t>(h) * a.tq + tok] = total == 0.0f ? -INFINITY : base + logf(total);
 }
 
 template <typename T>
@@ -590,7 +602,7 @@ cudaError_t launch_attention_simt_backward(const AttnArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_attention_join(int dtype, const AttnArgs& a, cudaStream_t st) {
-    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.tq) * a.hq + kT / 32 - 1) / (kT / 32)));
+    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.tq) * a.hq + kT / 16 - 1) / (kT / 16)));
     if (dtype == kF32) return launch_after(attn_join_kernel<float>, grid, st, a);
     if (dtype == kF16) return launch_after(attn_join_kernel<__half>, grid, st, a);
     return launch_after(attn_join_kernel<__nv_bfloat16>, grid, st, a);

@@ -489,12 +489,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     float v[16];
                     if (any) tmem_ld16(ocol + static_cast<uint32_t>(c), v);
                     if (!live) continue;
+                    // whole sectors: 32 bytes a store (head_dim is a multiple of 8)
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4)
-                        if (c + i < a.D)
-                            *reinterpret_cast<float4*>(po + c + i) =
-                                some ? make_float4(v[i] * inv, v[i + 1] * inv, v[i + 2] * inv, v[i + 3] * inv)
-                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int i = 0; i < 16; ++i) v[i] = some ? v[i] * inv : 0.0f;
+                    store8(po + c, v);
+                    if (c + 8 < a.D) store8(po + c + 8, v + 8);
                 }
                 if (live) a.part_lse[(static_cast<int64_t>(it.split) * a.hq + h) * a.tq + tok] = lse;
             } else {

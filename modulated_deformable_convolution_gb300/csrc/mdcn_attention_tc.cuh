@@ -96,6 +96,13 @@ __device__ __forceinline__ void store16(void* p, const float (&v)[16], int n, bo
     if (n >= 16) st_global_v4(static_cast<uint8_t*>(p) + 16, make_uint4(r[4], r[5], r[6], r[7]));
 }
 
+// 8 fp32 values to a 32-byte aligned address.
+__device__ __forceinline__ void store8(float* p, const float* v) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
+
 // ---------------------------------------------------------------- work items
 // A block works through items (a row or key tile of one key head) one after
 // the other: its own index first, then indices of blocks that have not started

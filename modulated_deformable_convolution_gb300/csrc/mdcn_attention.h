@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -45,6 +46,20 @@ inline int64_t attn_tiles(int64_t total, int64_t batch, int64_t tokens) {
 }
 
 constexpr size_t kAttnHeaderBytes = 256;  // the workspace's status word
+
+// Lets a kernel use `bytes` of dynamic shared memory: asked of the runtime the
+// first time on each device (`done`, one per kernel, holds a bit for each).
+template <typename F>
+cudaError_t attn_allow_smem(F kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 // CUDA-core kernels (float32; 64 rows x 64 keys).
 constexpr int kAttnSimtRows = 64;

@@ -159,7 +159,7 @@ AttnPlan attn_plan(const mdcn_attention_attrs& at, const mdcn_attention_dims& d,
     p.tiles = mdcn::attn_tiles(d.q_tokens, d.batch, tokens);
     p.splits = 1;
     const int64_t blocks = p.tiles * d.k_heads;
-    if (blocks > 0) {
+    if (blocks > 0 && blocks <= 4 * kSms) {  // beyond, the last wave is a small part of the whole
         const double mean = static_cast<double>(d.k_tokens) / static_cast<double>(d.batch);
         const double own = at.causal ? static_cast<double>(d.q_tokens) / static_cast<double>(d.batch) / 2 : 0.0;
         const double seen = mean > own ? mean - own : mean / 2;

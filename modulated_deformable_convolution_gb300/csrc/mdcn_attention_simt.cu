@@ -581,7 +581,8 @@ cudaError_t launch_after(F kernel, dim3 grid, cudaStream_t st, Args... args) {
 
 cudaError_t launch_attention_simt_forward(const AttnArgs& a, cudaStream_t st) {
     const int smem = (3 * kR * (a.D + 4) + kR * kPP) * 4;
-    cudaError_t e = cudaFuncSetAttribute(attn_forward_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = attn_allow_smem(attn_forward_simt_kernel, (3 * kR * 132 + kR * kPP) * 4, done);  // head_dim 128
     if (e != cudaSuccess) return e;
     attn_forward_simt_kernel<<<dim3(static_cast<unsigned>(a.tiles) * a.splits, static_cast<unsigned>(a.hk)), kT, smem,
                                st>>>(a);
@@ -590,7 +591,8 @@ cudaError_t launch_attention_simt_forward(const AttnArgs& a, cudaStream_t st) {
 
 cudaError_t launch_attention_simt_backward(const AttnArgs& a, cudaStream_t st) {
     const int smem = (4 * kR * (a.D + 4) + kR * kPP) * 4;
-    cudaError_t e = cudaFuncSetAttribute(attn_backward_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = attn_allow_smem(attn_backward_simt_kernel, (4 * kR * 132 + kR * kPP) * 4, done);  // head_dim 128
     if (e != cudaSuccess) return e;
     const int32_t kv = static_cast<int32_t>(attn_tiles(a.tk, a.batch, kC)) * a.kv_splits;
     const int32_t blocks = kv + (a.tq > 0 ? a.tiles : 0);

@@ -565,7 +565,8 @@ cudaError_t launch_forward(int dtype, const AttnArgs& a, cudaStream_t st) {
     auto kern = attn_forward_tc_kernel<kAtoms, kBf>;
     constexpr int smem = smem_of(kAtoms);
     static_assert(smem <= 227 * 1024, "shared memory");
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = attn_allow_smem(kern, smem, done);
     if (e != cudaSuccess) return e;
     kern<<<static_cast<unsigned>(a.tiles) * static_cast<unsigned>(a.splits) * static_cast<unsigned>(a.hk), kTcThreads,
            smem, st>>>(mq, mk, mv, a);

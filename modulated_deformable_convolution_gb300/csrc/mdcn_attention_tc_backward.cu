@@ -811,7 +811,8 @@ cudaError_t launch_backward(int dtype, const AttnArgs& a, cudaStream_t st) {
         auto kern = attn_grad_q_tc_kernel<kAtoms, kBf>;
         constexpr int smem = smem_q(kAtoms);
         static_assert(smem <= 227 * 1024, "shared memory");
-        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+        static std::atomic<uint64_t> done{0};
+        if ((e = attn_allow_smem(kern, smem, done)) != cudaSuccess) return e;
         const unsigned tiles = static_cast<unsigned>(attn_tiles(a.tq, a.batch, tpt));
         kern<<<tiles * hk, kTcThreads, smem, st>>>(mq, mg, mk, mv, a);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -820,7 +821,8 @@ cudaError_t launch_backward(int dtype, const AttnArgs& a, cudaStream_t st) {
         auto kern = attn_grad_kv_tc_kernel<kAtoms, kBf>;
         constexpr int smem = smem_kv(kAtoms);
         static_assert(smem <= 227 * 1024, "shared memory");
-        if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+        static std::atomic<uint64_t> done{0};
+        if ((e = attn_allow_smem(kern, smem, done)) != cudaSuccess) return e;
         const unsigned tiles = static_cast<unsigned>(attn_tiles(a.tk, a.batch, kKeys));
         kern<<<tiles * hk, kTcThreads, smem, st>>>(mq, mg, mk, mv, a);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;

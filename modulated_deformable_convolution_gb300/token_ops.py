@@ -16,6 +16,8 @@ structures, which the tests hold against each other).
 """
 from __future__ import annotations
 
+import ctypes
+import functools
 import struct
 
 import torch
@@ -36,6 +38,11 @@ _attention_dims = struct.Struct("=22q").pack
 def _new(t):
     """A new contiguous tensor like t (None: none)."""
     return None if t is None else torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+def _made(t, shape):
+    """What _view answers for a tensor that _new made."""
+    return t.data_ptr(), shape[1] * shape[2], shape[2]
 
 
 def _dtype_of(t):
@@ -90,32 +97,37 @@ def _workspace(ws, dev):
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
+@functools.lru_cache(maxsize=None)
+def _function(name):
+    from . import _check  # the package is loaded by now
+
+    return getattr(_abi.load(), name), _check
+
+
 def _call(name, dev, stream, *args):
     """The C function on device dev, with the stream (default: the current
     one) as its last argument."""
-    from . import _check
-
-    fn = getattr(_abi.load(), name)
+    fn, check = _function(name)
     if stream is None:
         stream = torch._C._cuda_getCurrentRawStream(dev)
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
     if torch.cuda.current_device() == dev:
-        status = fn(*args, int(stream))
+        status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, int(stream))
+            status = fn(*args, stream)
     if status:
-        _check(status, name)
+        check(status, name)
 
 
-def _size(name, *args):
-    import ctypes
-
-    from . import _check
-
+@functools.lru_cache(maxsize=4096)
+def _size(name, attrs, dims, dtype):
+    """A workspace size: the C function's answer for these attributes and
+    sizes, asked once."""
+    fn, check = _function(name)
     n = ctypes.c_size_t()
-    _check(getattr(_abi.load(), name)(*args, ctypes.byref(n)), name)
+    check(fn(attrs, dims, dtype, ctypes.byref(n)), name)
     return n.value
 
 
@@ -158,24 +170,30 @@ def _rotary_problem(q, k, positions, inv_freq, sections, layout, norm, q_weight,
             _flat("q_weight", q_weight, dt, (d,), dev), _flat("k_weight", k_weight, dt, (d,), dev))
 
 
-def mdcn_rotary_forward(q, k, positions, inv_freq, sections, q_out, k_out, layout="half", norm=False, q_weight=None,
-                        k_weight=None, eps=1e-6, stream=None) -> None:
-    """mdcn_rotary_forward on torch tensors; k and k_out may be None."""
+def _rotary_forward(q, k, positions, inv_freq, sections, q_out, k_out, layout, norm, q_weight, k_weight, eps, stream,
+                    made):
     dt, dev, attrs, sizes, pos, freq, qw, kw = _rotary_problem(q, k, positions, inv_freq, sections, layout, norm,
                                                                q_weight, k_weight, eps)
     if (k is None) != (k_out is None):
         raise ValueError("k_out is given exactly when k is")
     shape = q.shape
     qp, q0, q1 = _view("q", q, dt, dev, shape)
-    yp, y0, y1 = _view("q_out", q_out, dt, dev, shape)
+    yp, y0, y1 = _made(q_out, shape) if made else _view("q_out", q_out, dt, dev, shape)
     kp, k0, k1, zp, z0, z1 = None, 0, 0, None, 0, 0
     if k is not None:
         shape = k.shape
         kp, k0, k1 = _view("k", k, dt, dev, shape)
-        zp, z0, z1 = _view("k_out", k_out, dt, dev, shape)
+        zp, z0, z1 = _made(k_out, shape) if made else _view("k_out", k_out, dt, dev, shape)
     _call("mdcn_rotary_forward", dev, stream, attrs,
           _rotary_dims(*sizes, q0, q1, k0, k1, y0, y1, z0, z1, 0, 0, 0, 0), _dtype_of(q), qp, kp, pos, freq, qw, kw,
           yp, zp)
+
+
+def mdcn_rotary_forward(q, k, positions, inv_freq, sections, q_out, k_out, layout="half", norm=False, q_weight=None,
+                        k_weight=None, eps=1e-6, stream=None) -> None:
+    """mdcn_rotary_forward on torch tensors; k and k_out may be None."""
+    _rotary_forward(q, k, positions, inv_freq, sections, q_out, k_out, layout, norm, q_weight, k_weight, eps, stream,
+                    False)
 
 
 def rotary(q, k, positions, inv_freq, sections, layout="half", norm=False, q_weight=None, k_weight=None, eps=1e-6,
@@ -184,11 +202,13 @@ def rotary(q, k, positions, inv_freq, sections, layout="half", norm=False, q_wei
     normed per head (``norm``) and rotated by the int32 positions [tokens,
     axes]: axis a turns sections[a] pairs of elements, with the float32
     frequencies inv_freq. Returns (q_out, k_out), which may be q and k."""
+    made = q_out is None and k_out is None
     if q_out is None:
         q_out = _new(q)
-    if k_out is None and k is not None:
+    if k_out is None:
         k_out = _new(k)
-    mdcn_rotary_forward(q, k, positions, inv_freq, sections, q_out, k_out, layout, norm, q_weight, k_weight, eps)
+    _rotary_forward(q, k, positions, inv_freq, sections, q_out, k_out, layout, norm, q_weight, k_weight, eps, None,
+                    made)
     return q_out, k_out
 
 
@@ -331,9 +351,11 @@ def attention(q, k, v, q_starts, k_starts, k_lengths=None, causal=False, scale=N
     shape = p.q_shape
     if out is None:
         out = _new(q)
+        o = _made(out, shape)
+    else:
+        o = p.like_q("out", out)
     if lse is None:
         lse = torch.empty((shape[1], shape[0]), dtype=torch.float32, device=q.device)
-    o = p.like_q("out", out)
     dims = p.dims(o)
     need = _size("mdcn_attention_workspace_size", p.attrs, dims, p.code)
     if workspace is None or workspace.numel() * workspace.element_size() < need:

@@ -1,4 +1,5 @@
-"""Builds libmdcn.so in-tree with nvcc for sm_103a (no cmake).
+"""Builds libmdcn.so in-tree with nvcc for sm_103a (no cmake), and beside it
+_token_binding.so, the binding of the operators on tokens, with g++.
 
     python -m modulated_deformable_convolution_gb300.build [--force]
 
@@ -21,6 +22,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmdcn.so")
+BINDING_SOURCE = os.path.join(CSRC, "mdcn_token_binding.cpp")
+BINDING = os.path.join(HERE, "_token_binding.so")
 
 CU_SOURCES = ["mdcn_fused.cu", "mdcn_prep.cu", "mdcn_im2col.cu", "mdcn_noalloc.cu", "mdcn_backward.cu", "mdcn_gemm.cu",
               "mdcn_direct.cu", "mdcn_rotary.cu", "mdcn_attention_simt.cu",
@@ -65,6 +68,25 @@ def _compile(cmd, log_path=None):
     return r.stdout + r.stderr
 
 
+def _binding_command(home: str, out: str):
+    """g++ command of the binding that reads torch tensors in C++, and the
+    file whose age says which torch it was built against."""
+    import sysconfig
+
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           os.path.join(home, "include"), sysconfig.get_paths()["include"], INCLUDE]
+    lib = os.path.join(base, "lib")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+    for p in inc:
+        cmd += ["-isystem" if p != INCLUDE else "-I", p]
+    cmd += [BINDING_SOURCE, "-o", out, f"-L{lib}", f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch",
+            "-ltorch_python"]
+    return cmd, os.path.join(base, "version.py")
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     home = cuda_home()
     nvcc = os.path.join(home, "bin", "nvcc")
@@ -87,6 +109,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if force or _stale(o, s, headers):
             cmd = [nvcc, *ARCH, *common, "-x", "c++", "-c", s, "-o", o]
             jobs.append((cmd, None))
+    tmp_binding = BINDING + f".tmp{os.getpid()}"
+    command, torch_version = _binding_command(home, tmp_binding)
+    bind = force or _stale(BINDING, BINDING_SOURCE, [os.path.join(INCLUDE, "mdcn.h"), torch_version])
+    if bind:
+        jobs.append((command, None))
     if jobs:
         with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
             futs = [ex.submit(_compile, c, l) for c, l in jobs]
@@ -99,6 +126,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 p = os.path.join(BUILD, src + ".ptxas.log")
                 if os.path.exists(p):
                     f.write(open(p).read())
+    if bind:
+        os.replace(tmp_binding, BINDING)
     if force or jobs or not os.path.exists(LIB) or any(os.path.getmtime(o) > os.path.getmtime(LIB) for o in objs):
         tmp = LIB + f".tmp{os.getpid()}"
         lib64 = os.path.join(home, "lib64")

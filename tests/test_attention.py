@@ -398,18 +398,6 @@ def test_refuses_attrs_pointers_and_workspace(lib):
         assert back(q, n.value) == _abi.MDCN_ERR_ALIGN, i
 
 
-def test_packed_structs_are_those_of_the_header():
-    """The bytes the binding packs, read back through the ctypes structures."""
-    from modulated_deformable_convolution_gb300 import token_ops
-
-    flat = lambda s: [x for n, _ in s._fields_ for x in ([getattr(s, n).token, getattr(s, n).head] if isinstance(getattr(s, n), _abi.mdcn_strides) else list(getattr(s, n)) if n == "sections" else [getattr(s, n)])]  # noqa: E731
-    for pack, cls, values in ((token_ops._rotary_dims, _abi.mdcn_rotary_dims, range(21)), (token_ops._attention_dims, _abi.mdcn_attention_dims, range(22)),
-                              (token_ops._rotary_attrs, _abi.mdcn_rotary_attrs, (1, 2, 0.5)), (token_ops._attention_attrs, _abi.mdcn_attention_attrs, (1, 0.5))):
-        raw = pack(*values)
-        assert len(raw) == ctypes.sizeof(cls)
-        assert flat(cls.from_buffer_copy(raw)) == list(values)
-
-
 def test_binding_refuses(lib):
     q = torch.zeros(4, 2, 64)
     s = mdcn.sequence_starts([4], "cpu")

@@ -20,6 +20,7 @@
 #include <cstdint>
 
 #include "mdcn_attention.cuh"
+#include "mdcn_pdl.h"
 #include "mdcn_plan.h"
 
 namespace mdcn {
@@ -149,6 +150,7 @@ __device__ __forceinline__ float sum16(float v) {
 // (x % splits)-th share of the key tiles that the tile's rows see.
 __global__ void __launch_bounds__(kT, 2) attn_forward_simt_kernel(const __grid_constant__ AttnArgs a) {
     extern __shared__ float sm[];
+    dependency_wait();
     if (a.status && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.status = 0;
     const int tpt = kR / a.group;
     const AttnSeq s = attn_find(a, false, tpt, blockIdx.x / a.splits);
@@ -453,6 +455,7 @@ __device__ __forceinline__ void grad_kv_block(const AttnArgs& a, float* sm, int3
 // Grid: (key tiles * kv_splits + row tiles, key heads): the longer blocks first.
 __global__ void __launch_bounds__(kT) attn_backward_simt_kernel(const __grid_constant__ AttnArgs a, int32_t kv_blocks) {
     extern __shared__ float sm[];
+    dependency_wait();
     const int32_t b = blockIdx.x;
     if (b < kv_blocks)
         grad_kv_block(a, sm, b / a.kv_splits, b % a.kv_splits, blockIdx.y);
@@ -462,7 +465,7 @@ __global__ void __launch_bounds__(kT) attn_backward_simt_kernel(const __grid_con
 
 // grad_k (y 0) or grad_v (y 1): the shares' sums added in order, for the keys of a sequence.
 __global__ void __launch_bounds__(kT) attn_kv_sum_kernel(const __grid_constant__ AttnArgs a) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    dependency_wait();
     const int lane = threadIdx.x & 31;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * (kT / 32) + (threadIdx.x >> 5);  // (key, head)
     if (row >= static_cast<int64_t>(a.tk) * a.hk) return;
@@ -493,7 +496,7 @@ __global__ void __launch_bounds__(kT) attn_kv_sum_kernel(const __grid_constant__
 // head), up to 8 elements each.
 template <typename T>
 __global__ void __launch_bounds__(kT) attn_join_kernel(const __grid_constant__ AttnArgs a) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    dependency_wait();
     const int sub = threadIdx.x & 15;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * (kT / 16) + (threadIdx.x >> 4);
     const bool real = row < static_cast<int64_t>(a.tq) * a.hq;
@@ -545,6 +548,7 @@ __global__ void __launch_bounds__(kT) attn_join_kernel(const __grid_constant__ A
 
 template <typename T>
 __global__ void __launch_bounds__(kT) attn_delta_kernel(const __grid_constant__ AttnArgs a) {
+    dependency_wait();
     if (a.status && blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
     // 16 lanes to a row, up to 8 elements each
     const int sub = threadIdx.x & 15;
@@ -562,21 +566,6 @@ __global__ void __launch_bounds__(kT) attn_delta_kernel(const __grid_constant__ 
     if (live && sub == 0) a.delta[static_cast<int64_t>(h) * a.tq + tok] = sum;
 }
 
-template <typename F, typename... Args>
-cudaError_t launch_after(F kernel, dim3 grid, cudaStream_t st, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(kT);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-    return e == cudaSuccess ? cudaGetLastError() : e;
-}
-
 }  // namespace
 
 cudaError_t launch_attention_simt_forward(const AttnArgs& a, cudaStream_t st) {
@@ -584,9 +573,8 @@ cudaError_t launch_attention_simt_forward(const AttnArgs& a, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     cudaError_t e = attn_allow_smem(attn_forward_simt_kernel, (3 * kR * 132 + kR * kPP) * 4, done);  // head_dim 128
     if (e != cudaSuccess) return e;
-    attn_forward_simt_kernel<<<dim3(static_cast<unsigned>(a.tiles) * a.splits, static_cast<unsigned>(a.hk)), kT, smem,
-                               st>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(attn_forward_simt_kernel, dim3(static_cast<unsigned>(a.tiles) * a.splits, static_cast<unsigned>(a.hk)),
+                            kT, smem, st, a);
 }
 
 cudaError_t launch_attention_simt_backward(const AttnArgs& a, cudaStream_t st) {
@@ -597,29 +585,26 @@ cudaError_t launch_attention_simt_backward(const AttnArgs& a, cudaStream_t st) {
     const int32_t kv = static_cast<int32_t>(attn_tiles(a.tk, a.batch, kC)) * a.kv_splits;
     const int32_t blocks = kv + (a.tq > 0 ? a.tiles : 0);
     if (blocks == 0) return cudaSuccess;
-    attn_backward_simt_kernel<<<dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(a.hk)), kT, smem, st>>>(a, kv);
-    if ((e = cudaGetLastError()) != cudaSuccess || a.kv_splits == 1) return e;
+    e = launch_dependent(attn_backward_simt_kernel, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(a.hk)), kT, smem,
+                         st, a, kv);
+    if (e != cudaSuccess || a.kv_splits == 1) return e;
     const int64_t rows = static_cast<int64_t>(a.tk) * a.hk;
-    return launch_after(attn_kv_sum_kernel, dim3(static_cast<unsigned>((rows + kT / 32 - 1) / (kT / 32)), 2), st, a);
+    return launch_dependent(attn_kv_sum_kernel, dim3(static_cast<unsigned>((rows + kT / 32 - 1) / (kT / 32)), 2), kT, 0, st, a);
 }
 
 cudaError_t launch_attention_join(int dtype, const AttnArgs& a, cudaStream_t st) {
     const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.tq) * a.hq + kT / 16 - 1) / (kT / 16)));
-    if (dtype == kF32) return launch_after(attn_join_kernel<float>, grid, st, a);
-    if (dtype == kF16) return launch_after(attn_join_kernel<__half>, grid, st, a);
-    return launch_after(attn_join_kernel<__nv_bfloat16>, grid, st, a);
+    if (dtype == kF32) return launch_dependent(attn_join_kernel<float>, grid, kT, 0, st, a);
+    if (dtype == kF16) return launch_dependent(attn_join_kernel<__half>, grid, kT, 0, st, a);
+    return launch_dependent(attn_join_kernel<__nv_bfloat16>, grid, kT, 0, st, a);
 }
 
 cudaError_t launch_attention_delta(int dtype, const AttnArgs& a, cudaStream_t st) {
     const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(a.tq) * a.hq + kT / 16 - 1) / (kT / 16));
     if (grid == 0) return a.status ? cudaMemsetAsync(a.status, 0, sizeof(uint32_t), st) : cudaSuccess;
-    if (dtype == kF32)
-        attn_delta_kernel<float><<<grid, kT, 0, st>>>(a);
-    else if (dtype == kF16)
-        attn_delta_kernel<__half><<<grid, kT, 0, st>>>(a);
-    else
-        attn_delta_kernel<__nv_bfloat16><<<grid, kT, 0, st>>>(a);
-    return cudaGetLastError();
+    if (dtype == kF32) return launch_dependent(attn_delta_kernel<float>, grid, kT, 0, st, a);
+    if (dtype == kF16) return launch_dependent(attn_delta_kernel<__half>, grid, kT, 0, st, a);
+    return launch_dependent(attn_delta_kernel<__nv_bfloat16>, grid, kT, 0, st, a);
 }
 
 }  // namespace mdcn

@@ -27,6 +27,7 @@
 #include <type_traits>
 
 #include "mdcn_attention_tc.cuh"
+#include "mdcn_pdl.h"
 #include "mdcn_plan.h"
 
 namespace mdcn {
@@ -98,7 +99,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem_raw + slot_off + 4);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (a.status && blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
     if (warp == kWarpLoad && lane == 0) {
         for (uint32_t i = 0; i < S; ++i) {
             mbar_init(full(i), 1);
@@ -132,6 +132,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    dependency_wait();
+    if (a.status && blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
     // tensor memory: the S buffers (128 columns each, P over the first 64), O of row tile 0 and 1
     auto s_col = [&](uint32_t b) { return tmem + 128u * b; };
     auto o_col = [&](int t) { return tmem + 128u * NB + 64u * kAtoms * t; };
@@ -568,9 +570,8 @@ cudaError_t launch_forward(int dtype, const AttnArgs& a, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     cudaError_t e = attn_allow_smem(kern, smem, done);
     if (e != cudaSuccess) return e;
-    kern<<<static_cast<unsigned>(a.tiles) * static_cast<unsigned>(a.splits) * static_cast<unsigned>(a.hk), kTcThreads,
-           smem, st>>>(mq, mk, mv, a);
-    return cudaGetLastError();
+    return launch_dependent(kern, dim3(static_cast<unsigned>(a.tiles) * static_cast<unsigned>(a.splits) * static_cast<unsigned>(a.hk)),
+                            kTcThreads, smem, st, mq, mk, mv, a);
 }
 
 }  // namespace

@@ -25,6 +25,7 @@
 #include <cstdint>
 
 #include "mdcn_attention_tc.cuh"
+#include "mdcn_pdl.h"
 #include "mdcn_plan.h"
 
 namespace mdcn {
@@ -145,6 +146,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    dependency_wait();
     const uint32_t c_s = tmem, c_dp = tmem + 128u, c_ds = tmem + 256u, c_dq = tmem + 320u;
     const int tpt = kAttnTcRows / a.group;
 
@@ -466,6 +468,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    dependency_wait();
     const uint32_t c_dp = tmem + 128u * NS, c_dv = c_dp + 128u, c_dk = c_dv + 64u * kAtoms;
     auto c_s = [&](uint32_t b) { return tmem + 128u * b; };
 
@@ -814,8 +817,7 @@ cudaError_t launch_backward(int dtype, const AttnArgs& a, cudaStream_t st) {
         static std::atomic<uint64_t> done{0};
         if ((e = attn_allow_smem(kern, smem, done)) != cudaSuccess) return e;
         const unsigned tiles = static_cast<unsigned>(attn_tiles(a.tq, a.batch, tpt));
-        kern<<<tiles * hk, kTcThreads, smem, st>>>(mq, mg, mk, mv, a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = launch_dependent(kern, dim3(tiles * hk), kTcThreads, smem, st, mq, mg, mk, mv, a)) != cudaSuccess) return e;
     }
     if (a.tk > 0) {
         auto kern = attn_grad_kv_tc_kernel<kAtoms, kBf>;
@@ -824,8 +826,7 @@ cudaError_t launch_backward(int dtype, const AttnArgs& a, cudaStream_t st) {
         static std::atomic<uint64_t> done{0};
         if ((e = attn_allow_smem(kern, smem, done)) != cudaSuccess) return e;
         const unsigned tiles = static_cast<unsigned>(attn_tiles(a.tk, a.batch, kKeys));
-        kern<<<tiles * hk, kTcThreads, smem, st>>>(mq, mg, mk, mv, a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = launch_dependent(kern, dim3(tiles * hk), kTcThreads, smem, st, mq, mg, mk, mv, a)) != cudaSuccess) return e;
     }
     return cudaSuccess;
 }

@@ -29,6 +29,7 @@
 
 #include <cstdint>
 
+#include "mdcn_pdl.h"
 #include "mdcn_plan.h"
 #include "mdcn_rotary.h"
 
@@ -641,6 +642,7 @@ __global__ void __launch_bounds__(kThreads, 2) rotary_forward_kernel(const __gri
     __shared__ WarpSmem<kMode> smem[kWarps];
     __shared__ PairFreq table[kMaxD / 2];
     const LaneSetup<kMode> L(a);
+    dependency_wait();
     fill_freqs(a, table);
     const int t = blockIdx.y;
     Forward<T, kMode> op(a, t, L);
@@ -658,6 +660,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) rotary_backward_kernel(const _
     __shared__ PairFreq table[kMaxD / 2];
     __shared__ float sums[kBwdWarps][kMaxD];
     const LaneSetup<kMode> L(a);
+    dependency_wait();
     fill_freqs(a, table);
     const int t = blockIdx.y;
     Backward<T, kMode> op(a, t, L);
@@ -695,7 +698,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) rotary_backward_kernel(const _
 // lanes to an element. Grid: (head_dim / 8, 2).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) rotary_weight_sum_kernel(const float* part, int blocks, int D, T* gq, T* gk) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    dependency_wait();
     T* g = blockIdx.y ? gk : gq;
     if (!g) return;
     // 8 neighbouring elements x 32 slices of the blocks
@@ -737,38 +740,30 @@ int64_t blocks_for(const RotaryArgs& a, int warps) {
 template <typename T>
 cudaError_t forward_t(const RotaryArgs& a, RotaryMode mode, int64_t grid, cudaStream_t st) {
     const dim3 g(static_cast<unsigned>(grid), a.rows > a.hq ? 2u : 1u);
+    cudaError_t e;
     if (mode == kBeside)
-        rotary_forward_kernel<T, kBeside><<<g, kThreads, 0, st>>>(a);
+        e = launch_dependent(rotary_forward_kernel<T, kBeside>, g, kThreads, 0, st, a);
     else if (mode == kChunks)
-        rotary_forward_kernel<T, kChunks><<<g, kThreads, 0, st>>>(a);
+        e = launch_dependent(rotary_forward_kernel<T, kChunks>, g, kThreads, 0, st, a);
     else
-        rotary_forward_kernel<T, kAnywhere><<<g, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+        e = launch_dependent(rotary_forward_kernel<T, kAnywhere>, g, kThreads, 0, st, a);
+    return e;
 }
 
 template <typename T>
 cudaError_t backward_t(const RotaryArgs& a, RotaryMode mode, int64_t grid, void* gqw, void* gkw, cudaStream_t st) {
     const dim3 g(static_cast<unsigned>(grid), a.rows > a.hq ? 2u : 1u);
+    cudaError_t e;
     if (mode == kBeside)
-        rotary_backward_kernel<T, kBeside><<<g, kBwdThreads, 0, st>>>(a);
+        e = launch_dependent(rotary_backward_kernel<T, kBeside>, g, kBwdThreads, 0, st, a);
     else if (mode == kChunks)
-        rotary_backward_kernel<T, kChunks><<<g, kBwdThreads, 0, st>>>(a);
+        e = launch_dependent(rotary_backward_kernel<T, kChunks>, g, kBwdThreads, 0, st, a);
     else
-        rotary_backward_kernel<T, kAnywhere><<<g, kBwdThreads, 0, st>>>(a);
-    cudaError_t e = cudaGetLastError();
+        e = launch_dependent(rotary_backward_kernel<T, kAnywhere>, g, kBwdThreads, 0, st, a);
     if (e != cudaSuccess || !a.part) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(a.D / 8), 2);
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, rotary_weight_sum_kernel<T>, static_cast<const float*>(a.part),
-                           static_cast<int>(grid), static_cast<int>(a.D), static_cast<T*>(gqw), static_cast<T*>(gkw));
-    return e == cudaSuccess ? cudaGetLastError() : e;
+    return launch_dependent(rotary_weight_sum_kernel<T>, dim3(static_cast<unsigned>(a.D / 8), 2), kThreads, 0, st,
+                            static_cast<const float*>(a.part), static_cast<int>(grid), static_cast<int>(a.D),
+                            static_cast<T*>(gqw), static_cast<T*>(gkw));
 }
 
 }  // namespace

@@ -1,5 +1,5 @@
 // Device code shared by the attention kernels: which sequence a tile belongs
-// to, and element conversions.
+// to, packed fp32 arithmetic, element conversions.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -10,6 +10,33 @@
 #include "mdcn_attention.h"
 
 namespace mdcn {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Two fp32 values in one register pair: (lo, hi).
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 
 __device__ __forceinline__ float attn_to_f(float v) { return v; }
 __device__ __forceinline__ float attn_to_f(__half v) { return __half2float(v); }

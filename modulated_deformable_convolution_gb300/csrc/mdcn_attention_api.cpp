@@ -138,11 +138,14 @@ mdcn_status attn_check(const mdcn_attention_attrs* at, const mdcn_attention_dims
 // steps costs n + 2, or n + 4 where the steps wait for memory. Sequences that
 // fill their rows: as many waves of items as the SMs need, each as long as an
 // item. Sequences of any length up to their rows (k_lengths): half the steps on
-// average, taken as they come, and one item's length at the end. The join of
-// the shares costs a launch and the partial results' way to memory and back.
+// average, taken as they come, and one item's length at the end. In float32 a
+// step is some four times as long, several blocks share an SM and most calls
+// have few: the SMs' work, and one item's length at the end. The join of the
+// shares costs a launch and the partial results' way to memory and back.
 // (Measured: 4 maps of 80 x 80, 2 heads of 64: 112 us with one share, 104 with
 // three; 16 new tokens against up to 8192 keys: 90 with one, 81 with four; a
-// prompt of 1024 tokens, 32 heads: 28 with one, 40 with two.)
+// prompt of 1024 tokens, 32 heads: 28 with one, 40 with two; float32, 6 maps of
+// up to 32 x 32, 8 heads of 40: 118 with one, 88 with four, 91 with six.)
 struct AttnPlan {
     int64_t tiles, splits;
     size_t off_out, off_lse, bytes;
@@ -151,6 +154,7 @@ struct AttnPlan {
 AttnPlan attn_plan(const mdcn_attention_attrs& at, const mdcn_attention_dims& d, mdcn_dtype dtype, bool lengths) {
     constexpr int64_t kSms = 152, kMaxSplits = 32;
     constexpr double kItemSteps = 2.0, kWaitingItemSteps = 4.0, kJoinSteps = 2.5, kStepBytes = 8.0e6;
+    constexpr double kF32ItemSteps = 0.3, kF32Step = 0.25;
     AttnPlan p{};
     const int64_t group = d.q_heads / d.k_heads;
     const bool tc = dtype != MDCN_F32;
@@ -169,10 +173,15 @@ AttnPlan attn_plan(const mdcn_attention_attrs& at, const mdcn_attention_dims& d,
         double best = 0.0;
         for (int64_t s = 1; s <= kMaxSplits && s <= steps; ++s) {
             const double item = static_cast<double>((steps + s - 1) / s);
-            double cost = lengths ? (static_cast<double>(blocks) * (static_cast<double>(steps) / 2 + kWaitingItemSteps * s)) /
-                                            static_cast<double>(kSms) + item
-                                  : static_cast<double>((blocks * s + kSms - 1) / kSms) * (item + kItemSteps);
-            if (s > 1) cost += kJoinSteps + rows * static_cast<double>(s) / kStepBytes;
+            const double mean_steps = lengths ? static_cast<double>(steps) / 2 : static_cast<double>(steps);
+            double cost;
+            if (!tc)
+                cost = static_cast<double>(blocks) * (mean_steps + kF32ItemSteps * s) / static_cast<double>(kSms) + item;
+            else if (lengths)
+                cost = static_cast<double>(blocks) * (mean_steps + kWaitingItemSteps * s) / static_cast<double>(kSms) + item;
+            else
+                cost = static_cast<double>((blocks * s + kSms - 1) / kSms) * (item + kItemSteps);
+            if (s > 1) cost += (kJoinSteps + rows * static_cast<double>(s) / kStepBytes) * (tc ? 1.0 : kF32Step);
             if (s == 1 || cost < best) {
                 best = cost;
                 p.splits = s;
@@ -193,7 +202,9 @@ AttnPlan attn_plan(const mdcn_attention_attrs& at, const mdcn_attention_dims& d,
 
 // The backward's plan: where delta lies, and in float32 between how many blocks
 // the rows that see a key tile are shared out (the row tiles' own blocks run
-// beside them): as many as fill the SMs twice, each with two row tiles at least.
+// beside them): as many as make three blocks to an SM, each with two row tiles at
+// least (2 sequences of 2048, 6 heads of 64 over 2: 972 us with one share, 771
+// with two, 702 with three, 728 with six).
 struct AttnBwdPlan {
     int64_t tiles, kv_splits;
     size_t off_kv, bytes;
@@ -208,7 +219,7 @@ AttnBwdPlan attn_bwd_plan(const mdcn_attention_dims& d, mdcn_dtype dtype) {
     size_t off = align256(mdcn::kAttnHeaderBytes + static_cast<size_t>(d.q_tokens) * static_cast<size_t>(d.q_heads) * 4);
     const int64_t kv = mdcn::attn_tiles(d.k_tokens, d.batch, 64) * d.k_heads;
     if (dtype == MDCN_F32 && kv > 0) {
-        int64_t s = 2 * kSms / kv;
+        int64_t s = 3 * kSms / kv;
         const int64_t row_tiles = (d.q_tokens / d.batch + tokens - 1) / tokens;
         if (s > row_tiles / 2) s = row_tiles / 2;
         p.kv_splits = s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s;

@@ -7,15 +7,20 @@
 // p (g.v - delta) scale; some blocks sum ds k over the keys of 64 rows, the
 // others p^T g and ds^T q over the rows that see 64 keys, in one launch.
 //
-// Bound by fp32 multiply-adds. 256 threads hold a 64 x 64 score tile as 4 x 4
-// each and a 64 x D accumulator as 4 rows x 4-element pieces; operands come
-// from shared memory as 16-byte vectors (rows padded by 4 words, so that the
-// 16 rows a warp reads at once fall into different banks), 64 multiply-adds
-// for 8 vectors. Tiles are copied to shared memory asynchronously, each as
-// soon as the one before it has been used, and two blocks share an SM where
-// their tiles fit, so that one computes while the other waits. Tensor cores
-// would need three products of reduced precision for one of fp32 (or six
-// with 16-bit parts), each with its own copy of the operands.
+// Bound by fp32 multiply-adds and, as near, by the reads of their operands from
+// shared memory. 128 threads hold a 64 x 64 score tile as 4 rows x 8 keys each
+// (12 16-byte reads for 128 multiply-adds; 4 x 4 has 16) and a 64 x D
+// accumulator as 4 rows x D / 8 elements; two multiply-adds go to an
+// instruction, on pairs of elements. Loops over a head have constant bounds, by
+// sixteens of D. Tiles are copied to shared memory asynchronously, each as soon
+// as the one before it has been used, and two or three blocks share an SM where
+// their tiles fit, so that one computes while another waits. Tensor cores
+// would need three products of reduced precision for one of fp32 (or six with
+// 16-bit parts), each with its own copy of the operands.
+// Measured: forward, 2 sequences of 2048, 8 heads of 64 over 4: 470 us, 36
+// TFLOP/s of about 78; 6 maps of up to 32 x 32, 8 heads of 40 over 4: 88 us. Backward, 4
+// ragged sequences of up to 700, 6 heads of 72 over 2: 142 us; 2 sequences of
+// 2048, 6 heads of 64 over 2: 702 us, 32 TFLOP/s of seven products.
 #include <cfloat>
 #include <cstdint>
 
@@ -29,10 +34,14 @@ namespace {
 
 constexpr int kR = kAttnSimtRows;  // rows of a tile
 constexpr int kC = 64;             // keys of a tile
-constexpr int kT = 256;
-constexpr int kPP = kC + 4;        // padded row of the probability tile
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kAcc = 2;            // 4-element pieces of a row per thread: 64 * kAcc >= D
+constexpr int kT = 256;            // threads of the small kernels
+constexpr int kTT = 128;           // threads to a tile
+constexpr int kPP = kC + 8;        // padded row of the probability tile
+
+// Of a head of 16 kN elements at most: words of a padded row in shared memory.
+// A multiple of 4 and, in units of 4, odd: 8 rows that are read at once lie in
+// different banks.
+__host__ __device__ constexpr int pitch_of(int kN) { return 16 * kN + 4; }
 
 __device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
     c = fmaf(a.x, b.x, c);
@@ -55,197 +64,286 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
 }
 
-// Rows of a packed row tile into shared memory: row r = (token r / group, head
-// r % group) of key head kh, zero past the sequence's end. One group of copies.
-__device__ __forceinline__ void load_rows(float* dst, int pitch, const AttnTensor& t, const AttnArgs& a,
-                                          const AttnSeq& s, int32_t tok0, int32_t ntok, int kh) {
-    const int v4 = a.D / 4, rows = ntok * a.group;
-    for (int i = threadIdx.x; i < kR * v4; i += kT) {
-        const int r = i / v4, c = (i - r * v4) * 4;
-        const bool there = r < rows;
-        const int tk = there ? r / a.group : 0, h = kh * a.group + (there ? r - tk * a.group : 0);
-        copy16(dst + r * pitch + c,
-               static_cast<const float*>(t.p) + static_cast<int64_t>(s.q0 + tok0 + tk) * t.st +
-                   static_cast<int64_t>(h) * t.sh + c,
-               there);
-    }
-    copies_end();
-}
+// The part that a thread copies: every second 4-element piece of one row of 64.
+struct Copier {
+    int row, half;
+    int tk, head;  // of a row tile's row: its token and head within the tile
 
-// Keys (or values) [j0, j0 + 64) of the sequence, zero past its last key. One
-// group of copies.
-__device__ __forceinline__ void load_keys(float* dst, int pitch, const AttnTensor& t, const AttnArgs& a,
-                                          const AttnSeq& s, int32_t j0, int kh) {
-    const int v4 = a.D / 4;
-    for (int i = threadIdx.x; i < kC * v4; i += kT) {
-        const int r = i / v4, c = (i - r * v4) * 4;
-        const bool there = j0 + r < s.lk;
-        copy16(dst + r * pitch + c,
-               static_cast<const float*>(t.p) + static_cast<int64_t>(there ? s.k0 + j0 + r : 0) * t.st +
-                   static_cast<int64_t>(kh) * t.sh + c,
-               there);
+    __device__ __forceinline__ explicit Copier(int group) {
+        row = threadIdx.x >> 1;
+        half = threadIdx.x & 1;
+        tk = row / group;
+        head = row - tk * group;
     }
-    copies_end();
-}
+    // One group of copies: the row, with zeros past the head's elements, or all zeros.
+    template <int kN>
+    __device__ __forceinline__ void copy(float* dst, const float* src, bool there, int D) const {
+        float* to = dst + row * pitch_of(kN) + half * 4;
+        src += half * 4;
+#pragma unroll
+        for (int c = 0; c < 2 * kN; ++c) {
+            const bool in = there && 8 * c + 4 * half < D;
+            copy16(to + 8 * c, in ? src + 8 * c : src, in);
+        }
+        copies_end();
+    }
+    // Rows of a packed row tile: row r = (token r / group, head r % group) of
+    // key head kh, zero past the sequence's end.
+    template <int kN>
+    __device__ __forceinline__ void rows(float* dst, const AttnTensor& t, const AttnArgs& a, const AttnSeq& s,
+                                         int32_t tok0, int32_t ntok, int kh) const {
+        const bool there = tk < ntok;
+        copy<kN>(dst,
+                 static_cast<const float*>(t.p) +
+                     (there ? static_cast<int64_t>(s.q0 + tok0 + tk) * t.st + static_cast<int64_t>(kh * a.group + head) * t.sh
+                            : 0),
+                 there, a.D);
+    }
+    // Keys (or values) [j0, j0 + 64) of the sequence, zero past its last key.
+    template <int kN>
+    __device__ __forceinline__ void keys(float* dst, const AttnTensor& t, const AttnArgs& a, const AttnSeq& s,
+                                         int32_t j0, int kh) const {
+        const bool there = j0 + row < s.lk;
+        copy<kN>(dst,
+                 static_cast<const float*>(t.p) +
+                     (there ? static_cast<int64_t>(s.k0 + j0 + row) * t.st + static_cast<int64_t>(kh) * t.sh : 0),
+                 there, a.D);
+    }
+};
 
-// acc[i][j] = row (ty + 16 i) of x . row (tx + 16 j) of y
-__device__ __forceinline__ void products(float (&acc)[4][4], const float* x, const float* y, int pitch, int D, int tx,
-                                         int ty) {
+// The 4 rows of a thread (ty + 16 i): their tokens, heads and whether they are of the tile.
+struct Rows {
+    int tk[4], head[4];
+
+    __device__ __forceinline__ Rows(int ty, int group) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            tk[i] = (ty + 16 * i) / group;
+            head[i] = ty + 16 * i - tk[i] * group;
+        }
+    }
+};
+
+// acc[i][j] = row (ty + 16 i) of x . row (tx + 8 j) of y: even and odd elements
+// summed apart, two multiply-adds to an instruction.
+template <int kN>
+__device__ __forceinline__ void products(float (&acc)[4][8], const float* x, const float* y, int tx, int ty) {
+    constexpr int kPitch = pitch_of(kN);
+    uint64_t s[4][8];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-    for (int d = 0; d < D; d += 4) {
-        float4 u[4], w[4];
+        for (int j = 0; j < 8; ++j) s[i][j] = 0;
+    const float* xr = x + ty * kPitch;
+    const float* yr = y + tx * kPitch;
+#pragma unroll 2
+    for (int d = 0; d < 16 * kN; d += 4) {
+        ulonglong2 u[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const float4*>(x + (ty + 16 * i) * pitch + d);
+        for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const ulonglong2*>(xr + 16 * i * kPitch + d);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const float4*>(y + (tx + 16 * j) * pitch + d);
+        for (int j = 0; j < 8; ++j) {
+            const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(yr + 8 * j * kPitch + d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) s[i][j] = fma2(u[i].y, w.y, fma2(u[i].x, w.x, s[i][j]));
+        }
+    }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = dot4(u[i], w[j], acc[i][j]);
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float lo, hi;
+            unpack2(s[i][j], lo, hi);
+            acc[i][j] = lo + hi;
+        }
+}
+
+// A thread's elements of a row of 16 kN: pairs, two in each 4-element piece
+// 4 tx + 32 c, and one at 2 tx of the last 16 where kN is odd.
+template <int kN>
+__device__ __forceinline__ int element(int pair, int tx) {
+    return pair < 2 * (kN / 2) ? 4 * tx + 32 * (pair / 2) + 2 * (pair & 1) : 32 * (kN / 2) + 2 * tx;
+}
+
+template <int kN>
+using Sums = uint64_t[4][kN];
+
+// o[i] += f[i] * row y, for the thread's elements.
+template <int kN>
+__device__ __forceinline__ void add_row(Sums<kN>& o, const float (&f)[4], const float* y, int tx) {
+    uint64_t f2[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f2[i] = pack2(f[i], f[i]);
+#pragma unroll
+    for (int c = 0; c < kN / 2; ++c) {
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(y + 4 * tx + 32 * c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o[i][2 * c] = fma2(f2[i], v.x, o[i][2 * c]);
+            o[i][2 * c + 1] = fma2(f2[i], v.y, o[i][2 * c + 1]);
+        }
+    }
+    if constexpr (kN & 1) {
+        const uint64_t v = *reinterpret_cast<const uint64_t*>(y + 32 * (kN / 2) + 2 * tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i][kN - 1] = fma2(f2[i], v, o[i][kN - 1]);
     }
 }
 
-// o[i] (row ty + 16 i, elements tx * 4 + 64 c) += sum over the 64 columns j of p[row][j] * y[j]
-__device__ __forceinline__ void accumulate(float4 (&o)[4][kAcc], const float* p, const float* y, int pitch, int D,
-                                           int tx, int ty) {
+// o[i] (row ty + 16 i) += sum over the 64 columns j of p[row][j] * y[j]
+template <int kN>
+__device__ __forceinline__ void accumulate(Sums<kN>& o, const float* p, const float* y, int tx, int ty) {
+    constexpr int kPitch = pitch_of(kN);
+#pragma unroll 1
     for (int j = 0; j < kC; j += 4) {
         float4 w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(p + (ty + 16 * i) * kPP + j);
 #pragma unroll
-        for (int c = 0; c < kAcc; ++c) {
-            const int d = tx * 4 + 64 * c;
-            if (d >= D) continue;
+        for (int jj = 0; jj < 4; ++jj) {
+            float f[4];
 #pragma unroll
-            for (int jj = 0; jj < 4; ++jj) {
-                const float4 v = *reinterpret_cast<const float4*>(y + (j + jj) * pitch + d);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float f = jj == 0 ? w[i].x : jj == 1 ? w[i].y : jj == 2 ? w[i].z : w[i].w;
-                    o[i][c].x = fmaf(f, v.x, o[i][c].x);
-                    o[i][c].y = fmaf(f, v.y, o[i][c].y);
-                    o[i][c].z = fmaf(f, v.z, o[i][c].z);
-                    o[i][c].w = fmaf(f, v.w, o[i][c].w);
-                }
-            }
+            for (int i = 0; i < 4; ++i) f[i] = jj == 0 ? w[i].x : jj == 1 ? w[i].y : jj == 2 ? w[i].z : w[i].w;
+            add_row<kN>(o, f, y + (j + jj) * kPitch, tx);
         }
     }
 }
 
-__device__ __forceinline__ float max16(float v) {
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
-}
-__device__ __forceinline__ float sum16(float v) {
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+// o[i] (row 4 ty + i) += sum over the 64 rows r of p[r][row] * y[r]
+template <int kN>
+__device__ __forceinline__ void accumulate_t(Sums<kN>& o, const float* p, const float* y, int tx, int ty) {
+#pragma unroll 4
+    for (int r = 0; r < kR; ++r) {
+        const float4 w = *reinterpret_cast<const float4*>(p + r * kPP + ty * 4);
+        const float f[4] = {w.x, w.y, w.z, w.w};
+        add_row<kN>(o, f, y + r * pitch_of(kN), tx);
+    }
 }
 
-// Grid: (tiles * splits, key heads). Block x takes tile x / splits and the
-// (x % splits)-th share of the key tiles that the tile's rows see.
-__global__ void __launch_bounds__(kT, 2) attn_forward_simt_kernel(const __grid_constant__ AttnArgs a) {
+template <int kN>
+__device__ __forceinline__ void clear(Sums<kN>& o) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < kN; ++c) o[i][c] = 0;
+}
+
+// The thread's elements of a row times f to `to`.
+template <int kN>
+__device__ __forceinline__ void store_row(float* to, const uint64_t (&o)[kN], float f, int D, int tx) {
+#pragma unroll
+    for (int c = 0; c < kN; ++c) {
+        const int d = element<kN>(c, tx);
+        float lo, hi;
+        unpack2(o[c], lo, hi);
+        if (d < D) *reinterpret_cast<float2*>(to + d) = make_float2(lo * f, hi * f);
+    }
+}
+
+// Over the 8 lanes (tx) that share rows.
+__device__ __forceinline__ float max8(float v) {
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+__device__ __forceinline__ float sum8(float v) {
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ float max16(float v) { return max8(fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8))); }
+__device__ __forceinline__ float sum16(float v) { return sum8(v + __shfl_xor_sync(0xffffffffu, v, 8)); }
+
+// Grid: tiles * splits * key heads, the heads of one share of one tile side by
+// side, so that blocks of one length are spread evenly over the SMs. A block
+// takes the split-th share of the key tiles that its tile's rows see.
+template <int kN>
+__global__ void __launch_bounds__(kTT, kN <= 4 ? 3 : 2) attn_forward_simt_kernel(const __grid_constant__ AttnArgs a) {
     extern __shared__ float sm[];
     dependency_wait();
-    if (a.status && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.status = 0;
+    if (a.status && blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
     const int tpt = kR / a.group;
-    const AttnSeq s = attn_find(a, false, tpt, blockIdx.x / a.splits);
+    const int item = blockIdx.x / a.hk, kh = blockIdx.x - item * a.hk, split = item % a.splits;
+    const AttnSeq s = attn_find(a, false, tpt, item / a.splits);
     if (s.tile < 0) return;
-    const int kh = blockIdx.y, split = blockIdx.x % a.splits;
-    const int pitch = a.D + 4;
+    constexpr int kPitch = pitch_of(kN);
     float* qs = sm;
-    float* ks = qs + kR * pitch;
-    float* vs = ks + kC * pitch;
-    float* ps = vs + kC * pitch;
+    float* ks = qs + kR * kPitch;
+    float* vs = ks + kC * kPitch;
+    float* ps = vs + kC * kPitch;
     const int32_t tok0 = s.tile * tpt, ntok = min(tpt, s.lq - tok0);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
     const int32_t most = attn_seen(a, s, tok0 + ntok - 1);
     const int32_t ktiles = (most + kC - 1) / kC, per = (ktiles + a.splits - 1) / a.splits;
     const int32_t t0 = min(split * per, ktiles), t1 = min(t0 + per, ktiles);
-    load_rows(qs, pitch, a.q, a, s, tok0, ntok, kh);
-    if (t0 < t1) load_keys(ks, pitch, a.k, a, s, t0 * kC, kh);
+    const Copier mine(a.group);
+    mine.rows<kN>(qs, a.q, a, s, tok0, ntok, kh);
+    if (t0 < t1) mine.keys<kN>(ks, a.k, a, s, t0 * kC, kh);
 
+    const Rows rows(ty, a.group);
     int32_t seen[4];
     float m[4], l[4];
-    float4 o[4][kAcc];
+    Sums<kN> o;
+    clear<kN>(o);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int r = ty + 16 * i;
-        seen[i] = r < ntok * a.group ? attn_seen(a, s, tok0 + r / a.group) : 0;
+        seen[i] = rows.tk[i] < ntok ? attn_seen(a, s, tok0 + rows.tk[i]) : 0;
         m[i] = -INFINITY;
         l[i] = 0.0f;
-#pragma unroll
-        for (int c = 0; c < kAcc; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     const float to_log2 = a.scale * kLog2e;
+#pragma unroll 1
     for (int32_t t = t0; t < t1; ++t) {
-        load_keys(vs, pitch, a.v, a, s, t * kC, kh);
+        mine.keys<kN>(vs, a.v, a, s, t * kC, kh);
         copies_wait<1>();  // the keys
         __syncthreads();
-        float x[4][4];
-        products(x, qs, ks, pitch, a.D, tx, ty);
+        float x[4][8];
+        products<kN>(x, qs, ks, tx, ty);
         __syncthreads();
         if (t + 1 < t1)
-            load_keys(ks, pitch, a.k, a, s, (t + 1) * kC, kh);
+            mine.keys<kN>(ks, a.k, a, s, (t + 1) * kC, kh);
         else
             copies_end();
-        float corr[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float best = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                x[i][j] = t * kC + tx + 16 * j < seen[i] ? x[i][j] * to_log2 : -INFINITY;
+            for (int j = 0; j < 8; ++j) {
+                x[i][j] = t * kC + tx + 8 * j < seen[i] ? x[i][j] * to_log2 : -INFINITY;
                 best = fmaxf(best, x[i][j]);
             }
-            best = fmaxf(max16(best), m[i]);
+            best = fmaxf(max8(best), m[i]);
             const float base = best == -INFINITY ? 0.0f : best;  // no key seen so far: every term is exp2(-inf) = 0
-            corr[i] = exp2f(m[i] - base);
+            const float corr = exp2f(m[i] - base);
             m[i] = best;
             float sum = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 8; ++j) {
                 const float p = exp2f(x[i][j] - base);
                 sum += p;
-                ps[(ty + 16 * i) * kPP + tx + 16 * j] = p;
+                ps[(ty + 16 * i) * kPP + tx + 8 * j] = p;
             }
-            l[i] = fmaf(l[i], corr[i], sum16(sum));
+            l[i] = fmaf(l[i], corr, sum8(sum));
+            const uint64_t corr2 = pack2(corr, corr);
 #pragma unroll
-            for (int c = 0; c < kAcc; ++c) {
-                o[i][c].x *= corr[i];
-                o[i][c].y *= corr[i];
-                o[i][c].z *= corr[i];
-                o[i][c].w *= corr[i];
-            }
+            for (int c = 0; c < kN; ++c) o[i][c] = mul2(o[i][c], corr2);
         }
         copies_wait<1>();  // the values
         __syncthreads();
-        accumulate(o, ps, vs, pitch, a.D, tx, ty);
+        accumulate<kN>(o, ps, vs, tx, ty);
         __syncthreads();
     }
     copies_wait<0>();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int r = ty + 16 * i;
-        if (r >= ntok * a.group) continue;
-        const int64_t tok = s.q0 + tok0 + r / a.group;
-        const int h = kh * a.group + r % a.group;
+        if (rows.tk[i] >= ntok) continue;
+        const int64_t tok = s.q0 + tok0 + rows.tk[i];
+        const int h = kh * a.group + rows.head[i];
         const float inv = l[i] > 0.0f ? 1.0f / l[i] : (l[i] == 0.0f ? 0.0f : l[i]);
         const float lse = l[i] == 0.0f ? -INFINITY : m[i] * 0.6931471805599453f + logf(l[i]);
-#pragma unroll
-        for (int c = 0; c < kAcc; ++c) {
-            const int d = tx * 4 + 64 * c;
-            if (d >= a.D) continue;
-            const float4 v = make_float4(o[i][c].x * inv, o[i][c].y * inv, o[i][c].z * inv, o[i][c].w * inv);
-            if (a.splits > 1)
-                *reinterpret_cast<float4*>(a.part_out + ((static_cast<int64_t>(split) * a.tq + tok) * a.hq + h) * a.D + d) = v;
-            else
-                *reinterpret_cast<float4*>(static_cast<float*>(a.out.p) + tok * a.out.st + h * a.out.sh + d) = v;
-        }
+        float* to = a.splits > 1 ? a.part_out + ((static_cast<int64_t>(split) * a.tq + tok) * a.hq + h) * a.D
+                                 : static_cast<float*>(a.out.p) + tok * a.out.st + h * a.out.sh;
+        store_row<kN>(to, o[i], inv, a.D, tx);
         if (tx == 0) {
             if (a.splits > 1)
                 a.part_lse[(static_cast<int64_t>(split) * a.hq + h) * a.tq + tok] = lse;
@@ -256,177 +354,152 @@ __global__ void __launch_bounds__(kT, 2) attn_forward_simt_kernel(const __grid_c
 }
 
 // grad_q of one row tile.
+template <int kN>
 __device__ __forceinline__ void grad_q_block(const AttnArgs& a, float* sm, int32_t index, int kh) {
     const int tpt = kR / a.group;
     const AttnSeq s = attn_find(a, false, tpt, index);
     if (s.tile < 0) return;
-    const int pitch = a.D + 4;
+    constexpr int kPitch = pitch_of(kN);
     float* qs = sm;
-    float* gs = qs + kR * pitch;
-    float* ks = gs + kR * pitch;
-    float* vs = ks + kC * pitch;
-    float* ps = vs + kC * pitch;
+    float* gs = qs + kR * kPitch;
+    float* ks = gs + kR * kPitch;
+    float* vs = ks + kC * kPitch;
+    float* ps = vs + kC * kPitch;
     const int32_t tok0 = s.tile * tpt, ntok = min(tpt, s.lq - tok0);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
     const int32_t ktiles = (attn_seen(a, s, tok0 + ntok - 1) + kC - 1) / kC;
-    load_rows(qs, pitch, a.q, a, s, tok0, ntok, kh);
-    load_rows(gs, pitch, a.g, a, s, tok0, ntok, kh);
+    const Copier mine(a.group);
+    mine.rows<kN>(qs, a.q, a, s, tok0, ntok, kh);
+    mine.rows<kN>(gs, a.g, a, s, tok0, ntok, kh);
     if (ktiles > 0) {
-        load_keys(ks, pitch, a.k, a, s, 0, kh);
-        load_keys(vs, pitch, a.v, a, s, 0, kh);
+        mine.keys<kN>(ks, a.k, a, s, 0, kh);
+        mine.keys<kN>(vs, a.v, a, s, 0, kh);
     }
+    const Rows rows(ty, a.group);
     int32_t seen[4];
     float lse[4], delta[4];
-    float4 o[4][kAcc];
+    Sums<kN> o;
+    clear<kN>(o);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int r = ty + 16 * i;
-        const bool live = r < ntok * a.group;
-        const int64_t at = live ? static_cast<int64_t>(kh * a.group + r % a.group) * a.tq + s.q0 + tok0 + r / a.group : 0;
-        seen[i] = live ? attn_seen(a, s, tok0 + r / a.group) : 0;
+        const bool live = rows.tk[i] < ntok;
+        const int64_t at =
+            live ? static_cast<int64_t>(kh * a.group + rows.head[i]) * a.tq + s.q0 + tok0 + rows.tk[i] : 0;
+        seen[i] = live ? attn_seen(a, s, tok0 + rows.tk[i]) : 0;
         lse[i] = live ? a.lse[at] : 0.0f;
         delta[i] = live ? a.delta[at] : 0.0f;
-#pragma unroll
-        for (int c = 0; c < kAcc; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
+#pragma unroll 1
     for (int32_t t = 0; t < ktiles; ++t) {
         copies_wait<1>();  // the keys
         __syncthreads();
-        float x[4][4], dp[4][4];
-        products(x, qs, ks, pitch, a.D, tx, ty);
+        float x[4][8], dp[4][8];
+        products<kN>(x, qs, ks, tx, ty);
         copies_wait<0>();  // the values
         __syncthreads();
-        products(dp, gs, vs, pitch, a.D, tx, ty);
+        products<kN>(dp, gs, vs, tx, ty);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bool on = t * kC + tx + 16 * j < seen[i];
+            for (int j = 0; j < 8; ++j) {
+                const bool on = t * kC + tx + 8 * j < seen[i];
                 // s - lse is rounded once, before the small difference is scaled
                 const float p = on ? exp2f(fmaf(x[i][j], a.scale, -lse[i]) * kLog2e) : 0.0f;
-                ps[(ty + 16 * i) * kPP + tx + 16 * j] = on ? p * (dp[i][j] - delta[i]) : 0.0f;
+                ps[(ty + 16 * i) * kPP + tx + 8 * j] = on ? p * (dp[i][j] - delta[i]) : 0.0f;
             }
         __syncthreads();
-        accumulate(o, ps, ks, pitch, a.D, tx, ty);
+        accumulate<kN>(o, ps, ks, tx, ty);
         __syncthreads();
         if (t + 1 < ktiles) {
-            load_keys(ks, pitch, a.k, a, s, (t + 1) * kC, kh);
-            load_keys(vs, pitch, a.v, a, s, (t + 1) * kC, kh);
+            mine.keys<kN>(ks, a.k, a, s, (t + 1) * kC, kh);
+            mine.keys<kN>(vs, a.v, a, s, (t + 1) * kC, kh);
         }
     }
     copies_wait<0>();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int r = ty + 16 * i;
-        if (r >= ntok * a.group) continue;
-        const int64_t tok = s.q0 + tok0 + r / a.group;
-        const int h = kh * a.group + r % a.group;
-#pragma unroll
-        for (int c = 0; c < kAcc; ++c) {
-            const int d = tx * 4 + 64 * c;
-            if (d < a.D)
-                *reinterpret_cast<float4*>(static_cast<float*>(a.gq.p) + tok * a.gq.st + h * a.gq.sh + d) =
-                    make_float4(o[i][c].x * a.scale, o[i][c].y * a.scale, o[i][c].z * a.scale, o[i][c].w * a.scale);
-        }
-    }
-}
-
-// o[i] (row 4 ty + i) += sum over the 64 rows r of p[r][row] * y[r]
-__device__ __forceinline__ void accumulate_t(float4 (&o)[4][kAcc], const float* p, const float* y, int pitch, int D,
-                                             int tx, int ty) {
-#pragma unroll 4
-    for (int r = 0; r < kR; ++r) {
-        const float4 w = *reinterpret_cast<const float4*>(p + r * kPP + ty * 4);
-        const float f[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int c = 0; c < kAcc; ++c) {
-            const int d = tx * 4 + 64 * c;
-            if (d >= D) continue;
-            const float4 v = *reinterpret_cast<const float4*>(y + r * pitch + d);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                o[i][c].x = fmaf(f[i], v.x, o[i][c].x);
-                o[i][c].y = fmaf(f[i], v.y, o[i][c].y);
-                o[i][c].z = fmaf(f[i], v.z, o[i][c].z);
-                o[i][c].w = fmaf(f[i], v.w, o[i][c].w);
-            }
-        }
+        if (rows.tk[i] >= ntok) continue;
+        const int64_t tok = s.q0 + tok0 + rows.tk[i];
+        store_row<kN>(static_cast<float*>(a.gq.p) + tok * a.gq.st + (kh * a.group + rows.head[i]) * a.gq.sh, o[i], a.scale,
+                      a.D, tx);
     }
 }
 
 // grad_k and grad_v of 64 keys of one key head, or (a.kv_splits > 1) the sums
 // over a share of the row tiles that see them. P, then dS, in one buffer.
+template <int kN>
 __device__ __forceinline__ void grad_kv_block(const AttnArgs& a, float* sm, int32_t index, int32_t split, int kh) {
     const AttnSeq s = attn_find(a, true, kC, index);
     if (s.tile < 0) return;
-    const int pitch = a.D + 4, tpt = kR / a.group;
+    constexpr int kPitch = pitch_of(kN);
+    const int tpt = kR / a.group;
     float* qs = sm;
-    float* gs = qs + kR * pitch;
-    float* ks = gs + kR * pitch;
-    float* vs = ks + kC * pitch;
-    float* ps = vs + kC * pitch;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    float* gs = qs + kR * kPitch;
+    float* ks = gs + kR * kPitch;
+    float* vs = ks + kC * kPitch;
+    float* ps = vs + kC * kPitch;
+    const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
     const int32_t j0 = s.tile * kC;
-    float4 ok[4][kAcc], ov[4][kAcc];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int c = 0; c < kAcc; ++c) ok[i][c] = ov[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    Sums<kN> ok, ov;
+    clear<kN>(ok);
+    clear<kN>(ov);
     // row tiles from the first that sees key j0
     const int32_t first = a.causal ? max(0, j0 + s.lq - s.lk) / tpt : 0;
     const int32_t tiles = j0 < s.lk ? max(0, (s.lq + tpt - 1) / tpt - first) : 0;
     const int32_t per = (tiles + a.kv_splits - 1) / a.kv_splits;
     const int32_t b0 = first + min(split * per, tiles), b1 = first + min(split * per + per, tiles);
+    const Copier mine(a.group);
     if (b0 < b1) {
-        load_keys(ks, pitch, a.k, a, s, j0, kh);
-        load_keys(vs, pitch, a.v, a, s, j0, kh);
-        load_rows(qs, pitch, a.q, a, s, b0 * tpt, min(tpt, s.lq - b0 * tpt), kh);
-        load_rows(gs, pitch, a.g, a, s, b0 * tpt, min(tpt, s.lq - b0 * tpt), kh);
+        mine.keys<kN>(ks, a.k, a, s, j0, kh);
+        mine.keys<kN>(vs, a.v, a, s, j0, kh);
+        mine.rows<kN>(qs, a.q, a, s, b0 * tpt, min(tpt, s.lq - b0 * tpt), kh);
+        mine.rows<kN>(gs, a.g, a, s, b0 * tpt, min(tpt, s.lq - b0 * tpt), kh);
     }
+    const Rows rows(ty, a.group);
+#pragma unroll 1
     for (int32_t b = b0; b < b1; ++b) {
         const int32_t tok0 = b * tpt, ntok = min(tpt, s.lq - tok0);
         float lse[4], delta[4];
         int32_t seen[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int r = ty + 16 * i;
-            const bool live = r < ntok * a.group;
+            const bool live = rows.tk[i] < ntok;
             const int64_t at =
-                live ? static_cast<int64_t>(kh * a.group + r % a.group) * a.tq + s.q0 + tok0 + r / a.group : 0;
-            seen[i] = live ? attn_seen(a, s, tok0 + r / a.group) : 0;
+                live ? static_cast<int64_t>(kh * a.group + rows.head[i]) * a.tq + s.q0 + tok0 + rows.tk[i] : 0;
+            seen[i] = live ? attn_seen(a, s, tok0 + rows.tk[i]) : 0;
             lse[i] = live ? a.lse[at] : 0.0f;
             delta[i] = live ? a.delta[at] : 0.0f;
         }
         copies_wait<1>();  // the queries
         __syncthreads();
-        float x[4][4], dp[4][4];
-        products(x, qs, ks, pitch, a.D, tx, ty);
+        float x[4][8];
+        products<kN>(x, qs, ks, tx, ty);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bool on = j0 + tx + 16 * j < seen[i];
-                x[i][j] = on ? exp2f(fmaf(x[i][j], a.scale, -lse[i]) * kLog2e) : 0.0f;
-                ps[(ty + 16 * i) * kPP + tx + 16 * j] = x[i][j];
+            for (int j = 0; j < 8; ++j) {
+                const bool on = j0 + tx + 8 * j < seen[i];
+                ps[(ty + 16 * i) * kPP + tx + 8 * j] =
+                    on ? exp2f(fmaf(x[i][j], a.scale, -lse[i]) * kLog2e) : 0.0f;
             }
         copies_wait<0>();  // the gradients
         __syncthreads();
-        products(dp, gs, vs, pitch, a.D, tx, ty);
-        accumulate_t(ov, ps, gs, pitch, a.D, tx, ty);
+        accumulate_t<kN>(ov, ps, gs, tx, ty);
+        products<kN>(x, gs, vs, tx, ty);
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bool on = j0 + tx + 16 * j < seen[i];
-                ps[(ty + 16 * i) * kPP + tx + 16 * j] = on ? x[i][j] * (dp[i][j] - delta[i]) : 0.0f;
+            for (int j = 0; j < 8; ++j) {
+                float* p = ps + (ty + 16 * i) * kPP + tx + 8 * j;
+                *p = j0 + tx + 8 * j < seen[i] ? *p * (x[i][j] - delta[i]) : 0.0f;
             }
         __syncthreads();
-        accumulate_t(ok, ps, qs, pitch, a.D, tx, ty);
+        accumulate_t<kN>(ok, ps, qs, tx, ty);
         __syncthreads();
         if (b + 1 < b1) {
-            load_rows(qs, pitch, a.q, a, s, tok0 + tpt, min(tpt, s.lq - tok0 - tpt), kh);
-            load_rows(gs, pitch, a.g, a, s, tok0 + tpt, min(tpt, s.lq - tok0 - tpt), kh);
+            mine.rows<kN>(qs, a.q, a, s, tok0 + tpt, min(tpt, s.lq - tok0 - tpt), kh);
+            mine.rows<kN>(gs, a.g, a, s, tok0 + tpt, min(tpt, s.lq - tok0 - tpt), kh);
         }
     }
     copies_wait<0>();
@@ -435,32 +508,28 @@ __device__ __forceinline__ void grad_kv_block(const AttnArgs& a, float* sm, int3
         const int32_t j = j0 + ty * 4 + i;
         if (j >= s.room) continue;
         const int64_t row = s.k0 + j;
-#pragma unroll
-        for (int c = 0; c < kAcc; ++c) {
-            const int d = tx * 4 + 64 * c;
-            if (d >= a.D) continue;
-            const float4 k = make_float4(ok[i][c].x * a.scale, ok[i][c].y * a.scale, ok[i][c].z * a.scale, ok[i][c].w * a.scale);
-            if (a.kv_splits > 1) {
-                float* at = a.part_kv + ((static_cast<int64_t>(split) * 2 * a.tk + row) * a.hk + kh) * a.D + d;
-                *reinterpret_cast<float4*>(at) = k;
-                *reinterpret_cast<float4*>(at + static_cast<int64_t>(a.tk) * a.hk * a.D) = ov[i][c];
-            } else {
-                *reinterpret_cast<float4*>(static_cast<float*>(a.gk.p) + row * a.gk.st + kh * a.gk.sh + d) = k;
-                *reinterpret_cast<float4*>(static_cast<float*>(a.gv.p) + row * a.gv.st + kh * a.gv.sh + d) = ov[i][c];
-            }
+        float* to_k = static_cast<float*>(a.gk.p) + row * a.gk.st + kh * a.gk.sh;
+        float* to_v = static_cast<float*>(a.gv.p) + row * a.gv.st + kh * a.gv.sh;
+        if (a.kv_splits > 1) {
+            to_k = a.part_kv + ((static_cast<int64_t>(split) * 2 * a.tk + row) * a.hk + kh) * a.D;
+            to_v = to_k + static_cast<int64_t>(a.tk) * a.hk * a.D;
         }
+        store_row<kN>(to_k, ok[i], a.scale, a.D, tx);
+        store_row<kN>(to_v, ov[i], 1.0f, a.D, tx);
     }
 }
 
-// Grid: (key tiles * kv_splits + row tiles, key heads): the longer blocks first.
-__global__ void __launch_bounds__(kT) attn_backward_simt_kernel(const __grid_constant__ AttnArgs a, int32_t kv_blocks) {
+// Grid: (key tiles * kv_splits + row tiles) * key heads: the longer blocks first.
+template <int kN>
+__global__ void __launch_bounds__(kTT, 2)
+    attn_backward_simt_kernel(const __grid_constant__ AttnArgs a, int32_t kv_blocks) {
     extern __shared__ float sm[];
     dependency_wait();
-    const int32_t b = blockIdx.x;
+    const int32_t b = blockIdx.x / a.hk, kh = blockIdx.x - b * a.hk;
     if (b < kv_blocks)
-        grad_kv_block(a, sm, b / a.kv_splits, b % a.kv_splits, blockIdx.y);
+        grad_kv_block<kN>(a, sm, b / a.kv_splits, b % a.kv_splits, kh);
     else
-        grad_q_block(a, sm, b - kv_blocks, blockIdx.y);
+        grad_q_block<kN>(a, sm, b - kv_blocks, kh);
 }
 
 // grad_k (y 0) or grad_v (y 1): the shares' sums added in order, for the keys of a sequence.
@@ -568,25 +637,62 @@ __global__ void __launch_bounds__(kT) attn_delta_kernel(const __grid_constant__ 
 
 }  // namespace
 
-cudaError_t launch_attention_simt_forward(const AttnArgs& a, cudaStream_t st) {
-    const int smem = (3 * kR * (a.D + 4) + kR * kPP) * 4;
+namespace {
+
+template <int kN>
+cudaError_t launch_forward(const AttnArgs& a, cudaStream_t st) {
+    constexpr int smem = (3 * kR * pitch_of(kN) + kR * kPP) * 4;
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = attn_allow_smem(attn_forward_simt_kernel, (3 * kR * 132 + kR * kPP) * 4, done);  // head_dim 128
+    cudaError_t e = attn_allow_smem(attn_forward_simt_kernel<kN>, smem, done);
     if (e != cudaSuccess) return e;
-    return launch_dependent(attn_forward_simt_kernel, dim3(static_cast<unsigned>(a.tiles) * a.splits, static_cast<unsigned>(a.hk)),
-                            kT, smem, st, a);
+    return launch_dependent(attn_forward_simt_kernel<kN>,
+                            static_cast<unsigned>(a.tiles) * static_cast<unsigned>(a.splits) * static_cast<unsigned>(a.hk),
+                            kTT, smem, st, a);
+}
+
+template <int kN>
+cudaError_t launch_backward(const AttnArgs& a, int32_t kv, int32_t blocks, cudaStream_t st) {
+    constexpr int smem = (4 * kR * pitch_of(kN) + kR * kPP) * 4;
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = attn_allow_smem(attn_backward_simt_kernel<kN>, smem, done);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(attn_backward_simt_kernel<kN>, static_cast<unsigned>(blocks) * static_cast<unsigned>(a.hk), kTT, smem,
+                            st, a, kv);
+}
+
+}  // namespace
+
+// By sixteens of head_dim: the loops over a head's elements then have constant
+// bounds and shared memory holds no more than the head (at 40 and 72 elements
+// a power of two would compute on 1.6 and 1.8 times as many).
+cudaError_t launch_attention_simt_forward(const AttnArgs& a, cudaStream_t st) {
+    switch ((a.D + 15) / 16) {
+        case 1: return launch_forward<1>(a, st);
+        case 2: return launch_forward<2>(a, st);
+        case 3: return launch_forward<3>(a, st);
+        case 4: return launch_forward<4>(a, st);
+        case 5: return launch_forward<5>(a, st);
+        case 6: return launch_forward<6>(a, st);
+        case 7: return launch_forward<7>(a, st);
+        default: return launch_forward<8>(a, st);
+    }
 }
 
 cudaError_t launch_attention_simt_backward(const AttnArgs& a, cudaStream_t st) {
-    const int smem = (4 * kR * (a.D + 4) + kR * kPP) * 4;
-    static std::atomic<uint64_t> done{0};
-    cudaError_t e = attn_allow_smem(attn_backward_simt_kernel, (4 * kR * 132 + kR * kPP) * 4, done);  // head_dim 128
-    if (e != cudaSuccess) return e;
     const int32_t kv = static_cast<int32_t>(attn_tiles(a.tk, a.batch, kC)) * a.kv_splits;
     const int32_t blocks = kv + (a.tq > 0 ? a.tiles : 0);
     if (blocks == 0) return cudaSuccess;
-    e = launch_dependent(attn_backward_simt_kernel, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(a.hk)), kT, smem,
-                         st, a, kv);
+    cudaError_t e;
+    switch ((a.D + 15) / 16) {
+        case 1: e = launch_backward<1>(a, kv, blocks, st); break;
+        case 2: e = launch_backward<2>(a, kv, blocks, st); break;
+        case 3: e = launch_backward<3>(a, kv, blocks, st); break;
+        case 4: e = launch_backward<4>(a, kv, blocks, st); break;
+        case 5: e = launch_backward<5>(a, kv, blocks, st); break;
+        case 6: e = launch_backward<6>(a, kv, blocks, st); break;
+        case 7: e = launch_backward<7>(a, kv, blocks, st); break;
+        default: e = launch_backward<8>(a, kv, blocks, st); break;
+    }
     if (e != cudaSuccess || a.kv_splits == 1) return e;
     const int64_t rows = static_cast<int64_t>(a.tk) * a.hk;
     return launch_dependent(attn_kv_sum_kernel, dim3(static_cast<unsigned>((rows + kT / 32 - 1) / (kT / 32)), 2), kT, 0, st, a);

@@ -1,5 +1,5 @@
 // Device code shared by the tensor-core attention kernels: tensor maps of
-// packed row tiles and of key tiles, packed fp32 arithmetic, conversions.
+// packed row tiles and of key tiles, conversions.
 #pragma once
 
 #include <cuda.h>
@@ -13,7 +13,6 @@ namespace mdcn {
 
 constexpr int kAttnTcRows = kAttnTcBlockRows;       // rows of a tile: the MMA's M
 constexpr uint32_t kAtomBytes = 128 * 128;          // 64 elements of 128 rows
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Host: tensor maps with 64-element, 128-byte swizzled boxes; elements past
@@ -27,31 +26,6 @@ __device__ __forceinline__ float attn_exp2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-// Two fp32 values in one register pair: (lo, hi).
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
 }
 
 // (lo, hi) rounded to two 16-bit elements, lo in the low half.

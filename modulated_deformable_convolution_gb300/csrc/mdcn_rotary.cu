@@ -165,7 +165,10 @@ __device__ __forceinline__ PairFreq pair_freq(const RotaryArgs& a, int p) {
     return f;
 }
 
-// cos and sin of position * frequency.
+// cos and sin of position * frequency. For 16-bit tensors with the hardware's
+// functions, some 2^-20 off (the results are rounded to 2^-12 at best) and a
+// third of the instructions.
+template <typename T>
 __device__ __forceinline__ float2 pair_turn(int32_t pos, const PairFreq& f) {
     // the position in two parts that fp32 holds exactly
     const float pb = static_cast<float>(pos & 4095), pa = static_cast<float>(pos - (pos & 4095));
@@ -178,7 +181,10 @@ __device__ __forceinline__ float2 pair_turn(int32_t pos, const PairFreq& f) {
     float t = (ta + tb) + ((ea + eb) + (rest - rintf(rest)));
     t -= rintf(t);
     float2 cs;
-    sincospif(2.0f * t, &cs.y, &cs.x);
+    if constexpr (sizeof(T) == 2)
+        __sincosf(6.28318530717958648f * t, &cs.y, &cs.x);
+    else
+        sincospif(2.0f * t, &cs.y, &cs.x);
     return cs;
 }
 
@@ -229,6 +235,7 @@ enum RotaryMode {
 template <int kMode>
 struct alignas(16) WarpSmem {
     float2 cs[kMaxTurns];                             // (cos, sin) of the pairs of the warp's tokens
+    int32_t pos[4 * 32];                              // their positions, axis by axis
     float row[2][kMode == kAnywhere ? 32 * kE : 4];   // kAnywhere: the warp's rows, two in turn
 };
 
@@ -292,18 +299,34 @@ __device__ __forceinline__ void fill_freqs(const RotaryArgs& a, PairFreq* table)
     __syncthreads();
 }
 
-// The cosine of each pair, and its sine, of `n` tokens from `token` on into the
-// warp's shared memory.
-template <int kMode>
-__device__ __forceinline__ void turn_pairs(const RotaryArgs& a, int token, int n, const PairFreq* table,
+// The positions of the warp's next tokens (at most 32), on their way while it
+// works on others.
+struct Positions {
+    int32_t v[4];
+    __device__ __forceinline__ void load(const RotaryArgs& a, int64_t token, int n, int lane) {
+        const int32_t* p = a.pos + token * a.axes;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (lane + 32 * k < n * a.axes) v[k] = __ldg(p + lane + 32 * k);
+    }
+    __device__ __forceinline__ void put(int32_t* to, int count, int lane) const {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (lane + 32 * k < count) to[lane + 32 * k] = v[k];
+    }
+};
+
+// The cosine of each pair, and its sine, of the n tokens whose positions are at
+// `pos` into the warp's shared memory.
+template <typename T, int kMode>
+__device__ __forceinline__ void turn_pairs(const RotaryArgs& a, const int32_t* pos, int n, const PairFreq* table,
                                            WarpSmem<kMode>& w, int lane) {
-    const int32_t* pos = a.pos + static_cast<int64_t>(token) * a.axes;
     __syncwarp();
-    for (int i = 0; i < n; ++i, pos += a.axes)
-        for (int p = lane; p < a.pairs; p += 32) {
-            const PairFreq f = table[p];
-            w.cs[i * a.pairs + p] = pair_turn(__ldg(pos + f.axis), f);
-        }
+    for (int p = lane; p < a.pairs; p += 32) {
+        const PairFreq f = table[p];
+#pragma unroll 2
+        for (int i = 0; i < n; ++i) w.cs[i * a.pairs + p] = pair_turn<T>(pos[i * a.axes + f.axis], f);
+    }
     __syncwarp();
 }
 
@@ -391,6 +414,7 @@ struct Weights {
 // as zeros, so that the chunks that a lane lacks add nothing to its row's sums.
 template <typename T, int kMode>
 struct Forward {
+    using Type = T;
     static constexpr int kC = LaneSetup<kMode>::kC;
     static constexpr int kAhead = sizeof(T) == 4 ? 2 : (kMode == kAnywhere ? 4 : 3);
     static constexpr float kDirection = 1.0f;
@@ -469,6 +493,7 @@ struct Forward {
 
 template <typename T, int kMode>
 struct Backward {
+    using Type = T;
     static constexpr int kC = LaneSetup<kMode>::kC;
     static constexpr int kAhead = sizeof(T) == 4 ? 1 : 2;
     static constexpr float kDirection = -1.0f;
@@ -573,17 +598,20 @@ struct Backward {
 // All rows of q (t 0) or k (t 1), by warp `warp` of `warps`. Heads enough for
 // the warp's lane groups: a warp takes a token's heads (or a `parts`-th of
 // them), so many passes ahead in flight. Fewer: the lane groups take several
-// tokens' heads at once, the next blocks of tokens in flight.
+// tokens' heads at once, the next blocks of tokens in flight. The first loads
+// start before the block's frequencies are laid out.
 template <int kMode, typename Op>
 __device__ __forceinline__ void all_rows(const RotaryArgs& a, int heads, const LaneSetup<kMode>& L, Op& op,
-                                         const PairFreq* table, WarpSmem<kMode>& w, int64_t warp, int64_t warps) {
+                                         PairFreq* table, WarpSmem<kMode>& w, int64_t warp, int64_t warps) {
     constexpr int kAhead = Op::kAhead;
     typename Op::Buffers buf[kAhead];
+    Positions pos;
     int which = 0;
     const int rpw = L.rows_per_warp;
     if (heads * 2 > rpw) {
         const int64_t units = static_cast<int64_t>(a.tokens) * a.parts;
         const int share = ((heads + a.parts * rpw - 1) / (a.parts * rpw)) * rpw;  // whole warps' worth
+        fill_freqs(a, table);
         for (int64_t u = warp; u < units; u += warps) {
             const int token = static_cast<int>(u / a.parts), part = static_cast<int>(u % a.parts);
             const int h0 = part * share, h1 = min(h0 + share, heads);
@@ -594,7 +622,7 @@ __device__ __forceinline__ void all_rows(const RotaryArgs& a, int heads, const L
                 op.fetch(buf[k], ahead, h0 + k * rpw + L.row_in_warp < h1);
                 op.advance_in(ahead, rpw);
             }
-            turn_pairs(a, token, 1, table, w, L.lane);
+            turn_pairs<typename Op::Type>(a, a.pos + static_cast<int64_t>(token) * a.axes, 1, table, w, L.lane);
             const Turns<kMode> turns(a, L, w.cs, Op::kDirection);
             for (int hb = h0; hb < h1; hb += kAhead * rpw) {
 #pragma unroll
@@ -620,13 +648,21 @@ __device__ __forceinline__ void all_rows(const RotaryArgs& a, int heads, const L
         auto there = [&](int64_t b) { return b < blocks && mine < n && b * n + mine < a.tokens; };
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) op.fetch(buf[k], op.at(token_of(warp + k * warps), h), there(warp + k * warps));
+        // the tokens of block b that there are
+        auto count = [&](int64_t b) {
+            return b < blocks ? static_cast<int>(min(static_cast<int64_t>(n), a.tokens - b * n)) : 0;
+        };
+        pos.load(a, warp * n, count(warp), L.lane);
+        fill_freqs(a, table);
         for (int64_t b0 = warp; b0 < blocks; b0 += kAhead * warps) {
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 const int64_t b = b0 + k * warps, bn = b + kAhead * warps;
                 if (b >= blocks) break;
-                const int first = static_cast<int>(b * n);
-                turn_pairs(a, first, min(n, a.tokens - first), table, w, L.lane);
+                __syncwarp();
+                pos.put(w.pos, count(b) * a.axes, L.lane);
+                turn_pairs<typename Op::Type>(a, w.pos, count(b), table, w, L.lane);
+                pos.load(a, (b + warps) * n, count(b + warps), L.lane);
                 const Turns<kMode> turns(a, L, w.cs + (mine < n ? mine : 0) * a.pairs, Op::kDirection);
                 op.work(buf[k], op.at(token_of(b), h), there(b), turns, w.row[which],
                         [&] { op.fetch(buf[k], op.at(token_of(bn), h), there(bn)); });
@@ -643,7 +679,6 @@ __global__ void __launch_bounds__(kThreads, 2) rotary_forward_kernel(const __gri
     __shared__ PairFreq table[kMaxD / 2];
     const LaneSetup<kMode> L(a);
     dependency_wait();
-    fill_freqs(a, table);
     const int t = blockIdx.y;
     Forward<T, kMode> op(a, t, L);
     all_rows<kMode>(a, t ? a.rows - a.hq : a.hq, L, op, table, smem[threadIdx.x >> 5],
@@ -661,7 +696,6 @@ __global__ void __launch_bounds__(kBwdThreads, 3) rotary_backward_kernel(const _
     __shared__ float sums[kBwdWarps][kMaxD];
     const LaneSetup<kMode> L(a);
     dependency_wait();
-    fill_freqs(a, table);
     const int t = blockIdx.y;
     Backward<T, kMode> op(a, t, L);
     all_rows<kMode>(a, t ? a.rows - a.hq : a.hq, L, op, table, smem[threadIdx.x >> 5],

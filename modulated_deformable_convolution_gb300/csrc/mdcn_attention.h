@@ -27,11 +27,13 @@ struct AttnArgs {
     float* part_lse;                  // [splits][hq][tq]
     float* delta;                     // backward: [hq][tq]
     float* part_kv;                   // float32 backward, row tiles shared out: [kv_splits][grad_k, grad_v][tk][hk][D]
+    float* part_q;                    // float32 backward, key tiles shared out: [q_splits][tq][hq][D]
     int32_t batch, tq, tk, hq, hk, group, D;
     int32_t causal;
     float scale;
     int32_t splits;                   // blocks that share a row tile's keys
     int32_t kv_splits;                // float32 backward: blocks that share a key tile's rows
+    int32_t q_splits;                 // float32 backward: blocks that share a row tile's keys
     int32_t tiles;                    // row tiles of one key head at most (see attn_tiles)
 };
 

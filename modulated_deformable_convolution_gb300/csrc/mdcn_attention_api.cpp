@@ -201,13 +201,14 @@ AttnPlan attn_plan(const mdcn_attention_attrs& at, const mdcn_attention_dims& d,
 }
 
 // The backward's plan: where delta lies, and in float32 between how many blocks
-// the rows that see a key tile are shared out (the row tiles' own blocks run
-// beside them): as many as make three blocks to an SM, each with two row tiles at
-// least (2 sequences of 2048, 6 heads of 64 over 2: 972 us with one share, 771
-// with two, 702 with three, 728 with six).
+// the rows that see a key tile, and the keys that a row tile sees, are shared
+// out: as many as make three blocks of the first kind to an SM and six of the
+// second, each with two tiles at least. (Ragged sequences of up to 700, 6 heads
+// of 72 over 2: 374 us with neither shared, 146 with rows, 99 with both; 2
+// sequences of 2048, heads of 64: 972, 706 and 626.)
 struct AttnBwdPlan {
-    int64_t tiles, kv_splits;
-    size_t off_kv, bytes;
+    int64_t tiles, kv_splits, q_splits;
+    size_t off_kv, off_q, bytes;
 };
 
 AttnBwdPlan attn_bwd_plan(const mdcn_attention_dims& d, mdcn_dtype dtype) {
@@ -215,18 +216,26 @@ AttnBwdPlan attn_bwd_plan(const mdcn_attention_dims& d, mdcn_dtype dtype) {
     AttnBwdPlan p{};
     const int64_t tokens = mdcn::kAttnSimtRows / (d.q_heads / d.k_heads);
     p.tiles = mdcn::attn_tiles(d.q_tokens, d.batch, tokens);
-    p.kv_splits = 1;
+    p.kv_splits = p.q_splits = 1;
     size_t off = align256(mdcn::kAttnHeaderBytes + static_cast<size_t>(d.q_tokens) * static_cast<size_t>(d.q_heads) * 4);
-    const int64_t kv = mdcn::attn_tiles(d.k_tokens, d.batch, 64) * d.k_heads;
-    if (dtype == MDCN_F32 && kv > 0) {
-        int64_t s = 3 * kSms / kv;
-        const int64_t row_tiles = (d.q_tokens / d.batch + tokens - 1) / tokens;
-        if (s > row_tiles / 2) s = row_tiles / 2;
-        p.kv_splits = s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s;
+    if (dtype == MDCN_F32 && d.batch > 0) {
+        auto shares = [](int64_t blocks, int64_t wanted, int64_t steps) {
+            int64_t s = blocks > 0 ? wanted * kSms / blocks : 1;
+            if (s > steps / 2) s = steps / 2;
+            return s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s;
+        };
+        const int64_t row_tiles = (d.q_tokens / d.batch + tokens - 1) / tokens, key_tiles = (d.k_tokens / d.batch + 63) / 64;
+        p.kv_splits = shares(mdcn::attn_tiles(d.k_tokens, d.batch, 64) * d.k_heads, 3, row_tiles);
+        p.q_splits = shares(p.tiles * d.k_heads, 6, key_tiles);
         if (p.kv_splits > 1) {
             p.off_kv = off;
             off = align256(off + static_cast<size_t>(p.kv_splits) * 2 * static_cast<size_t>(d.k_tokens) *
                                      static_cast<size_t>(d.k_heads) * static_cast<size_t>(d.head_dim) * 4);
+        }
+        if (p.q_splits > 1) {
+            p.off_q = off;
+            off = align256(off + static_cast<size_t>(p.q_splits) * static_cast<size_t>(d.q_tokens) *
+                                     static_cast<size_t>(d.q_heads) * static_cast<size_t>(d.head_dim) * 4);
         }
     }
     p.bytes = off;
@@ -451,7 +460,7 @@ mdcn_status mdcn_attention_backward(const mdcn_attention_attrs* attrs, const mdc
         if (!aligned16(p)) return MDCN_ERR_ALIGN;
     const AttnBwdPlan p = attn_bwd_plan(*dims, dtype);
     if (p.tiles > kI31 / dims->k_heads ||
-        mdcn::attn_tiles(dims->k_tokens, dims->batch, 64) + p.tiles > kI31 / dims->k_heads / p.kv_splits)
+        mdcn::attn_tiles(dims->k_tokens, dims->batch, 64) * p.kv_splits + p.tiles * p.q_splits > kI31 / dims->k_heads)
         return MDCN_ERR_UNSUPPORTED;
     if (workspace_bytes < p.bytes) return MDCN_ERR_WORKSPACE;
     s = mdcn::api_check_device(nullptr);
@@ -467,7 +476,9 @@ mdcn_status mdcn_attention_backward(const mdcn_attention_attrs* attrs, const mdc
     a.delta = reinterpret_cast<float*>(ws + mdcn::kAttnHeaderBytes);
     a.tiles = static_cast<int32_t>(p.tiles);
     a.kv_splits = static_cast<int32_t>(p.kv_splits);
+    a.q_splits = static_cast<int32_t>(p.q_splits);
     if (p.kv_splits > 1) a.part_kv = reinterpret_cast<float*>(ws + p.off_kv);
+    if (p.q_splits > 1) a.part_q = reinterpret_cast<float*>(ws + p.off_q);
     cudaError_t e = mdcn::launch_attention_delta(dtype, a, st);
     if (e == cudaSuccess)
         e = dtype == MDCN_F32 ? mdcn::launch_attention_simt_backward(a, st)

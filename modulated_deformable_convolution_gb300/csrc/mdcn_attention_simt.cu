@@ -19,8 +19,8 @@
 // 16-bit parts), each with its own copy of the operands.
 // Measured: forward, 2 sequences of 2048, 8 heads of 64 over 4: 470 us, 36
 // TFLOP/s of about 78; 6 maps of up to 32 x 32, 8 heads of 40 over 4: 88 us. Backward, 4
-// ragged sequences of up to 700, 6 heads of 72 over 2: 142 us; 2 sequences of
-// 2048, 6 heads of 64 over 2: 702 us, 32 TFLOP/s of seven products.
+// ragged sequences of up to 700, 6 heads of 72 over 2: 99 us; 2 sequences of
+// 2048, 6 heads of 64 over 2: 626 us, 36 TFLOP/s of seven products.
 #include <cfloat>
 #include <cstdint>
 
@@ -353,9 +353,10 @@ __global__ void __launch_bounds__(kTT, kN <= 4 ? 3 : 2) attn_forward_simt_kernel
     }
 }
 
-// grad_q of one row tile.
+// grad_q of one row tile, or (a.q_splits > 1) the sum over a share of the key
+// tiles that it sees.
 template <int kN>
-__device__ __forceinline__ void grad_q_block(const AttnArgs& a, float* sm, int32_t index, int kh) {
+__device__ __forceinline__ void grad_q_block(const AttnArgs& a, float* sm, int32_t index, int32_t split, int kh) {
     const int tpt = kR / a.group;
     const AttnSeq s = attn_find(a, false, tpt, index);
     if (s.tile < 0) return;
@@ -367,13 +368,14 @@ __device__ __forceinline__ void grad_q_block(const AttnArgs& a, float* sm, int32
     float* ps = vs + kC * kPitch;
     const int32_t tok0 = s.tile * tpt, ntok = min(tpt, s.lq - tok0);
     const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
-    const int32_t ktiles = (attn_seen(a, s, tok0 + ntok - 1) + kC - 1) / kC;
+    const int32_t ktiles = (attn_seen(a, s, tok0 + ntok - 1) + kC - 1) / kC, per = (ktiles + a.q_splits - 1) / a.q_splits;
+    const int32_t t0 = min(split * per, ktiles), t1 = min(t0 + per, ktiles);
     const Copier mine(a.group);
-    mine.rows<kN>(qs, a.q, a, s, tok0, ntok, kh);
-    mine.rows<kN>(gs, a.g, a, s, tok0, ntok, kh);
-    if (ktiles > 0) {
-        mine.keys<kN>(ks, a.k, a, s, 0, kh);
-        mine.keys<kN>(vs, a.v, a, s, 0, kh);
+    if (t0 < t1) {
+        mine.rows<kN>(qs, a.q, a, s, tok0, ntok, kh);
+        mine.rows<kN>(gs, a.g, a, s, tok0, ntok, kh);
+        mine.keys<kN>(ks, a.k, a, s, t0 * kC, kh);
+        mine.keys<kN>(vs, a.v, a, s, t0 * kC, kh);
     }
     const Rows rows(ty, a.group);
     int32_t seen[4];
@@ -390,7 +392,7 @@ __device__ __forceinline__ void grad_q_block(const AttnArgs& a, float* sm, int32
         delta[i] = live ? a.delta[at] : 0.0f;
     }
 #pragma unroll 1
-    for (int32_t t = 0; t < ktiles; ++t) {
+    for (int32_t t = t0; t < t1; ++t) {
         copies_wait<1>();  // the keys
         __syncthreads();
         float x[4][8], dp[4][8];
@@ -410,7 +412,7 @@ __device__ __forceinline__ void grad_q_block(const AttnArgs& a, float* sm, int32
         __syncthreads();
         accumulate<kN>(o, ps, ks, tx, ty);
         __syncthreads();
-        if (t + 1 < ktiles) {
+        if (t + 1 < t1) {
             mine.keys<kN>(ks, a.k, a, s, (t + 1) * kC, kh);
             mine.keys<kN>(vs, a.v, a, s, (t + 1) * kC, kh);
         }
@@ -420,8 +422,10 @@ __device__ __forceinline__ void grad_q_block(const AttnArgs& a, float* sm, int32
     for (int i = 0; i < 4; ++i) {
         if (rows.tk[i] >= ntok) continue;
         const int64_t tok = s.q0 + tok0 + rows.tk[i];
-        store_row<kN>(static_cast<float*>(a.gq.p) + tok * a.gq.st + (kh * a.group + rows.head[i]) * a.gq.sh, o[i], a.scale,
-                      a.D, tx);
+        const int h = kh * a.group + rows.head[i];
+        float* to = a.q_splits > 1 ? a.part_q + ((static_cast<int64_t>(split) * a.tq + tok) * a.hq + h) * a.D
+                                   : static_cast<float*>(a.gq.p) + tok * a.gq.st + h * a.gq.sh;
+        store_row<kN>(to, o[i], a.scale, a.D, tx);
     }
 }
 
@@ -519,7 +523,7 @@ __device__ __forceinline__ void grad_kv_block(const AttnArgs& a, float* sm, int3
     }
 }
 
-// Grid: (key tiles * kv_splits + row tiles) * key heads: the longer blocks first.
+// Grid: (key tiles * kv_splits + row tiles * q_splits) * key heads.
 template <int kN>
 __global__ void __launch_bounds__(kTT, 2)
     attn_backward_simt_kernel(const __grid_constant__ AttnArgs a, int32_t kv_blocks) {
@@ -529,36 +533,43 @@ __global__ void __launch_bounds__(kTT, 2)
     if (b < kv_blocks)
         grad_kv_block<kN>(a, sm, b / a.kv_splits, b % a.kv_splits, kh);
     else
-        grad_q_block<kN>(a, sm, b - kv_blocks, kh);
+        grad_q_block<kN>(a, sm, (b - kv_blocks) / a.q_splits, (b - kv_blocks) % a.q_splits, kh);
 }
 
-// grad_k (y 0) or grad_v (y 1): the shares' sums added in order, for the keys of a sequence.
-__global__ void __launch_bounds__(kT) attn_kv_sum_kernel(const __grid_constant__ AttnArgs a) {
+// The shares' sums added in order: of kv_rows (key, head) grad_k, as many
+// grad_v, then of q_rows (token, head) grad_q; a warp to a row. Rows of no
+// sequence are not written.
+__global__ void __launch_bounds__(kT)
+    attn_grad_sum_kernel(const __grid_constant__ AttnArgs a, int64_t kv_rows, int64_t q_rows) {
     dependency_wait();
     const int lane = threadIdx.x & 31;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kT / 32) + (threadIdx.x >> 5);  // (key, head)
-    if (row >= static_cast<int64_t>(a.tk) * a.hk) return;
-    const int64_t key = row / a.hk;
-    const int kh = static_cast<int>(row - key * a.hk);
-    bool mine = false;  // keys of no sequence are not written
+    const int64_t index = static_cast<int64_t>(blockIdx.x) * (kT / 32) + (threadIdx.x >> 5);
+    if (index >= 2 * kv_rows + q_rows) return;
+    const int which = index < kv_rows ? 0 : index < 2 * kv_rows ? 1 : 2;  // grad_k, grad_v, grad_q
+    const bool of_q = which == 2;
+    const int64_t row = index - which * kv_rows;
+    const int heads = of_q ? a.hq : a.hk, shares = of_q ? a.q_splits : a.kv_splits;
+    const int64_t token = row / heads;
+    const int head = static_cast<int>(row - token * heads);
+    bool mine = false;
     for (int b = lane; b < a.batch; b += 32) {
         int32_t first, len;
-        attn_range(a.k_starts, b, a.tk, first, len);
-        mine = mine || (key >= first && key < first + len);
+        attn_range(of_q ? a.q_starts : a.k_starts, b, of_q ? a.tq : a.tk, first, len);
+        mine = mine || (token >= first && token < first + len);
     }
     if (!__any_sync(0xffffffffu, mine) || lane * 4 >= a.D) return;
-    const int64_t one = static_cast<int64_t>(a.tk) * a.hk * a.D;
-    const float* p = a.part_kv + blockIdx.y * one + row * a.D + lane * 4;
+    const int64_t one = static_cast<int64_t>(of_q ? a.tq : a.tk) * heads * a.D, step = of_q ? one : 2 * one;
+    const float* p = (of_q ? a.part_q : a.part_kv + which * one) + row * a.D + lane * 4;
     float4 sum = *reinterpret_cast<const float4*>(p);
-    for (int i = 1; i < a.kv_splits; ++i) {
-        const float4 v = *reinterpret_cast<const float4*>(p + 2 * i * one);
+    for (int i = 1; i < shares; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(p + i * step);
         sum.x += v.x;
         sum.y += v.y;
         sum.z += v.z;
         sum.w += v.w;
     }
-    const AttnTensor& t = blockIdx.y ? a.gv : a.gk;
-    *reinterpret_cast<float4*>(static_cast<float*>(t.p) + key * t.st + kh * t.sh + lane * 4) = sum;
+    const AttnTensor& t = of_q ? a.gq : which ? a.gv : a.gk;
+    *reinterpret_cast<float4*>(static_cast<float*>(t.p) + token * t.st + head * t.sh + lane * 4) = sum;
 }
 
 // out = sum over the shares of exp(lse_i - lse) out_i; 16 lanes per (token,
@@ -680,7 +691,7 @@ cudaError_t launch_attention_simt_forward(const AttnArgs& a, cudaStream_t st) {
 
 cudaError_t launch_attention_simt_backward(const AttnArgs& a, cudaStream_t st) {
     const int32_t kv = static_cast<int32_t>(attn_tiles(a.tk, a.batch, kC)) * a.kv_splits;
-    const int32_t blocks = kv + (a.tq > 0 ? a.tiles : 0);
+    const int32_t blocks = kv + (a.tq > 0 ? a.tiles * a.q_splits : 0);
     if (blocks == 0) return cudaSuccess;
     cudaError_t e;
     switch ((a.D + 15) / 16) {
@@ -693,9 +704,11 @@ cudaError_t launch_attention_simt_backward(const AttnArgs& a, cudaStream_t st) {
         case 7: e = launch_backward<7>(a, kv, blocks, st); break;
         default: e = launch_backward<8>(a, kv, blocks, st); break;
     }
-    if (e != cudaSuccess || a.kv_splits == 1) return e;
-    const int64_t rows = static_cast<int64_t>(a.tk) * a.hk;
-    return launch_dependent(attn_kv_sum_kernel, dim3(static_cast<unsigned>((rows + kT / 32 - 1) / (kT / 32)), 2), kT, 0, st, a);
+    const int64_t kv_rows = a.kv_splits > 1 ? static_cast<int64_t>(a.tk) * a.hk : 0;
+    const int64_t q_rows = a.q_splits > 1 ? static_cast<int64_t>(a.tq) * a.hq : 0;
+    if (e != cudaSuccess || 2 * kv_rows + q_rows == 0) return e;
+    return launch_dependent(attn_grad_sum_kernel, static_cast<unsigned>((2 * kv_rows + q_rows + kT / 32 - 1) / (kT / 32)), kT,
+                            0, st, a, kv_rows, q_rows);
 }
 
 cudaError_t launch_attention_join(int dtype, const AttnArgs& a, cudaStream_t st) {

@@ -182,6 +182,14 @@ def test_new_tokens_against_a_cache(dtype, new):
 
 
 @gpu
+@pytest.mark.parametrize("d", [8, 16, 32, 48, 56, 88, 112, 128])
+def test_float32_head_sizes_shared_out(d):
+    """Each length of the float32 kernels' loops over a head, whole and with
+    elements left over; keys and rows enough that both are shared out."""
+    _run(Problem(FS, [70, 300], [530, 300], 4, 2, d, d % 16 == 0, seed=d))
+
+
+@gpu
 @pytest.mark.parametrize("dtype", [BF, FS])
 def test_neighbours_do_not_leak(dtype):
     """What the next sequence holds (NaN, infinities) reaches no other."""

@@ -46,7 +46,7 @@ using One = std::integral_constant<int, 1>;
 // Stages of the ring: as many 128-row tiles as fit beside Q.
 __host__ __device__ constexpr int stages_of(int atoms) { return atoms == 2 ? 5 : 8; }
 __host__ __device__ constexpr int smem_of(int atoms) {
-    return 1024 + (2 + stages_of(atoms)) * atoms * static_cast<int>(kAtomBytes) + 768;
+    return (2 + stages_of(atoms)) * atoms * static_cast<int>(kAtomBytes) + 768;
 }
 
 // S buffers in tensor memory, which the steps of both row tiles use in turn.
@@ -74,10 +74,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     constexpr uint32_t S = stages_of(kAtoms);
     constexpr uint32_t kTile = kAtoms * kAtomBytes;
     constexpr uint32_t NB = scores_of(kAtoms);
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
-    const uint32_t base = (raw + 1023u) & ~1023u;
-    const uint32_t q_s = base, ring = base + 2 * kTile;
+    if (raw & 1023u) {  // the tiles' swizzle needs the alignment asked for above
+        if (threadIdx.x == 0) atomicOr(a.status, kStatusTimeout | kSiteSelftest);
+        return;
+    }
+    const uint32_t q_s = raw, ring = raw + 2 * kTile;
     const ItemQueue queue{ring + S * kTile};
     const uint32_t bars = queue.base + ItemQueue::kBytes;
     auto full = [&](uint32_t s) { return bars + 8u * s; };
@@ -429,19 +432,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         tc_fence_after();
                         const uint64_t c2 = pack2(corr, corr);
 #pragma unroll 1
-                        for (int c = 0; c < 2 * kAtoms; ++c) {
-                            uint32_t o[32];
-                            tmem_ld32_async(ocol + 32u * c, o);
-                            tmem_wait_ld();
-                            tmem_landed(o);
+                        for (int c = 0; c < 4 * kAtoms; ++c) {
+                            float o[16];
+                            uint32_t s[16];
+                            tmem_ld16(ocol + 16u * c, o);
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
+                            for (int i = 0; i < 16; i += 2) {
                                 float u, w;
-                                unpack2(mul2(pack2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), c2), u, w);
-                                o[i] = __float_as_uint(u);
-                                o[i + 1] = __float_as_uint(w);
+                                unpack2(mul2(pack2(o[i], o[i + 1]), c2), u, w);
+                                s[i] = __float_as_uint(u);
+                                s[i + 1] = __float_as_uint(w);
                             }
-                            tmem_st32(ocol + 32u * c, o);
+                            tmem_st16(ocol + 16u * c, s);
                         }
                     }
                 }
@@ -449,19 +451,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const uint64_t sc2 = pack2(sc, sc), m2 = pack2(-mm, -mm);
                 uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t p[32];
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t p[16];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int c = 2 * h + i / 16, o = 2 * (i % 16);
+                    for (int i = 0; i < 16; ++i) {
                         float u, w;
-                        unpack2(fma2(pack2(__uint_as_float(x[c][o]), __uint_as_float(x[c][o + 1])), sc2, m2), u, w);
+                        unpack2(fma2(pack2(__uint_as_float(x[c][2 * i]), __uint_as_float(x[c][2 * i + 1])), sc2, m2), u, w);
                         u = attn_exp2(u);
                         w = attn_exp2(w);
                         sum[i & 3] = add2(sum[i & 3], pack2(u, w));
                         p[i] = round2<kBf>(u, w);
                     }
-                    tmem_st32(scol + 32u * h, p);
+                    tmem_st16(scol + 16u * c, p);
                 }
                 tmem_wait_st();
                 tc_fence_before();

@@ -440,7 +440,8 @@ typedef struct mdcn_rotary_dims {
  *   t = positions[token][axis of the pair] * inv_freq[pair],
  * the pairs taking the axes in order, sections[0] of them the first. One
  * rounding to the type of y. The angle is reduced to a turn from the exact
- * product, so it keeps 32-bit precision at any position up to 2^24.
+ * product, so it keeps 32-bit precision at any position up to 2^24; its cosine
+ * and sine are those of float32, for 16-bit types within 2^-20.
  *   q [tokens][q_heads][head_dim], k_or_null likewise with k_heads;
  *   positions int32 [tokens][axes], inv_freq float32 [P], both contiguous;
  *   q_weight_or_null, k_weight_or_null [head_dim], the type of q (NULL: ones;
@@ -507,8 +508,9 @@ typedef struct mdcn_attention_dims {
  *   are clamped to them; rows of no sequence are not written;
  *   out (the type of q, not q itself), lse float32 [q_heads][q_tokens].
  * Keys and values past a sequence's last key are not used, whatever they hold
- * (infinities, NaN). Inside a sequence, the value of a key that a query must
- * not see yet reaches that query only as 0 * value, so it has to be finite.
+ * (infinities, NaN), nor is another sequence's content. Inside a sequence, the
+ * value of a key that a query must not see yet reaches that query only as
+ * 0 * value, so it has to be finite.
  * Few queries against many keys (new tokens of a decoder): the keys of a
  * sequence are shared out between blocks whose partial results are joined.
  * float16, bfloat16: products on the tensor cores, the probabilities rounded
@@ -531,11 +533,13 @@ mdcn_status mdcn_attention_forward(const mdcn_attention_attrs* attrs, const mdcn
  *   grad_v = p^T grad_out, ds = p * (grad_out . v - delta) * scale,
  *   grad_q = ds k, grad_k = ds^T q (summed over the query heads of a key head).
  * Keys past a sequence's last key (and queries that see no key) get gradient
- * 0; rows of no sequence are not written. Deterministic: grad_q and
- * (grad_k, grad_v) are computed by kernels of their own, each output by one
- * block, instead of with atomic additions. Arguments, alignment (strides of
- * all eight tensors) and errors as the forward's; q, k, v and out must not be
- * written to by the outputs. The workspace's first word is the call's status
+ * 0; rows of no sequence are not written. Inside a sequence q, k, v and
+ * grad_out have to be finite (what a query does not see enters its sums as 0
+ * times that), whatever other sequences and the room past the last key hold.
+ * Deterministic: grad_q and (grad_k, grad_v) are computed apart, every output
+ * summed in a fixed order, instead of with atomic additions. Arguments,
+ * alignment (strides of all eight tensors) and errors as the forward's; q, k,
+ * v and out must not be written to by the outputs. The workspace's first word is the call's status
  * word, as for the forward (mdcn_query_status). */
 mdcn_status mdcn_attention_backward_workspace_size(const mdcn_attention_attrs* attrs, const mdcn_attention_dims* dims,
                                                    mdcn_dtype dtype, size_t* bytes);

@@ -56,17 +56,20 @@ __device__ __forceinline__ __nv_bfloat16 attn_from_f<__nv_bfloat16>(float v) {
     return __float2bfloat16_rn(v);
 }
 
-// 4 consecutive elements as fp32 (16-byte aligned fp32, 8-byte aligned 16-bit).
+// 8 consecutive elements as fp32, 16-byte aligned.
 template <typename T>
-__device__ __forceinline__ float4 attn_load4(const T* p) {
+__device__ __forceinline__ void attn_load8(const T* p, float4 (&v)[2]) {
     if constexpr (sizeof(T) == 4) {
-        return *reinterpret_cast<const float4*>(p);
+        v[0] = reinterpret_cast<const float4*>(p)[0];
+        v[1] = reinterpret_cast<const float4*>(p)[1];
     } else {
-        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        const uint4 u = *reinterpret_cast<const uint4*>(p);
         const T* e = reinterpret_cast<const T*>(&u);
-        return make_float4(attn_to_f(e[0]), attn_to_f(e[1]), attn_to_f(e[2]), attn_to_f(e[3]));
+        v[0] = make_float4(attn_to_f(e[0]), attn_to_f(e[1]), attn_to_f(e[2]), attn_to_f(e[3]));
+        v[1] = make_float4(attn_to_f(e[4]), attn_to_f(e[5]), attn_to_f(e[6]), attn_to_f(e[7]));
     }
 }
+// 4 elements (16-byte aligned fp32, 8-byte aligned 16-bit).
 template <typename T>
 __device__ __forceinline__ void attn_store4(T* p, float4 v) {
     if constexpr (sizeof(T) == 4) {

@@ -160,10 +160,9 @@ struct PairFreq {
     int32_t axis;
 };
 
-__device__ __forceinline__ PairFreq pair_freq(const RotaryArgs& a, int p) {
+__device__ __forceinline__ PairFreq pair_freq(const RotaryArgs& a, int p, float freq) {
     constexpr float kHi = 0.15915494309189535f;                                        // 1 / (2 pi), rounded
     constexpr float kLo = static_cast<float>(0.15915494309189533577 - static_cast<double>(kHi));  // what is left
-    const float freq = a.freq[p];
     PairFreq f;
     f.hi = freq * kHi;
     f.lo = fmaf(freq, kHi, -f.hi) + freq * kLo;
@@ -301,10 +300,17 @@ struct LaneSetup {
 };
 
 // The block's table of pair frequencies (all threads; ends with a barrier).
-__device__ __forceinline__ void fill_freqs(const RotaryArgs& a, PairFreq* table) {
-    for (int p = threadIdx.x; p < a.pairs; p += blockDim.x) table[p] = pair_freq(a, p);
+// `mine` is the thread's, fetched at the kernel's start: of the first loads none
+// waits for another. (At most as many pairs as threads.)
+__device__ __forceinline__ float fetch_freq(const RotaryArgs& a) {
+    return threadIdx.x < a.pairs ? __ldg(a.freq + threadIdx.x) : 0.0f;
+}
+__device__ __forceinline__ void fill_freqs(const RotaryArgs& a, PairFreq* table, float mine) {
+    if (threadIdx.x < a.pairs) table[threadIdx.x] = pair_freq(a, threadIdx.x, mine);
     __syncthreads();
 }
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // The positions of the warp's next tokens (at most 32), on their way while it
 // works on others.
@@ -424,6 +430,7 @@ struct Forward {
     using Type = T;
     static constexpr int kC = LaneSetup<kMode>::kC;
     static constexpr int kAhead = sizeof(T) == 4 ? 2 : (kMode == kAnywhere ? 4 : 3);
+    static constexpr bool kForward = true;
     static constexpr float kDirection = 1.0f;
     struct Buffers {
         Pack<T> x[kC];
@@ -456,6 +463,11 @@ struct Forward {
     __device__ __forceinline__ At at(int64_t token, int64_t head) const {
         return {static_cast<const T*>(x.p) + token * x.st + head * x.sh + L.e0[0],
                 static_cast<T*>(y.p) + token * y.st + head * y.sh + L.e0[0]};
+    }
+    __device__ __forceinline__ void prefetch(const At& p) const {
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+            if (L.on[c]) prefetch_l2(p.in + (L.e0[c] - L.e0[0]));
     }
     __device__ __forceinline__ void advance_in(At& p, int heads) const { p.in += heads * x.sh; }
     __device__ __forceinline__ void advance_out(At& p, int heads) const { p.out += heads * y.sh; }
@@ -503,6 +515,7 @@ struct Backward {
     using Type = T;
     static constexpr int kC = LaneSetup<kMode>::kC;
     static constexpr int kAhead = sizeof(T) == 4 ? 1 : 2;
+    static constexpr bool kForward = false;
     static constexpr float kDirection = -1.0f;
     struct Buffers {
         Pack<T> g[kC], x[kC];
@@ -609,7 +622,8 @@ struct Backward {
 // start before the block's frequencies are laid out.
 template <int kMode, typename Op>
 __device__ __forceinline__ void all_rows(const RotaryArgs& a, int heads, const LaneSetup<kMode>& L, Op& op,
-                                         PairFreq* table, WarpSmem<kMode>& w, int64_t warp, int64_t warps) {
+                                         float freq, PairFreq* table, WarpSmem<kMode>& w, int64_t warp,
+                                         int64_t warps) {
     constexpr int kAhead = Op::kAhead;
     typename Op::Buffers buf[kAhead];
     Positions pos;
@@ -618,7 +632,17 @@ __device__ __forceinline__ void all_rows(const RotaryArgs& a, int heads, const L
     if (heads * 2 > rpw) {
         const int64_t units = static_cast<int64_t>(a.tokens) * a.parts;
         const int share = ((heads + a.parts * rpw - 1) / (a.parts * rpw)) * rpw;  // whole warps' worth
-        fill_freqs(a, table);
+        if constexpr (Op::kForward) {
+            // the first unit's rows and positions on their way to L2 (the backward, with
+            // more to a row, gains nothing: 109 us either way)
+            if (warp < units && L.on[0]) {
+                const int64_t token = warp / a.parts;
+                const int h = static_cast<int>(warp % a.parts) * share + L.row_in_warp;
+                if (h < heads) op.prefetch(op.at(token, h));
+                prefetch_l2(a.pos + token * a.axes);
+            }
+        }
+        fill_freqs(a, table, freq);
         for (int64_t u = warp; u < units; u += warps) {
             const int token = static_cast<int>(u / a.parts), part = static_cast<int>(u % a.parts);
             const int h0 = part * share, h1 = min(h0 + share, heads);
@@ -660,7 +684,7 @@ __device__ __forceinline__ void all_rows(const RotaryArgs& a, int heads, const L
             return b < blocks ? static_cast<int>(min(static_cast<int64_t>(n), a.tokens - b * n)) : 0;
         };
         pos.load(a, warp * n, count(warp), L.lane);
-        fill_freqs(a, table);
+        fill_freqs(a, table, freq);
         for (int64_t b0 = warp; b0 < blocks; b0 += kAhead * warps) {
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
@@ -686,9 +710,10 @@ __global__ void __launch_bounds__(kThreads, 2) rotary_forward_kernel(const __gri
     __shared__ PairFreq table[kMaxD / 2];
     const LaneSetup<kMode> L(a);
     dependency_wait();
+    const float freq = fetch_freq(a);
     const int t = blockIdx.y;
     Forward<T, kMode> op(a, t, L);
-    all_rows<kMode>(a, t ? a.rows - a.hq : a.hq, L, op, table, smem[threadIdx.x >> 5],
+    all_rows<kMode>(a, t ? a.rows - a.hq : a.hq, L, op, freq, table, smem[threadIdx.x >> 5],
                     static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5),
                     static_cast<int64_t>(gridDim.x) * kWarps);
 }
@@ -703,9 +728,10 @@ __global__ void __launch_bounds__(kBwdThreads, 3) rotary_backward_kernel(const _
     __shared__ float sums[kBwdWarps][kMaxD];
     const LaneSetup<kMode> L(a);
     dependency_wait();
+    const float freq = fetch_freq(a);
     const int t = blockIdx.y;
     Backward<T, kMode> op(a, t, L);
-    all_rows<kMode>(a, t ? a.rows - a.hq : a.hq, L, op, table, smem[threadIdx.x >> 5],
+    all_rows<kMode>(a, t ? a.rows - a.hq : a.hq, L, op, freq, table, smem[threadIdx.x >> 5],
                     static_cast<int64_t>(blockIdx.x) * kBwdWarps + (threadIdx.x >> 5),
                     static_cast<int64_t>(gridDim.x) * kBwdWarps);
     if (!a.part) return;

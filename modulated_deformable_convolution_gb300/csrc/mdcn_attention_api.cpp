@@ -142,10 +142,11 @@ mdcn_status attn_check(const mdcn_attention_attrs* at, const mdcn_attention_dims
 // step is some four times as long, several blocks share an SM and most calls
 // have few: the SMs' work, and one item's length at the end. The join of the
 // shares costs a launch and the partial results' way to memory and back.
-// (Measured: 4 maps of 80 x 80, 2 heads of 64: 112 us with one share, 104 with
-// three; 16 new tokens against up to 8192 keys: 90 with one, 81 with four; a
-// prompt of 1024 tokens, 32 heads: 28 with one, 40 with two; float32, 6 maps of
-// up to 32 x 32, 8 heads of 40: 118 with one, 88 with four, 91 with six.)
+// (Measured: 4 maps of 80 x 80, 2 heads of 64: 114 us with one share, 102 with
+// two, 97 with three, 110 with four; 16 new tokens against up to 8192 keys: 90
+// with one, 77 to 81 with two to eight; a prompt of 1024 tokens, 32 heads: 28
+// with one, 40 with two; float32, 6 maps of up to 32 x 32, 8 heads of 40: 118
+// with one, 88 with four, 91 with six.)
 struct AttnPlan {
     int64_t tiles, splits;
     size_t off_out, off_lse, bytes;
@@ -162,7 +163,11 @@ AttnPlan attn_plan(const mdcn_attention_attrs& at, const mdcn_attention_dims& d,
     const int64_t keys = tc ? 128 : 64;
     p.tiles = mdcn::attn_tiles(d.q_tokens, d.batch, tokens);
     p.splits = 1;
-    const int64_t blocks = p.tiles * d.k_heads;
+    // the tiles that there are at least: p.tiles has room for one more in each sequence
+    int64_t least = (d.q_tokens + tokens - 1) / tokens;
+    const int64_t sequences = d.batch < d.q_tokens ? d.batch : d.q_tokens;
+    if (least < sequences) least = sequences;
+    const int64_t blocks = least * d.k_heads;
     if (blocks > 0 && blocks <= 4 * kSms) {  // beyond, the last wave is a small part of the whole
         const double mean = static_cast<double>(d.k_tokens) / static_cast<double>(d.batch);
         const double own = at.causal ? static_cast<double>(d.q_tokens) / static_cast<double>(d.batch) / 2 : 0.0;

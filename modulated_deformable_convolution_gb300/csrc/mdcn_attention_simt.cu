@@ -14,13 +14,14 @@
 // instruction, on pairs of elements. Loops over a head have constant bounds, by
 // sixteens of D. Tiles are copied to shared memory asynchronously, each as soon
 // as the one before it has been used, and two or three blocks share an SM where
-// their tiles fit, so that one computes while another waits. Tensor cores
-// would need three products of reduced precision for one of fp32 (or six with
-// 16-bit parts), each with its own copy of the operands.
+// their tiles fit, so that one computes while another waits. Tensor cores would
+// need three products of TF32 parts for one of fp32, each with its own copy of
+// the operands, and leave products some 2^-22 off where fp32 rounds to 2^-24.
 // Measured: forward, 2 sequences of 2048, 8 heads of 64 over 4: 470 us, 36
-// TFLOP/s of about 78; 6 maps of up to 32 x 32, 8 heads of 40 over 4: 88 us. Backward, 4
-// ragged sequences of up to 700, 6 heads of 72 over 2: 99 us; 2 sequences of
-// 2048, 6 heads of 64 over 2: 626 us, 36 TFLOP/s of seven products.
+// TFLOP/s of the 70 that a large float32 matrix product reaches; 6 maps of up to
+// 32 x 32, 8 heads of 40 over 4: 77 us. Backward, 4 ragged sequences of up to 700,
+// 6 heads of 72 over 2: 94 us; 2 sequences of 2048, 6 heads of 64 over 2: 626 us,
+// 36 TFLOP/s of seven products.
 #include <cfloat>
 #include <cstdint>
 

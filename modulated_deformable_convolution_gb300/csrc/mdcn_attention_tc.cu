@@ -25,10 +25,10 @@
 // 8192 tokens 1109 us, 1510 TFLOP/s of the pairs that are seen; 4 x 8192 without a mask
 // 2640 us, 1665 TFLOP/s. A step of both row tiles takes about 2600 cycles, of
 // which the tensor pipe works 2048: with P over S, the next S waits for it. At
-// D = 64 (4 maps of 80 x 80, 2 heads, float16) 101 us, 833 TFLOP/s: some 2000
+// D = 64 (4 maps of 80 x 80, 2 heads, float16) 92 us, 912 TFLOP/s: some 2000
 // cycles a step; the exponentials of a warp's 64 pairs of columns alone take
 // 740 cycles, of two warps to a scheduler 630 each, the tensor pipe 1024. One
-// new token against 16 caches of up to 8192 keys: 64 us, 4.6 TB/s of keys and
+// new token against 16 caches of up to 8192 keys: 63 us, 4.6 TB/s of keys and
 // values.
 #include <cuda.h>
 #include <cudaTypedefs.h>

@@ -24,7 +24,7 @@
 // Measured with delta (bfloat16, 32 heads of 128 over 8): 9 packed causal prompts
 // of up to 6400 tokens 1482 us, 940 TFLOP/s of five products, 1315 of the seven;
 // 2 x 8192 without a mask 4.74 ms, 1160 and 1620. 16 maps of 32 x 32, 8 heads of
-// 64, float16: 147 us, 583 TFLOP/s of five products: at D = 64 the products of a
+// 64, float16: 143 us, 599 TFLOP/s of five products: at D = 64 the products of a
 // tile take half as long and its elementwise step as long as before (a grad_kv
 // block about 2130 cycles, exponentials 710, dS 510, loads and stores of tensor
 // memory and waits the rest; 16 elementwise warps instead of 8 changed nothing).

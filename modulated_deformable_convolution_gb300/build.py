@@ -82,7 +82,7 @@ def _binding_command(home: str, out: str):
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
     for p in inc:
         cmd += ["-isystem" if p != INCLUDE else "-I", p]
-    cmd += [BINDING_SOURCE, "-o", out, f"-L{lib}", f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch",
+    cmd += [BINDING_SOURCE, "-o", out, f"-L{lib}", f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch",
             "-ltorch_python"]
     return cmd, os.path.join(base, "version.py")
 

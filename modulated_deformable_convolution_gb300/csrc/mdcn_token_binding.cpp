@@ -11,7 +11,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -19,6 +19,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <optional>
 #include <stdexcept>
 #include <string>
 
@@ -101,8 +102,10 @@ struct Call {
             refuse(std::string(name) + " must be contiguous and on the device of the other tensors");
         return t.data_ptr();
     }
+    // From the caching allocator straight away: two outputs by way of the dispatcher take longer than
+    // the rest of a call.
     at::Tensor make(Shape shape, at::ScalarType t) const {
-        return at::empty(shape, at::TensorOptions().dtype(t).device(device));
+        return at::Tensor(at::detail::empty_cuda(shape, t, device, std::nullopt));
     }
     // The workspace given (None: none) where it has the bytes, else a new one; its address and size.
     void* workspace(PyObject* o, size_t need, at::Tensor& keep, size_t& bytes, bool grow) const {

@@ -38,15 +38,10 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     return r;
 }
 
-__device__ __forceinline__ float attn_to_f(float v) { return v; }
 __device__ __forceinline__ float attn_to_f(__half v) { return __half2float(v); }
 __device__ __forceinline__ float attn_to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 template <typename T>
 __device__ __forceinline__ T attn_from_f(float v);
-template <>
-__device__ __forceinline__ float attn_from_f<float>(float v) {
-    return v;
-}
 template <>
 __device__ __forceinline__ __half attn_from_f<__half>(float v) {
     return __float2half_rn(v);

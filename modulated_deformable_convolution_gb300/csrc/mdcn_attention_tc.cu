@@ -500,14 +500,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
                 for (int c = 0; c < a.D; c += 16) {
                     float v[16];
+                    __syncwarp();  // the stores part the lanes; the load needs the whole warp
                     if (any) tmem_ld16(ocol + static_cast<uint32_t>(c), v);
-                    if (!live) continue;
-                    // whole sectors: 32 bytes a store (head_dim is a multiple of 8)
+                    if (live) {
+                        // whole sectors: 32 bytes a store (head_dim is a multiple of 8)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = some ? v[i] * inv : 0.0f;
-                    store8(po + c, v);
-                    if (c + 8 < a.D) store8(po + c + 8, v + 8);
+                        for (int i = 0; i < 16; ++i) v[i] = some ? v[i] * inv : 0.0f;
+                        store8(po + c, v);
+                        if (c + 8 < a.D) store8(po + c + 8, v + 8);
+                    }
                 }
+                __syncwarp();
                 if (live) a.part_lse[(static_cast<int64_t>(it.split) * a.hq + h) * a.tq + tok] = lse;
             } else {
                 uint8_t* po = static_cast<uint8_t*>(a.out.p) + 2 * (tok * a.out.st + h * a.out.sh);
@@ -515,12 +518,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
                 for (int c = 0; c < a.D; c += 16) {
                     float v[16];
+                    __syncwarp();
                     if (any) tmem_ld16(ocol + static_cast<uint32_t>(c), v);
-                    if (!live) continue;
+                    if (live) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = some ? v[i] * inv : 0.0f;
-                    store16<kBf>(po + 2 * c, v, a.D - c, wide);
+                        for (int i = 0; i < 16; ++i) v[i] = some ? v[i] * inv : 0.0f;
+                        store16<kBf>(po + 2 * c, v, a.D - c, wide);
+                    }
                 }
+                __syncwarp();
                 if (live) a.lse[static_cast<int64_t>(h) * a.tq + tok] = lse;
             }
             if (any) {  // the next item's first product may overwrite O

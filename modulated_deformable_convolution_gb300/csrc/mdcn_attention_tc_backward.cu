@@ -80,12 +80,15 @@ __device__ __forceinline__ void store_row(uint32_t col, uint8_t* p, int c0, int 
 #pragma unroll 1
     for (int c = c0; c < c1; c += 16) {
         float v[16];
+        __syncwarp();  // the stores part the lanes; the load needs the whole warp
         if (any) tmem_ld16(col + static_cast<uint32_t>(c), v);
-        if (!live) continue;
+        if (live) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = any ? v[i] * f : 0.0f;
-        store16<kBf>(p + 2 * c, v, c1 - c, wide);
+            for (int i = 0; i < 16; ++i) v[i] = any ? v[i] * f : 0.0f;
+            store16<kBf>(p + 2 * c, v, c1 - c, wide);
+        }
     }
+    __syncwarp();
 }
 
 // d (+)= rows of x times rows of y over the head, both K-major; one thread.
@@ -357,6 +360,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (32 * c + i >= left) x[c][i] = dp[c][i] = 0u;
+                    __syncwarp();  // lanes differ in what they mask; the store below needs the whole warp
                 }
                 score_grads<kBf>(x, dp, [&](int) { return d2; }, ds);
                 // the sum before this step has read dS
@@ -726,6 +730,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
                             if (32 * c + k < lo || 32 * c + k >= hi) x[c][k] = 0u;
+                    __syncwarp();
                 }
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
@@ -748,6 +753,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
                             if (32 * c + k < lo || 32 * c + k >= hi) dp[c][k] = 0u;
+                    __syncwarp();
                 }
                 uint64_t d2[2];
                 score_grads<kBf>(
@@ -786,12 +792,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
             for (int c = 0; c < a.D; c += 16) {
                 float v[16];
+                __syncwarp();
                 if (any) tmem_ld16((half ? c_dk : c_dv) + lanes + static_cast<uint32_t>(c), v);
-                if (!live) continue;
+                if (live) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = used ? v[i] * f : 0.0f;
-                store16<kBf>(p + 2 * c, v, a.D - c, wide);
+                    for (int i = 0; i < 16; ++i) v[i] = used ? v[i] * f : 0.0f;
+                    store16<kBf>(p + 2 * c, v, a.D - c, wide);
+                }
             }
+            __syncwarp();
             if (any) {  // the next item's first sums may overwrite dV and dK
                 tc_fence_before();
                 __syncwarp();

@@ -14,6 +14,7 @@ tensors' type and e = 2^-24:
 The sums over many terms add (64 + terms / 64) e of the magnitudes' sum."""
 import ctypes
 import math
+import os
 
 import pytest
 import torch
@@ -187,6 +188,31 @@ def test_float32_head_sizes_shared_out(d):
     """Each length of the float32 kernels' loops over a head, whole and with
     elements left over; keys and rows enough that both are shared out."""
     _run(Problem(FS, [70, 300], [530, 300], 4, 2, d, d % 16 == 0, seed=d))
+
+
+@gpu
+@pytest.mark.parametrize("d", range(8, 136, 8))
+@pytest.mark.parametrize("dtype", [BF, FH])
+def test_every_head_size_with_partial_tiles(dtype, d):
+    """Row and key tiles of which some lanes of a warp have a row and others
+    none: one to eight turns of the loops that read results out."""
+    _run(Problem(dtype, [5, 131, 44], [133, 40, 44], 2, 1, d, d % 16 == 0, seed=d))
+
+
+def test_whole_warps_at_tensor_memory():
+    """A load of results from tensor memory is the whole warp's, and the stores
+    before it, in the loop's last turn, were those of the lanes that have a row: the
+    warp meets before each."""
+    csrc = os.path.join(os.path.dirname(_abi.__file__), "csrc")
+    loads = 0
+    for name in ("mdcn_attention_tc.cu", "mdcn_attention_tc_backward.cu"):
+        with open(os.path.join(csrc, name)) as f:
+            lines = [x.strip() for x in f]
+        for i, line in enumerate(lines):
+            if line.startswith("if (any) tmem_ld16("):
+                loads += 1
+                assert lines[i - 1].startswith("__syncwarp();"), (name, i + 1)
+    assert loads == 4
 
 
 @gpu

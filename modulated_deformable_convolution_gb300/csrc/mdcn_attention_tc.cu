@@ -497,17 +497,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const float lse = some ? fmaf(m, sc, log2f(l)) * kLn2 : -INFINITY;
             if (a.splits > 1) {
                 float* po = a.part_out + ((static_cast<int64_t>(it.split) * a.tq + tok) * a.hq + h) * a.D;
+                // rows lie a multiple of 32 bytes apart, so that all have the workspace's alignment: 16 at least
+                const bool wide = (reinterpret_cast<uintptr_t>(a.part_out) & 31u) == 0;
 #pragma unroll 1
                 for (int c = 0; c < a.D; c += 16) {
                     float v[16];
                     __syncwarp();  // the stores part the lanes; the load needs the whole warp
                     if (any) tmem_ld16(ocol + static_cast<uint32_t>(c), v);
                     if (live) {
-                        // whole sectors: 32 bytes a store (head_dim is a multiple of 8)
+                        // whole sectors where they can be (head_dim is a multiple of 8)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) v[i] = some ? v[i] * inv : 0.0f;
-                        store8(po + c, v);
-                        if (c + 8 < a.D) store8(po + c + 8, v + 8);
+                        store8(po + c, v, wide);
+                        if (c + 8 < a.D) store8(po + c + 8, v + 8, wide);
                     }
                 }
                 __syncwarp();

@@ -70,11 +70,17 @@ __device__ __forceinline__ void store16(void* p, const float (&v)[16], int n, bo
     if (n >= 16) st_global_v4(static_cast<uint8_t*>(p) + 16, make_uint4(r[4], r[5], r[6], r[7]));
 }
 
-// 8 fp32 values to a 32-byte aligned address.
-__device__ __forceinline__ void store8(float* p, const float* v) {
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
-                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-                 : "memory");
+// 8 fp32 values; `wide`: to a 32-byte aligned address (one store, a whole
+// sector), else to a 16-byte aligned one.
+__device__ __forceinline__ void store8(float* p, const float* v, bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]),
+                     "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                     : "memory");
+        return;
+    }
+    reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
 // ---------------------------------------------------------------- work items

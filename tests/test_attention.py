@@ -357,6 +357,38 @@ def test_gradient_against_differences():
         assert abs(terms.sum() - diff) <= 1e-5 * terms.abs().sum()
 
 
+def _on_16_bytes(need):
+    """A workspace of `need` bytes that starts on 16 but not on 32 bytes."""
+    ws = torch.full((need + 64,), 255, dtype=torch.uint8, device="cuda")
+    first = (16 - ws.data_ptr()) % 32
+    ws = ws[first:first + need]
+    assert ws.data_ptr() % 32 == 16
+    return ws
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF, FH, FS])
+@pytest.mark.parametrize("d", [40, 64, 128])
+def test_workspace_on_16_bytes(dtype, d):
+    """A workspace on the 16 bytes that are asked for and no more, with the
+    work shared out, gives the bits of one on 256."""
+    p = Problem(dtype, [2, 1, 3], [1500, 129, 700], 8, 2, d, True, room=[1600] * 3, seed=d)
+    q, k, v, g, qs, ks, kn = (p.cuda(x) for x in ("q", "k", "v", "g", "qs", "ks", "kn"))
+    kw = dict(k_lengths=kn, causal=True)
+    want, wlse = mdcn.attention(q, k, v, qs, ks, **kw)
+    need = mdcn.mdcn_attention_workspace_size(q, k, v, want, qs, ks, **kw)
+    assert need > 256  # there are partial results
+    out, lse = torch.empty_like(want), torch.empty_like(wlse)
+    mdcn.mdcn_attention_forward(q, k, v, qs, ks, out, lse, _on_16_bytes(need), **kw)
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
+    wg = mdcn.attention_backward(g, q, k, v, out, lse, qs, ks, **kw)
+    grads = [torch.empty_like(t) for t in (q, k, v)]
+    need = mdcn.mdcn_attention_backward_workspace_size(g, q, k, v, out, lse, qs, ks, *grads, **kw)
+    mdcn.mdcn_attention_backward(g, q, k, v, out, lse, qs, ks, *grads, _on_16_bytes(need), **kw)
+    for got, x in zip(grads, ("q", "k", "v")):
+        assert torch.equal(got, wg[x]), x
+
+
 # ---------------------------------------------------------------- refusals
 FAKE = 0x7F0000000000  # never dereferenced: each call below fails validation first
 

@@ -452,8 +452,9 @@ typedef struct mdcn_rotary_dims {
  * narrow to one element.
  * Errors: MDCN_ERR_NULL, MDCN_ERR_ATTR (attrs out of range, or a weight with
  * norm 0), MDCN_ERR_SHAPE, MDCN_ERR_DTYPE, MDCN_ERR_ALIGN,
- * MDCN_ERR_UNSUPPORTED (head_dim not a multiple of 8 up to 256, an extent
- * beyond 2^31-1), MDCN_ERR_ARCH, MDCN_ERR_CUDA. */
+ * MDCN_ERR_UNSUPPORTED (head_dim not a multiple of 8 up to 256, more than
+ * 2^31 - 2^17 heads of q and k together, an extent beyond 2^31-1), MDCN_ERR_ARCH,
+ * MDCN_ERR_CUDA. */
 mdcn_status mdcn_rotary_forward(const mdcn_rotary_attrs* attrs, const mdcn_rotary_dims* dims, mdcn_dtype dtype,
                                 const void* q, const void* k_or_null, const void* positions, const void* inv_freq,
                                 const void* q_weight_or_null, const void* k_weight_or_null, void* q_out,

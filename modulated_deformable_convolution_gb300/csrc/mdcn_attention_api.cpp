@@ -36,6 +36,11 @@ bool on16(const mdcn_strides& s, int64_t tokens, int64_t heads, int64_t size) {
 }
 
 // ---------------------------------------------------------------- rotary
+// Heads of q and k together at most: the kernels count a token's heads in 32
+// bits, and round them up to whole shares of whole warps (32 rows for each of
+// the 16 warps to an SM that may share a token) with some rows more ahead.
+constexpr int64_t kRotaryHeads = kI31 + 1 - (int64_t(1) << 17);
+
 mdcn_status rotary_check(const mdcn_rotary_attrs* at, const mdcn_rotary_dims* d, mdcn_dtype dtype, bool backward) {
     if (!at || !d) return MDCN_ERR_NULL;
     if (at->layout < 0 || at->layout > 2 || at->norm < 0 || at->norm > 1 || !(at->eps >= 0.0f) || !std::isfinite(at->eps))
@@ -43,8 +48,8 @@ mdcn_status rotary_check(const mdcn_rotary_attrs* at, const mdcn_rotary_dims* d,
     if (!dtype_ok(dtype)) return MDCN_ERR_DTYPE;
     if (d->tokens < 0 || d->q_heads < 1 || d->k_heads < 0 || d->head_dim < 1 || d->axes < 1 || d->axes > 4)
         return MDCN_ERR_SHAPE;
-    if (d->tokens > kI31 || d->q_heads > kI31 || d->k_heads > kI31 || d->q_heads + d->k_heads > kI31 ||
-        d->head_dim > 256 || d->head_dim % 8 != 0)
+    if (d->tokens > kI31 || d->q_heads > kRotaryHeads || d->k_heads > kRotaryHeads ||
+        d->q_heads + d->k_heads > kRotaryHeads || d->head_dim > 256 || d->head_dim % 8 != 0)
         return MDCN_ERR_UNSUPPORTED;
     int64_t pairs = 0;
     for (int a = 0; a < 4; ++a) {

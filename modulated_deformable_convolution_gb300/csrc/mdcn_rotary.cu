@@ -629,7 +629,7 @@ __device__ __forceinline__ void all_rows(const RotaryArgs& a, int heads, const L
     Positions pos;
     int which = 0;
     const int rpw = L.rows_per_warp;
-    if (heads * 2 > rpw) {
+    if (heads > rpw / 2) {
         const int64_t units = static_cast<int64_t>(a.tokens) * a.parts;
         const int share = ((heads + a.parts * rpw - 1) / (a.parts * rpw)) * rpw;  // whole warps' worth
         if constexpr (Op::kForward) {

@@ -295,6 +295,20 @@ def test_refuses_dims(lib, kw, status):
     assert _fwd(lib, _attrs(), _dims(**kw)) == status
 
 
+MOST = 2**31 - 2**17  # heads that the kernels can count
+
+
+@pytest.mark.parametrize("q_heads,k_heads", [(MOST + 1, 0), (MOST, 1), (1, MOST), (2**31 - 1, 0), (2**30, 2**30 - 1), (2**30, 2**30)])
+def test_refuses_more_heads_than_the_kernels_count(lib, q_heads, k_heads):
+    d = _dims(q_heads=q_heads, k_heads=k_heads, head_dim=8, sections=(2, 2, 0, 0))
+    assert _fwd(lib, _attrs(), d) == _abi.MDCN_ERR_UNSUPPORTED
+    n = ctypes.c_size_t()
+    size = lambda: lib.mdcn_rotary_backward_workspace_size(ctypes.byref(_attrs()), ctypes.byref(d), _abi.MDCN_F16, ctypes.byref(n))  # noqa: E731
+    assert size() == _abi.MDCN_ERR_UNSUPPORTED
+    d.q_heads, d.k_heads = MOST - 1, 1
+    assert size() == _abi.MDCN_OK
+
+
 def test_refuses_attrs_pointers_and_types(lib):
     d = _dims()
     for a in (_attrs(layout=3), _attrs(layout=-1), _attrs(norm=2), _attrs(eps=-1.0), _attrs(eps=math.inf), _attrs(eps=math.nan)):

@@ -87,10 +87,12 @@ struct AttnSeq {
     int32_t room;    // keys the sequence has rows for
 };
 
-// Rows [start, end) of sequence b, clamped to the tensor.
+// Rows [start, end) of sequence b, clamped to the tensor. Plain loads, here and
+// wherever a kernel reads after dependency_wait(): the compiler keeps them
+// behind it, which it need not do with read-only ones (__ldg).
 __device__ __forceinline__ void attn_range(const int32_t* starts, int b, int32_t total, int32_t& first, int32_t& len) {
-    const int32_t s = min(max(__ldg(starts + b), 0), total);
-    const int32_t e = min(max(__ldg(starts + b + 1), s), total);
+    const int32_t s = min(max(starts[b], 0), total);
+    const int32_t e = min(max(starts[b + 1], s), total);
     first = s;
     len = e - s;
 }
@@ -127,7 +129,7 @@ __device__ __forceinline__ AttnSeq attn_find(const AttnArgs& a, bool by_keys, in
             s.tile = by_keys ? left - before : tiles - 1 - (left - before);
             attn_range(a.q_starts, b, a.tq, s.q0, s.lq);
             attn_range(a.k_starts, b, a.tk, s.k0, s.room);
-            s.lk = a.k_lengths ? min(max(__ldg(a.k_lengths + b), 0), s.room) : s.room;
+            s.lk = a.k_lengths ? min(max(a.k_lengths[b], 0), s.room) : s.room;
             return s;
         }
         left -= __shfl_sync(0xffffffffu, sum, 31);

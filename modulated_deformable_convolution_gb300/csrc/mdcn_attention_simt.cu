@@ -552,7 +552,7 @@ __device__ __forceinline__ void token_head(int64_t row, int heads, int64_t& toke
 
 // Whether a sequence has the row: they lie side by side from the first's start to the last's end.
 __device__ __forceinline__ bool of_a_sequence(const int32_t* starts, int32_t batch, int64_t token) {
-    return token >= __ldg(starts) && token < __ldg(starts + batch);
+    return token >= starts[0] && token < starts[batch];
 }
 
 template <int kLanes>

@@ -1,7 +1,9 @@
 // Launch that may overlap the end of the kernel before it on the stream
 // (programmatic dependent launch): the kernel's set-up runs early, and
 // dependency_wait() comes before its first access to memory that others write
-// or read.
+// or read. Reads behind it are plain loads: a read-only load (__ldg, or a const
+// __restrict__ parameter) is taken to give the same value anywhere in the
+// kernel, so that the compiler may move it ahead of the wait.
 #pragma once
 
 #include <cuda_runtime.h>

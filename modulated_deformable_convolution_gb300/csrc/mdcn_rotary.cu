@@ -303,7 +303,7 @@ struct LaneSetup {
 // `mine` is the thread's, fetched at the kernel's start: of the first loads none
 // waits for another. (At most as many pairs as threads.)
 __device__ __forceinline__ float fetch_freq(const RotaryArgs& a) {
-    return threadIdx.x < a.pairs ? __ldg(a.freq + threadIdx.x) : 0.0f;
+    return threadIdx.x < a.pairs ? a.freq[threadIdx.x] : 0.0f;
 }
 __device__ __forceinline__ void fill_freqs(const RotaryArgs& a, PairFreq* table, float mine) {
     if (threadIdx.x < a.pairs) table[threadIdx.x] = pair_freq(a, threadIdx.x, mine);
@@ -320,7 +320,7 @@ struct Positions {
         const int32_t* p = a.pos + token * a.axes;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (lane + 32 * k < n * a.axes) v[k] = __ldg(p + lane + 32 * k);
+            if (lane + 32 * k < n * a.axes) v[k] = p[lane + 32 * k];
     }
     __device__ __forceinline__ void put(int32_t* to, int count, int lane) const {
 #pragma unroll

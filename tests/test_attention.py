@@ -389,6 +389,24 @@ def test_workspace_on_16_bytes(dtype, d):
         assert torch.equal(got, wg[x]), x
 
 
+def test_dependent_kernels_wait_before_they_read():
+    """Kernels that may start before the one ahead of them has ended wait for
+    it, and hold no read-only load, which the compiler may move above the wait."""
+    csrc = os.path.join(os.path.dirname(_abi.__file__), "csrc")
+    kernels = 0
+    for name in sorted(os.listdir(csrc)):
+        with open(os.path.join(csrc, name)) as f:
+            code = "\n".join(x.split("//")[0] for x in f.read().splitlines())
+        if not name.endswith((".cu", ".cuh")) or "dependency_wait()" not in code and name != "mdcn_attention.cuh":
+            continue
+        for word in ("__ldg(", "__restrict__", "ld.global.nc"):
+            assert word not in code, (name, word)
+        for body in code.split("__global__")[1:]:
+            kernels += 1
+            assert "dependency_wait();" in body.split("\n}\n")[0], name
+    assert kernels == 11
+
+
 # ---------------------------------------------------------------- refusals
 FAKE = 0x7F0000000000  # never dereferenced: each call below fails validation first
 

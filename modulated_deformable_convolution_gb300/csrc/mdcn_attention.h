@@ -35,6 +35,7 @@ struct AttnArgs {
     int32_t kv_splits;                // float32 backward: blocks that share a key tile's rows
     int32_t q_splits;                 // float32 backward: blocks that share a row tile's keys
     int32_t tiles;                    // row tiles of one key head at most (see attn_tiles)
+    uint64_t item_limit;              // tensor-core kernels: cycles to wait for an item's end at most
 };
 
 // Row tiles hold the query heads of one key head together: row r of a tile is
@@ -71,6 +72,13 @@ cudaError_t launch_attention_simt_backward(const AttnArgs& a, cudaStream_t st);
 // Tensor-core kernels (float16, bfloat16; 128 rows x 128 keys, two row tiles to
 // a block).
 constexpr int kAttnTcBlockRows = 128;
+// Cycles that a role may wait for another to finish an item of `steps` tiles
+// (or two of them): the limit of a pipeline's step, and for each tile some 40
+// times what one was measured to take.
+constexpr uint64_t kAttnStepLimitCycles = 100000;
+constexpr uint64_t attn_item_limit(uint64_t step_limit, int64_t steps) {
+    return step_limit + static_cast<uint64_t>(steps) * kAttnStepLimitCycles;
+}
 cudaError_t launch_attention_tc_forward(int dtype, const AttnArgs& a, cudaStream_t st);
 cudaError_t launch_attention_tc_backward(int dtype, const AttnArgs& a, cudaStream_t st);
 

@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         return;
     }
     const uint32_t q_s = raw, ring = raw + 2 * kTile;
-    const ItemQueue queue{ring + S * kTile};
+    const ItemQueue queue{ring + S * kTile, a.item_limit};
     const uint32_t bars = queue.base + ItemQueue::kBytes;
     auto full = [&](uint32_t s) { return bars + 8u * s; };
     auto empty = [&](uint32_t s) { return bars + 8u * (S + s); };
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 e += 2u * nmax;
                 if (valid >= kKeys) return true;
                 // the issuing thread has seen the tile arrive
-                if (!warp_wait2(to_clear, 0u, turn, abort_flag, a.status, kSiteTmaEmpty)) return false;
+                if (!warp_wait2(to_clear, 0u, turn, abort_flag, a.status, kSiteTmaEmpty, a.item_limit)) return false;
                 turn ^= 1u;
                 zero_rows(ring + st * kTile, kAtoms, kAtomBytes, valid, kKeys);
                 if (lane == 0) mbar_arrive(cleared);
@@ -393,7 +393,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             float m = -INFINITY, l = 0.0f;
             const int nt = t ? it.n1 : it.n0;
             for (int32_t j = 0; j < nt; ++j) {
-                if (!warp_wait2(s_full(t, done), 0u, (done / NB) & 1u, abort_flag, a.status, kSiteGatherEmpty))
+                // an item of the other row tile alone may come before this one's first S
+                if (!warp_wait2(s_full(t, done), 0u, (done / NB) & 1u, abort_flag, a.status, kSiteGatherEmpty,
+                                a.item_limit))
                     return false;
                 tc_fence_after();
                 const uint32_t scol = s_col(score_buffer<kAtoms>(t, j, it.n0, it.n1, g)) + lanes;
@@ -615,7 +617,9 @@ bool attn_encode_keys(CUtensorMap* m, const AttnArgs& a, const AttnTensor& t, in
     return encode(m, base, 3, dims, strides, box, dtype);
 }
 
-cudaError_t launch_attention_tc_forward(int dtype, const AttnArgs& a, cudaStream_t st) {
+cudaError_t launch_attention_tc_forward(int dtype, const AttnArgs& args, cudaStream_t st) {
+    AttnArgs a = args;
+    a.item_limit = attn_item_limit(kWaitLimitCycles, a.tk / kKeys + 1);
     if (a.D <= 64)
         return dtype == kBF16 ? launch_forward<1, true>(dtype, a, st) : launch_forward<1, false>(dtype, a, st);
     return dtype == kBF16 ? launch_forward<2, true>(dtype, a, st) : launch_forward<2, false>(dtype, a, st);

@@ -102,10 +102,12 @@ struct alignas(16) AttnItem {
 };
 static_assert(sizeof(AttnItem) == 64, "four vectors");
 
-// Shared memory of the item queue, at 16-byte aligned `base`.
+// Shared memory of the item queue, at 16-byte aligned `base`. `limit`: a role
+// that has nothing to do in an item waits for the others to finish it.
 struct ItemQueue {
     static constexpr uint32_t kBytes = 2 * 64 + 16 + 5 * 8 + 8;
     uint32_t base;
+    uint64_t limit;
     __device__ __forceinline__ uint32_t slot(uint32_t i) const { return base + 64u * i; }
     __device__ __forceinline__ uint32_t answer() const { return base + 128u; }
     __device__ __forceinline__ uint32_t full(uint32_t i) const { return base + 144u + 8u * i; }
@@ -148,7 +150,7 @@ template <typename F>
 __device__ __forceinline__ void for_items(const ItemQueue& q, volatile int* abort_flag, uint32_t* status, F body) {
     for (uint32_t i = 0;; ++i) {
         const uint32_t s = i & 1u;
-        if (!warp_wait2(q.full(s), 0u, (i >> 1) & 1u, abort_flag, status, kSiteEpilogue)) return;
+        if (!warp_wait2(q.full(s), 0u, (i >> 1) & 1u, abort_flag, status, kSiteEpilogue, q.limit)) return;
         const AttnItem it = read_item(q.slot(s));
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(q.empty(s));
@@ -161,7 +163,7 @@ template <typename F>
 __device__ __forceinline__ void for_items_one(const ItemQueue& q, volatile int* abort_flag, uint32_t* status, F body) {
     for (uint32_t i = 0;; ++i) {
         const uint32_t s = i & 1u;
-        if (!mbar_wait_bounded(q.full(s), (i >> 1) & 1u, abort_flag, status, kSiteEpilogue)) return;
+        if (!mbar_wait_bounded(q.full(s), (i >> 1) & 1u, abort_flag, status, kSiteEpilogue, q.limit)) return;
         const AttnItem it = read_item(q.slot(s));
         mbar_arrive(q.empty(s));
         if (!it.go || !body(it)) return;
@@ -186,7 +188,7 @@ __device__ __forceinline__ void serve_items(const ItemQueue& q, volatile int* ab
         it.go = there ? 1 : 0;
         if (there || index < 0) {
             const uint32_t s = out & 1u;
-            if (!warp_wait2(q.empty(s), 0u, ((out >> 1) & 1u) ^ 1u, abort_flag, status, kSiteTmaEmpty)) {
+            if (!warp_wait2(q.empty(s), 0u, ((out >> 1) & 1u) ^ 1u, abort_flag, status, kSiteTmaEmpty, q.limit)) {
                 if (index >= 0) {  // the answer asked for lands before the block exits
                     volatile int never = 0;
                     warp_wait_bounded(q.asked(), i & 1u, &never, status, kSiteDrain, 200000000ull);

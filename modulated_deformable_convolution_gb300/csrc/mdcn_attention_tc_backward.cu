@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
     const uint32_t q_s = base, g_s = base + kTile, ring = base + 2 * kTile;
-    const ItemQueue queue{ring + S * kTile};
+    const ItemQueue queue{ring + S * kTile, a.item_limit};
     const uint32_t bars = queue.base + ItemQueue::kBytes;
     auto full = [&](uint32_t s) { return bars + 8u * s; };
     auto empty = [&](uint32_t s) { return bars + 8u * (S + s); };
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 e += 2u * it.n0;
                 if (valid >= kKeys) return true;
                 // the issuing thread has seen the tile arrive
-                if (!warp_wait2(to_clear, 0u, turn, abort_flag, a.status, kSiteTmaEmpty)) return false;
+                if (!warp_wait2(to_clear, 0u, turn, abort_flag, a.status, kSiteTmaEmpty, a.item_limit)) return false;
                 turn ^= 1u;
                 zero_rows(ring + st * kTile, kAtoms, kAtomBytes, valid, kKeys);
                 if (lane == 0) mbar_arrive(cleared);
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     const uint32_t k_s = raw, v_s = raw + kTile, q_ring = raw + 2 * kTile, g_ring = q_ring + SQ * kTile;
     const uint32_t stats = g_ring + SG * kTile;  // per stage: 128 x (8 - lse'), 128 x (-delta 2^-8)
-    const ItemQueue queue{stats + ST * 1024u};
+    const ItemQueue queue{stats + ST * 1024u, a.item_limit};
     const uint32_t bars = queue.base + ItemQueue::kBytes;
     auto q_full = [&](uint32_t s) { return bars + 8u * s; };
     auto q_empty = [&](uint32_t s) { return bars + 8u * (SQ + s); };
@@ -850,7 +850,10 @@ cudaError_t launch_backward(int dtype, const AttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_attention_tc_backward(int dtype, const AttnArgs& a, cudaStream_t st) {
+cudaError_t launch_attention_tc_backward(int dtype, const AttnArgs& args, cudaStream_t st) {
+    AttnArgs a = args;
+    const int64_t row_steps = a.tq / (kAttnTcRows / a.group) + 1, key_steps = a.tk / kKeys + 1;
+    a.item_limit = attn_item_limit(kWaitLimitCycles, row_steps > key_steps ? row_steps : key_steps);
     if (a.D <= 64)
         return dtype == kBF16 ? launch_backward<1, true>(dtype, a, st) : launch_backward<1, false>(dtype, a, st);
     return dtype == kBF16 ? launch_backward<2, true>(dtype, a, st) : launch_backward<2, false>(dtype, a, st);

@@ -19,11 +19,13 @@ constexpr uint32_t kSiteDrain = 1u << 13;
 constexpr uint32_t kSiteSelftest = 1u << 14;
 constexpr uint32_t kSiteSplitWait = 1u << 15;
 
-// Limit of every pipeline wait in the fused kernel, in SM clock cycles
-// (4e9 cycles: about 2 s at the 2.07 GHz maximum clock, longer at lower
-// clocks). A correct launch never waits more than microseconds; the limit
-// only bounds a bug. The cycle counter is read every 64 polls, so a wait
-// that completes is noticed after one mbarrier test, not after a timer read.
+// Limit of every pipeline wait, in SM clock cycles (4e9 cycles: about 2 s at
+// the 2.07 GHz maximum clock, longer at lower clocks). A correct launch waits
+// microseconds for a pipeline's next step; the limit only bounds a bug. Where
+// a role waits for a whole work item of the attention kernels, the item's
+// steps add to it (AttnArgs::item_limit). The cycle counter is read every 64
+// polls, so a wait that completes is noticed after one mbarrier test, not
+// after a timer read.
 constexpr uint64_t kWaitLimitCycles = 4000000000ull;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

@@ -1,6 +1,7 @@
 """The example that runs the deformable layer and the token operators together,
 and sizes whose offsets pass 32 bits."""
 import importlib.util
+import math
 import os
 
 import pytest
@@ -85,3 +86,27 @@ def test_offsets_beyond_32_bits(dtype):
     pos = torch.zeros(tokens, 1, dtype=torch.int32, device="cuda")
     yq, _ = mdcn.rotary(kv, None, pos, mdcn.rotary_frequencies((64,)), (64,), q_out=kv)  # angle 0: unchanged
     assert torch.equal(mdcn.attention(q[1:], yq[-n:], yq[-n:], mdcn.sequence_starts([1]), mdcn.sequence_starts([n]), k_lengths=used[1:].clone(), causal=True)[0], own)
+
+
+def test_an_item_longer_than_a_wait_may_be():
+    """One query against 400 million keys: its gradient is one work item of some
+    three seconds, and the roles that have nothing to do in it (the one that
+    clears the last tile's tail, the one that gets items) wait that long. All
+    keys score 0, so that every probability is 1 / n; 1000 of them, the first
+    and the last among these, have a value and a key of ones."""
+    n, d, step = 400_000_005, 8, 400_000
+    ones = torch.cat([torch.arange(0, n, step, device="cuda")[:999], torch.tensor([n - 1], device="cuda")])
+    k = torch.zeros(n, 1, d, dtype=torch.bfloat16, device="cuda")
+    k[ones] = 1
+    q, g = torch.zeros(1, 1, d, dtype=k.dtype, device="cuda"), torch.ones(1, 1, d, dtype=k.dtype, device="cuda")
+    out, lse = torch.zeros_like(q), torch.full((1, 1), math.log(n), device="cuda")
+    qs, ks = mdcn.sequence_starts([1]), mdcn.sequence_starts([n])
+    gq, gk, gv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(k)
+    ws = torch.empty(mdcn.mdcn_attention_backward_workspace_size(g, q, k, k, out, lse, qs, ks, gq, gk, gv), dtype=torch.uint8, device="cuda")
+    mdcn.mdcn_attention_backward(g, q, k, k, out, lse, qs, ks, gq, gk, gv, ws)
+    assert mdcn.mdcn_query_status(ws) == (0, 0)
+    # p is rounded once, ds once, each result once; lse, near 20, is off by 2^-20 in fp32
+    p, tol = 1 / n, 4 * 2.0**-8
+    assert ((gq.double() / (1000 * p * d * d**-0.5) - 1).abs() <= tol).all()
+    assert ((gv.float().amin() / p - 1).abs() <= tol) and ((gv.float().amax() / p - 1).abs() <= tol)
+    assert (gk == 0).all()

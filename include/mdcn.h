@@ -538,7 +538,10 @@ mdcn_status mdcn_attention_forward(const mdcn_attention_attrs* attrs, const mdcn
  * grad_out have to be finite (what a query does not see enters its sums as 0
  * times that), whatever other sequences and the room past the last key hold.
  * Deterministic: grad_q and (grad_k, grad_v) are computed apart, every output
- * summed in a fixed order, instead of with atomic additions. Arguments,
+ * summed in a fixed order, instead of with atomic additions. In 16-bit types p
+ * and ds are rounded for these products; in float16 ds is scaled by powers of
+ * two from the norms of grad_out and v, so that gradients of any size keep
+ * float16's precision. Arguments,
  * alignment (strides of all eight tensors) and errors as the forward's; q, k,
  * v and out must not be written to by the outputs. The workspace's first word is the call's status
  * word, as for the forward (mdcn_query_status). */

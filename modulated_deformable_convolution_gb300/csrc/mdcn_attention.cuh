@@ -80,11 +80,20 @@ __device__ __forceinline__ void attn_store4(T* p, float4 v) {
     }
 }
 
+// Size of a row with the sum of squares s, in one byte: 64 + E with norm <= 2^E
+// <= 2 norm; 0 for a row of zeros. (float16: E from -23 to 20.)
+__device__ __forceinline__ uint8_t norm_size(float s) {
+    if (s == 0.0f) return 0;
+    const int e = static_cast<int>(__float_as_uint(s) >> 23 & 255u) - 127;  // s < 2^(e + 1)
+    return static_cast<uint8_t>(64 + ((e + 2) >> 1));
+}
+
 struct AttnSeq {
     int32_t tile;    // tile of the sequence; -1: there is none
     int32_t q0, lq;  // first query row, queries
     int32_t k0, lk;  // first key row, keys in use
     int32_t room;    // keys the sequence has rows for
+    int32_t b;       // the sequence
 };
 
 // Rows [start, end) of sequence b, clamped to the tensor. Plain loads, here and
@@ -106,7 +115,7 @@ __device__ __forceinline__ AttnSeq attn_find(const AttnArgs& a, bool by_keys, in
     const int lane = threadIdx.x & 31;
     const int32_t* starts = by_keys ? a.k_starts : a.q_starts;
     const int32_t total = by_keys ? a.tk : a.tq;
-    AttnSeq s{-1, 0, 0, 0, 0, 0};
+    AttnSeq s{-1, 0, 0, 0, 0, 0, 0};
     int32_t left = index;
     for (int32_t b0 = 0; b0 < a.batch; b0 += 32) {
         int32_t first = 0, len = 0, n = 0;
@@ -126,6 +135,7 @@ __device__ __forceinline__ AttnSeq attn_find(const AttnArgs& a, bool by_keys, in
             const int32_t before = __shfl_sync(0xffffffffu, sum - n, src);
             const int32_t tiles = __shfl_sync(0xffffffffu, n, src);
             const int b = b0 + src;
+            s.b = b;
             s.tile = by_keys ? left - before : tiles - 1 - (left - before);
             attn_range(a.q_starts, b, a.tq, s.q0, s.lq);
             attn_range(a.k_starts, b, a.tk, s.k0, s.room);

@@ -26,6 +26,9 @@ struct AttnArgs {
     float* part_out;                  // forward, keys shared out: [splits][tq][hq][D]
     float* part_lse;                  // [splits][hq][tq]
     float* delta;                     // backward: [hq][tq]
+    uint8_t* g_size;                  // float16 backward: [hq][tq], sizes of the rows of grad_out (norm_size)
+    uint8_t* v_size;                  // float16 backward: [hk][tk], sizes of the values
+    int32_t* sizes;                   // float16 backward: [batch][hk][2], a sequence's largest of both
     float* part_kv;                   // float32 backward, row tiles shared out: [kv_splits][grad_k, grad_v][tk][hk][D]
     float* part_q;                    // float32 backward, key tiles shared out: [q_splits][tq][hq][D]
     int32_t batch, tq, tk, hq, hk, group, D;
@@ -85,6 +88,8 @@ cudaError_t launch_attention_tc_backward(int dtype, const AttnArgs& a, cudaStrea
 // Joins the partial results of rows whose keys were shared out.
 cudaError_t launch_attention_join(int dtype, const AttnArgs& a, cudaStream_t st);
 // delta[h][t] = sum over the head of grad_out * out; clears the status word.
+// float16: the sizes of grad_out's rows and of the values too, then each
+// sequence's largest of both (they scale dS).
 cudaError_t launch_attention_delta(int dtype, const AttnArgs& a, cudaStream_t st);
 
 }  // namespace mdcn

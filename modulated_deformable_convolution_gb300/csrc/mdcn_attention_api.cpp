@@ -210,7 +210,8 @@ AttnPlan attn_plan(const mdcn_attention_attrs& at, const mdcn_attention_dims& d,
     return p;
 }
 
-// The backward's plan: where delta lies, and in float32 between how many blocks
+// The backward's plan: where delta lies, in float16 the sizes that scale dS, and
+// in float32 between how many blocks
 // the rows that see a key tile, and the keys that a row tile sees, are shared
 // out: as many as make three blocks of the first kind to an SM and six of the
 // second, each with two tiles at least. (Ragged sequences of up to 700, 6 heads
@@ -218,7 +219,7 @@ AttnPlan attn_plan(const mdcn_attention_attrs& at, const mdcn_attention_dims& d,
 // sequences of 2048, heads of 64: 972, 706 and 626.)
 struct AttnBwdPlan {
     int64_t tiles, kv_splits, q_splits;
-    size_t off_kv, off_q, bytes;
+    size_t off_g_size, off_v_size, off_sizes, off_kv, off_q, bytes;
 };
 
 AttnBwdPlan attn_bwd_plan(const mdcn_attention_dims& d, mdcn_dtype dtype) {
@@ -228,6 +229,14 @@ AttnBwdPlan attn_bwd_plan(const mdcn_attention_dims& d, mdcn_dtype dtype) {
     p.tiles = mdcn::attn_tiles(d.q_tokens, d.batch, tokens);
     p.kv_splits = p.q_splits = 1;
     size_t off = align256(mdcn::kAttnHeaderBytes + static_cast<size_t>(d.q_tokens) * static_cast<size_t>(d.q_heads) * 4);
+    if (dtype == MDCN_F16) {
+        p.off_g_size = off;
+        off = align256(off + static_cast<size_t>(d.q_tokens) * static_cast<size_t>(d.q_heads));
+        p.off_v_size = off;
+        off = align256(off + static_cast<size_t>(d.k_tokens) * static_cast<size_t>(d.k_heads));
+        p.off_sizes = off;
+        off = align256(off + static_cast<size_t>(d.batch) * static_cast<size_t>(d.k_heads) * 8);
+    }
     if (dtype == MDCN_F32 && d.batch > 0) {
         auto shares = [](int64_t blocks, int64_t wanted, int64_t steps) {
             int64_t s = blocks > 0 ? wanted * kSms / blocks : 1;
@@ -487,6 +496,11 @@ mdcn_status mdcn_attention_backward(const mdcn_attention_attrs* attrs, const mdc
     a.tiles = static_cast<int32_t>(p.tiles);
     a.kv_splits = static_cast<int32_t>(p.kv_splits);
     a.q_splits = static_cast<int32_t>(p.q_splits);
+    if (dtype == MDCN_F16) {
+        a.g_size = ws + p.off_g_size;
+        a.v_size = ws + p.off_v_size;
+        a.sizes = reinterpret_cast<int32_t*>(ws + p.off_sizes);
+    }
     if (p.kv_splits > 1) a.part_kv = reinterpret_cast<float*>(ws + p.off_kv);
     if (p.q_splits > 1) a.part_q = reinterpret_cast<float*>(ws + p.off_q);
     cudaError_t e = mdcn::launch_attention_delta(dtype, a, st);

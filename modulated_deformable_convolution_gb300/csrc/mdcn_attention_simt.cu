@@ -22,8 +22,10 @@
 // 32 x 32, 8 heads of 40 over 4: 77 us. Backward, 4 ragged sequences of up to 700,
 // 6 heads of 72 over 2: 94 us; 2 sequences of 2048, 6 heads of 64 over 2: 626 us,
 // 36 TFLOP/s of seven products.
+#include <algorithm>
 #include <cfloat>
 #include <cstdint>
+#include <type_traits>
 
 #include "mdcn_attention.cuh"
 #include "mdcn_pdl.h"
@@ -541,7 +543,10 @@ __global__ void __launch_bounds__(kTT, 2)
 // elements each: as few as cover head_dim. Bound by the memory that they read
 // once, mostly from L2; measured cold: the join of 2 shares of 51200 rows of 64
 // 12 us (19 with 16 lanes to a row and its sequence looked for), of 4 shares of
-// 512 rows of 128 5 us; delta of 521000 rows of 128, bfloat16, 45 us, 5.9 TB/s.
+// 512 rows of 128 5 us; delta of 521000 rows of 128, bfloat16, 45 us, 5.9 TB/s; of
+// 131000 rows of 64 8.5 us, in float16 with the sizes and as many values 15, and 4
+// each sequence's largest (looked for by the kernels that use it instead, item by
+// item: 2 us less here, 30 more on prompts of 6400).
 __device__ __forceinline__ void token_head(int64_t row, int heads, int64_t& token, int& head) {
     if (row >> 31 == 0)
         token = static_cast<uint32_t>(row) / static_cast<uint32_t>(heads);
@@ -648,26 +653,139 @@ __global__ void __launch_bounds__(kT) attn_join_kernel(const __grid_constant__ A
     if (sub == 0) a.lse[static_cast<int64_t>(h) * a.tq + tok] = total == 0.0f ? -INFINITY : base + logf(total);
 }
 
-// delta = sum(grad_out * out) of each row.
+__device__ __forceinline__ float dot8(const float4 (&x)[2], const float4 (&y)[2]) {
+    return dot4(x[0], y[0], dot4(x[1], y[1], 0.0f));
+}
+
+// Sum of the squares of 8 float16 elements, in fp32.
+__device__ __forceinline__ float squares8(uint4 u) {
+    const __half2* e = reinterpret_cast<const __half2*>(&u);
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(e[i]);
+        sum = fmaf(f.x, f.x, fmaf(f.y, f.y, sum));
+    }
+    return sum;
+}
+
+// delta = sum(grad_out * out) of each row. In float16 the sizes of the rows of
+// grad_out too, and in blocks from `row_blocks` on those of the values, of which a
+// thread has several under way.
+constexpr int kValueRows = 2;
 template <typename T, int kLanes>
-__global__ void __launch_bounds__(kT) attn_delta_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kT, 8) attn_delta_kernel(const __grid_constant__ AttnArgs a, uint32_t row_blocks) {
+    constexpr bool kSizes = std::is_same_v<T, __half>;
+    constexpr int kPer = kT / kLanes;
     dependency_wait();
     if (a.status && blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
     const int sub = threadIdx.x % kLanes, d = sub * 8;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kT / kLanes) + threadIdx.x / kLanes;
+    if constexpr (kSizes) {
+        if (blockIdx.x >= row_blocks) {
+            const uint32_t block = blockIdx.x - row_blocks;
+            const int64_t all = static_cast<int64_t>(a.batch) * a.hk * 2;
+            for (int64_t i = static_cast<int64_t>(block) * kT + threadIdx.x; i < all;
+                 i += static_cast<int64_t>(gridDim.x - row_blocks) * kT)
+                a.sizes[i] = 0;
+            const int64_t row0 = static_cast<int64_t>(block) * (kPer * kValueRows) + threadIdx.x / kLanes;
+            const int64_t rows = static_cast<int64_t>(a.tk) * a.hk;
+            int64_t key;
+            int kh;
+            uint4 v[kValueRows];
+#pragma unroll
+            for (int i = 0; i < kValueRows; ++i) {
+                v[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (row0 + i * kPer < rows && d < a.D) {
+                    token_head(row0 + i * kPer, a.hk, key, kh);
+                    v[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v.p) + key * a.v.st + kh * a.v.sh + d);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kValueRows; ++i) {
+                const float sum = lanes_sum<kLanes>(squares8(v[i]));
+                if (sub == 0 && row0 + i * kPer < rows) {
+                    token_head(row0 + i * kPer, a.hk, key, kh);
+                    a.v_size[static_cast<int64_t>(kh) * a.tk + key] = norm_size(sum);
+                }
+            }
+            return;
+        }
+    }
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kPer + threadIdx.x / kLanes;
     const bool live = row < static_cast<int64_t>(a.tq) * a.hq;
     int64_t tok = 0;
     int h = 0;
     if (live) token_head(row, a.hq, tok, h);
-    float sum = 0.0f;
+    float sum = 0.0f, squares = 0.0f;
     if (live && d < a.D) {
         float4 g[2], o[2];
         attn_load8(static_cast<const T*>(a.g.p) + tok * a.g.st + h * a.g.sh + d, g);
         attn_load8(static_cast<const T*>(a.out.p) + tok * a.out.st + h * a.out.sh + d, o);
-        sum = dot4(g[0], o[0], dot4(g[1], o[1], 0.0f));
+        sum = dot8(g, o);
+        if constexpr (kSizes) squares = dot8(g, g);
     }
     sum = lanes_sum<kLanes>(sum);
-    if (live && sub == 0) a.delta[static_cast<int64_t>(h) * a.tq + tok] = sum;
+    if constexpr (kSizes) squares = lanes_sum<kLanes>(squares);
+    if (live && sub == 0) {
+        const int64_t at = static_cast<int64_t>(h) * a.tq + tok;
+        a.delta[at] = sum;
+        if constexpr (kSizes) a.g_size[at] = norm_size(squares);
+    }
+}
+
+// The largest of the n sizes from `at` on in each of `heads` rows `pitch` apart:
+// a thread's part, of the `step` threads that share them, in bytes. 16 bytes at
+// a time: the array starts on 16 bytes and has room up to a multiple of 16.
+__device__ __forceinline__ uint32_t top_sizes(const uint8_t* at, uint32_t heads, int64_t pitch, uint32_t n,
+                                              uint32_t thread, uint32_t step) {
+    const uint32_t words = (n + 30u) / 16u;  // that a head's sizes can touch; heads * words < 2^31
+    uint32_t top = 0;
+#pragma unroll 4
+    for (uint32_t i = thread; i < heads * words; i += step) {
+        const uint32_t head = i / words;
+        const uintptr_t first = reinterpret_cast<uintptr_t>(at + head * pitch), end = first + n;
+        const uintptr_t w = (first & ~static_cast<uintptr_t>(15)) + 16u * (i - head * words);
+        if (w >= end) continue;
+        const uint4 v = *reinterpret_cast<const uint4*>(w);
+        uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        if (w < first || w + 16 > end) {  // bytes before the first and past the last count as 0
+            const int lo = w < first ? static_cast<int>(first - w) : 0, hi = w + 16 > end ? static_cast<int>(end - w) : 16;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int from = min(max(lo - 4 * k, 0), 4), to = min(max(hi - 4 * k, 0), 4);
+                x[k] &= static_cast<uint32_t>((uint64_t(1) << (8 * to)) - (uint64_t(1) << (8 * min(from, to))));
+            }
+        }
+        top = __vmaxu4(__vmaxu4(top, x[0]), __vmaxu4(x[1], __vmaxu4(x[2], x[3])));
+    }
+    return top;
+}
+
+// Each sequence's largest size of a grad_out row, and of a value in use, for
+// each key head. Grid: (sequences * key heads or fewer, blocks that share one's
+// rows). The largest is the same in any order.
+__global__ void __launch_bounds__(kT) attn_sizes_kernel(const __grid_constant__ AttnArgs a) {
+    dependency_wait();
+    const int64_t all = static_cast<int64_t>(a.batch) * a.hk;
+    const uint32_t thread = blockIdx.y * kT + threadIdx.x, step = gridDim.y * kT;
+    for (int64_t i = blockIdx.x; i < all; i += gridDim.x) {
+        const int b = static_cast<int>(i / a.hk), kh = static_cast<int>(i - static_cast<int64_t>(b) * a.hk);
+        int32_t q0, lq, k0, lk;
+        attn_range(a.q_starts, b, a.tq, q0, lq);
+        attn_range(a.k_starts, b, a.tk, k0, lk);
+        if (a.k_lengths) lk = min(max(a.k_lengths[b], 0), lk);
+        const uint32_t top[2] = {top_sizes(a.g_size + static_cast<int64_t>(kh) * a.group * a.tq + q0,
+                                           static_cast<uint32_t>(a.group), a.tq, static_cast<uint32_t>(lq), thread, step),
+                                 top_sizes(a.v_size + static_cast<int64_t>(kh) * a.tk + k0, 1, 0,
+                                           static_cast<uint32_t>(lk), thread, step)};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t t = top[k];
+            const uint32_t most = max(max(t & 255u, t >> 8 & 255u), max(t >> 16 & 255u, t >> 24));
+            const int32_t one = static_cast<int32_t>(__reduce_max_sync(0xffffffffu, most));
+            if ((threadIdx.x & 31) == 0 && one > 0) atomicMax(a.sizes + 2 * i + k, one);
+        }
+    }
 }
 
 }  // namespace
@@ -750,9 +868,19 @@ cudaError_t join(const AttnArgs& a, cudaStream_t st) {
 
 template <typename T>
 cudaError_t delta(const AttnArgs& a, cudaStream_t st) {
-    const int64_t rows = static_cast<int64_t>(a.tq) * a.hq;
-    if (a.D <= 64) return launch_dependent(attn_delta_kernel<T, 8>, groups(rows, 8), kT, 0, st, a);
-    return launch_dependent(attn_delta_kernel<T, 16>, groups(rows, 16), kT, 0, st, a);
+    const int lanes = a.D <= 64 ? 8 : 16;
+    const uint32_t rows = groups(static_cast<int64_t>(a.tq) * a.hq, lanes);
+    const uint32_t values =
+        a.sizes ? groups((static_cast<int64_t>(a.tk) * a.hk + kValueRows - 1) / kValueRows, lanes) + 1 : 0;
+    const cudaError_t e = lanes == 8 ? launch_dependent(attn_delta_kernel<T, 8>, rows + values, kT, 0, st, a, rows)
+                                     : launch_dependent(attn_delta_kernel<T, 16>, rows + values, kT, 0, st, a, rows);
+    if (e != cudaSuccess || !a.sizes) return e;
+    // blocks that share a sequence's rows of a key head: two to an SM in all, 16 sizes to a thread
+    const int64_t pairs = static_cast<int64_t>(a.batch) * a.hk;
+    const int64_t words = (static_cast<int64_t>(a.tq) * a.group + a.tk) / a.batch / (16 * kT) + 1;
+    const int64_t shares = std::min(std::max<int64_t>(2 * 152 / pairs, 1), words);
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(pairs, 1 << 16)), static_cast<unsigned>(shares));
+    return launch_dependent(attn_sizes_kernel, grid, kT, 0, st, a);
 }
 
 }  // namespace

@@ -92,7 +92,7 @@ __device__ __forceinline__ void store8(float* p, const float* v, bool wide) {
 // item's sequence and publishes the item in shared memory; two slots.
 struct alignas(16) AttnItem {
     int32_t go;          // 0: no more items
-    int32_t kh, split;   // key head; share of the keys
+    int32_t kh, split;   // key head; share of the keys (float16 gradients: see score_shift)
     int32_t q0, k0;      // the sequence's first query and key row
     int32_t lq, lk, room;
     int32_t first;       // first token (row tiles) or key (key tiles)

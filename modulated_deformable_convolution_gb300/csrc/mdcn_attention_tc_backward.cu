@@ -15,7 +15,13 @@
 // tensors' type, go back there as the next product's left operand. Two
 // warpgroups take 64 of a product's 128 columns each, a thread one row. P is
 // kept times 2^8 (exact): probabilities down to 2^-22 then stay normal float16
-// numbers; dS is kept unscaled, since a gradient's size is not bounded.
+// numbers. dS, whose size is the gradients', is kept in float16 times a power of
+// two, undone when the sums are read: |ds| <= 2 |grad_out row| |value|, so that the
+// norms bound it that two small launches leave behind: a grad_q row's own with
+// the sequence's largest value's, in grad_kv the sequence's largest of both. The
+// bound goes to 2^15: nothing passes float16's largest number, and what is 2^-29 of
+// it is still a normal one (unscaled, gradients of 1e-4 over 6400 keys were off by
+// 8%). bfloat16 has fp32's range and needs none.
 //
 // Bound by the tensor cores: 3 (grad_q) and 4 (grad_kv) products of 128 x 128 x
 // D per tile, about 512 cycles each at D = 128. While the elementwise step of
@@ -24,7 +30,7 @@
 // Measured with delta (bfloat16, 32 heads of 128 over 8): 9 packed causal prompts
 // of up to 6400 tokens 1482 us, 940 TFLOP/s of five products, 1315 of the seven;
 // 2 x 8192 without a mask 4.74 ms, 1160 and 1620. 16 maps of 32 x 32, 8 heads of
-// 64, float16: 143 us, 599 TFLOP/s of five products: at D = 64 the products of a
+// 64, float16: 152 us, 566 TFLOP/s of five products, 10 us of them for the sizes: at D = 64 the products of a
 // tile take half as long and its elementwise step as long as before (a grad_kv
 // block about 2130 cycles, exponentials 710, dS 510, loads and stores of tensor
 // memory and waits the rest; 16 elementwise warps instead of 8 changed nothing).
@@ -47,12 +53,17 @@ static_assert(2 * kRegsRow + kRegsCtl <= 3 * 168, "register split must fit the l
 constexpr int kKeys = 128;
 constexpr float kShift = 8.0f, kUnshift = 0.00390625f;  // P is kept times 2^8
 
+__device__ __forceinline__ float power2(int e) { return __int_as_float((e + 127) << 23); }
+
+// The exponent of the factor that dS is kept times, from the sizes of a row of
+// grad_out and of a value (norm_size): 2 |g| |v| 2^shift <= 2^15.
+__device__ __forceinline__ int score_shift(int sizes) { return min(max(14 - (sizes - 128), -60), 60); }
+
 // ds = p 2^8 * (dp - delta) 2^-8 for 64 columns of a row; p in, packed ds out.
-// d2: -delta * 2^-8 for column pairs.
+// un: 2^-8 (float16: times dS's factor) twice; minus_delta: -delta * un for column pairs.
 template <bool kBf, typename F>
-__device__ __forceinline__ void score_grads(const uint32_t (&p)[2][32], const uint32_t (&dp)[2][32], F minus_delta,
-                                            uint32_t (&out)[32]) {
-    const uint64_t un = pack2(kUnshift, kUnshift);
+__device__ __forceinline__ void score_grads(const uint32_t (&p)[2][32], const uint32_t (&dp)[2][32], uint64_t un,
+                                            F minus_delta, uint32_t (&out)[32]) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
         const int c = i >> 4, o = 2 * (i & 15);
@@ -175,6 +186,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 it.lk = s.lk;
                 it.first = s.tile * tpt;
                 it.n0 = (attn_seen(a, s, it.first + min(tpt, s.lq - it.first) - 1) + kKeys - 1) / kKeys;
+                if constexpr (!kBf) it.split = a.sizes[(static_cast<int64_t>(s.b) * a.hk + it.kh) * 2 + 1];
                 return true;
             });
         } else if (warp == kWarpLoad) {
@@ -326,8 +338,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!live) seen = 0;
             const int32_t seen_all = __reduce_min_sync(0xffffffffu, live ? seen : 0x7fffffff);
             const float lse = live ? a.lse[static_cast<int64_t>(h) * a.tq + tok] * kLog2e : 0.0f;
-            const float delta = live ? a.delta[static_cast<int64_t>(h) * a.tq + tok] * kUnshift : 0.0f;
-            const uint64_t l2 = pack2(kShift - lse, kShift - lse), d2 = pack2(-delta, -delta);
+            float un = kUnshift, factor = a.scale;
+            if constexpr (!kBf) {
+                const int shift =
+                    score_shift(live ? a.g_size[static_cast<int64_t>(h) * a.tq + tok] + it.split : 128);
+                un = power2(shift - 8);
+                factor *= power2(-shift);
+            }
+            const float delta = live ? a.delta[static_cast<int64_t>(h) * a.tq + tok] * un : 0.0f;
+            const uint64_t l2 = pack2(kShift - lse, kShift - lse), d2 = pack2(-delta, -delta), un2 = pack2(un, un);
             for (int32_t j = 0; j < n; ++j, ++g) {
                 if (!warp_wait2(s_full, 0u, g & 1u, abort_flag, a.status, kSiteGatherEmpty)) return false;
                 tc_fence_after();
@@ -362,7 +381,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             if (32 * c + i >= left) x[c][i] = dp[c][i] = 0u;
                     __syncwarp();  // lanes differ in what they mask; the store below needs the whole warp
                 }
-                score_grads<kBf>(x, dp, [&](int) { return d2; }, ds);
+                score_grads<kBf>(x, dp, un2, [&](int) { return d2; }, ds);
                 // the sum before this step has read dS
                 if (j > 0 && !warp_wait2(dq_done, 0u, (g - 1u) & 1u, abort_flag, a.status, kSiteGatherEmpty))
                     return false;
@@ -378,7 +397,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tc_fence_after();
             uint8_t* p = static_cast<uint8_t*>(a.gq.p) + 2 * (tok * a.gq.st + h * a.gq.sh);
             const int mid = min(32 * kAtoms, a.D);
-            store_row<kBf>(c_dq + lanes, p, half ? mid : 0, half ? a.D : mid, a.scale, any, live);
+            store_row<kBf>(c_dq + lanes, p, half ? mid : 0, half ? a.D : mid, factor, any, live);
             if (any) {  // the next item's first sum may overwrite dQ
                 tc_fence_before();
                 __syncwarp();
@@ -427,7 +446,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         return;
     }
     const uint32_t k_s = raw, v_s = raw + kTile, q_ring = raw + 2 * kTile, g_ring = q_ring + SQ * kTile;
-    const uint32_t stats = g_ring + SG * kTile;  // per stage: 128 x (8 - lse'), 128 x (-delta 2^-8)
+    const uint32_t stats = g_ring + SG * kTile;  // per stage: 128 x (8 - lse'), 128 x (-delta 2^-8, scaled as dS)
     const ItemQueue queue{stats + ST * 1024u, a.item_limit};
     const uint32_t bars = queue.base + ItemQueue::kBytes;
     auto q_full = [&](uint32_t s) { return bars + 8u * s; };
@@ -501,6 +520,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 // the blocks of query rows that see the tile's first key, or later ones
                 it.j0 = a.causal ? max(0, it.first + s.lq - s.lk) / tpt : 0;
                 it.n0 = it.first < s.lk ? max(0, (s.lq + tpt - 1) / tpt - it.j0) : 0;
+                if constexpr (!kBf) {
+                    const int32_t* sizes = a.sizes + (static_cast<int64_t>(s.b) * a.hk + it.kh) * 2;
+                    it.split = sizes[0] + sizes[1];
+                }
                 return true;
             });
         } else if (warp == kWarpLoad) {
@@ -555,6 +578,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             for_items(queue, abort_flag, a.status, [&](const AttnItem& it) {
                 const int64_t head = static_cast<int64_t>(it.kh) * a.group * a.tq + it.q0;
+                const float un = kBf ? kUnshift : power2(score_shift(it.split) - 8);
                 float nl[4], nd[4];
                 auto fetch = [&](int32_t i) {
                     const int32_t tok0 = (it.j0 + i) * tpt, rows = i < it.n0 ? min(tpt, it.lq - tok0) * a.group : 0;
@@ -582,7 +606,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         st_shared_f32(stats + st * 1024u + 4u * (lane + 32 * k), fmaf(-kLog2e, l[k], kShift));
-                        st_shared_f32(stats + st * 1024u + 512u + 4u * (lane + 32 * k), -d[k] * kUnshift);
+                        st_shared_f32(stats + st * 1024u + 512u + 4u * (lane + 32 * k), -d[k] * un);
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(t_full(st));
@@ -694,6 +718,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         uint32_t b = 0, items = 0;  // blocks, and items with any, so far
         for_items(queue, abort_flag, a.status, [&](const AttnItem& it) {
             const int32_t key = it.first + r, shift = it.lk - it.lq, n = it.n0;
+            const int scaled = kBf ? 0 : score_shift(it.split);  // of dS: its factor's exponent
+            const uint64_t un2 = pack2(power2(scaled - 8), power2(scaled - 8));
             for (int32_t i = 0; i < n; ++i, ++b) {
                 const uint32_t st = b % ST, ph = (b / ST) & 1u, scol = c_s(b % NS) + lanes + 64u * half;
                 const int32_t tok0 = (it.j0 + i) * tpt, rows = min(tpt, it.lq - tok0) * a.group;
@@ -757,7 +783,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 uint64_t d2[2];
                 score_grads<kBf>(
-                    x, dp,
+                    x, dp, un2,
                     [&](int k) {
                         if ((k & 2) == 0) {
                             const uint4 d = ld_shared_v4(delta_s + 4u * k);
@@ -786,7 +812,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             uint8_t* p = static_cast<uint8_t*>(t.p) + 2 * (static_cast<int64_t>(it.k0 + key) * t.st + it.kh * t.sh);
             // keys past the last in use see nothing: their rows hold zeros
             const bool used = any && key < it.lk;
-            const float f = used ? (half ? a.scale : kUnshift) : 0.0f;
+            const float f = used ? (half ? a.scale * power2(-scaled) : kUnshift) : 0.0f;
             const bool live = key < it.room;
             const bool wide = (reinterpret_cast<uintptr_t>(p) & 31u) == 0;
 #pragma unroll 1

@@ -380,12 +380,15 @@ mdcn_status mdcn_rotary_backward(const mdcn_rotary_attrs* attrs, const mdcn_rota
     if (s != MDCN_OK) return s;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
-    if (dims->tokens == 0) {  // no tokens: the weights' gradients are empty sums
-        const size_t bytes = static_cast<size_t>(dims->head_dim) * static_cast<size_t>(size_of(dtype));
-        if (grad_q_weight_or_null) e = cudaMemsetAsync(grad_q_weight_or_null, 0, bytes, cs);
-        if (e == cudaSuccess && grad_k_weight_or_null) e = cudaMemsetAsync(grad_k_weight_or_null, 0, bytes, cs);
-        return e == cudaSuccess ? MDCN_OK : mdcn::api_cuda_fail(e);
+    // no tokens, or no heads of k: the weights' gradients are empty sums
+    const size_t bytes = static_cast<size_t>(dims->head_dim) * static_cast<size_t>(size_of(dtype));
+    if (dims->tokens == 0 && grad_q_weight_or_null) e = cudaMemsetAsync(grad_q_weight_or_null, 0, bytes, cs);
+    if (e == cudaSuccess && tk == 0 && grad_k_weight_or_null) {
+        e = cudaMemsetAsync(grad_k_weight_or_null, 0, bytes, cs);
+        grad_k_weight_or_null = nullptr;
     }
+    if (e != cudaSuccess) return mdcn::api_cuda_fail(e);
+    if (dims->tokens == 0) return MDCN_OK;
     a.y[0] = tensor(grad_q_out, dims->q_out, dims->tokens, dims->q_heads);
     a.y[1] = tensor(grad_k_out_or_null, dims->k_out, dims->tokens, dims->k_heads);
     a.x[0] = tensor(q_or_null, dims->q, dims->tokens, dims->q_heads);
@@ -396,7 +399,7 @@ mdcn_status mdcn_rotary_backward(const mdcn_rotary_attrs* attrs, const mdcn_rota
     a.w[1] = k_weight_or_null;
     a.pos = static_cast<const int32_t*>(positions);
     a.freq = static_cast<const float*>(inv_freq);
-    a.part = weights ? static_cast<float*>(workspace) : nullptr;
+    a.part = grad_q_weight_or_null || grad_k_weight_or_null ? static_cast<float*>(workspace) : nullptr;
     e = mdcn::launch_rotary_backward(dtype, a, grad_q_weight_or_null, grad_k_weight_or_null, sms, cs);
     return e == cudaSuccess ? MDCN_OK : mdcn::api_cuda_fail(e);
 }

@@ -211,6 +211,24 @@ def test_zero_rows_and_no_tokens():
 
 
 @gpu
+@pytest.mark.parametrize("q_weight", [True, False])
+def test_weight_of_no_heads(q_weight):
+    """A k without heads: its weight's gradient is an empty sum, whatever the
+    workspace held."""
+    p = Problem(torch.float16, 9, 3, 1, 40, (10, 10), "half", True)
+    gq, q = p.cuda("gq"), p.cuda("q")
+    none = torch.empty(9, 0, 40, dtype=p.dtype, device="cuda")
+    kw = dict(layout=p.layout, norm=True, eps=p.eps, q_weight=p.cuda("qw") if q_weight else None)
+    want = mdcn.rotary_backward(gq, None, q, None, p.cuda("pos"), p.cuda("freq"), p.sections, **kw)
+    g, gw = torch.empty_like(q), [torch.full((40,), math.nan, dtype=p.dtype, device="cuda") for _ in range(2)]
+    ws = torch.full((mdcn.mdcn_rotary_backward_workspace_size(gq, none, p.cuda("pos"), p.cuda("freq"), p.sections, norm=True),), 255, dtype=torch.uint8, device="cuda")
+    mdcn.mdcn_rotary_backward(gq, none, q, none, p.cuda("pos"), p.cuda("freq"), p.sections, g, none, gw[0] if q_weight else None, gw[1], ws, k_weight=p.cuda("kw"), **kw)
+    assert (gw[1] == 0).all() and torch.equal(g, want["q"])
+    if q_weight:
+        assert torch.equal(gw[0], want["q_weight"])
+
+
+@gpu
 def test_deterministic_and_on_a_stream():
     p = Problem(torch.bfloat16, 3001, 6, 2, 64, (16, 16), "half", True)
     args = (p.cuda("gq"), p.cuda("gk"), p.cuda("q"), p.cuda("k"), p.cuda("pos"), p.cuda("freq"), p.sections)

@@ -345,13 +345,20 @@ __device__ __forceinline__ void turn_pairs(const RotaryArgs& a, const int32_t* p
 
 // A token's turns for the lane's 8 pairs (kBeside, kChunks: one cosine and
 // sine per pair) or 8 elements (kAnywhere: the sine has the sign of the
-// element's place in its pair). direction -1 turns back.
-template <int kMode>
+// element's place in its pair). direction -1 turns back. Where part of a head
+// is not rotated, its elements are left out of the arithmetic rather than
+// turned by nothing: an infinity times a sine of 0 would be NaN.
+// kWhole: every element of a head is rotated (32768 tokens of 32 + 8 heads of 128:
+// 120 us, and 123 with one kernel for both).
+template <int kMode, bool kWhole>
 struct Turns {
     float c[kE], s[kE];
+    int32_t mine;  // kBeside, kChunks: so many of the lane's pairs are rotated, all where it has fewer
     // `cs`: the pairs of the lane's token.
     __device__ __forceinline__ Turns(const RotaryArgs& a, const LaneSetup<kMode>& L, const float2* cs,
                                      float direction) {
+        mine = 0;
+        if constexpr (kMode != kAnywhere) mine = a.pairs - L.pair0;
 #pragma unroll
         for (int i = 0; i < kE; ++i) {
             float2 v = make_float2(1.0f, 0.0f);
@@ -379,9 +386,11 @@ struct Turns {
                     const int p = k * (kE / 2) + i;
                     float lo, hi;
                     unpack2(x[k][i], lo, hi);
-                    x[k][i] = pack2(fmaf(lo, c[p], -(hi * s[p])), fmaf(hi, c[p], lo * s[p]));
+                    const uint64_t turned = pack2(fmaf(lo, c[p], -(hi * s[p])), fmaf(hi, c[p], lo * s[p]));
+                    x[k][i] = kWhole || p < mine ? turned : x[k][i];
                 }
         } else if constexpr (kMode == kChunks) {
+            if (!kWhole && mine <= 0) return;
 #pragma unroll
             for (int i = 0; i < kE / 2; ++i) {
                 const uint64_t c2 = pack2(c[2 * i], c[2 * i + 1]), s2 = pack2(s[2 * i], s[2 * i + 1]);
@@ -397,7 +406,12 @@ struct Turns {
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < kE / 2; ++i) {
-                const uint64_t far = pack2(buf[L.code[i] & 0xffu], buf[(L.code[i] >> 16) & 0xffu]);
+                float far0 = buf[L.code[i] & 0xffu], far1 = buf[(L.code[i] >> 16) & 0xffu];
+                if constexpr (!kWhole) {
+                    far0 = L.code[i] & 0x8000u ? far0 : 0.0f;
+                    far1 = L.code[i] & 0x80000000u ? far1 : 0.0f;
+                }
+                const uint64_t far = pack2(far0, far1);
                 const uint64_t c2 = pack2(c[2 * i], c[2 * i + 1]), s2 = pack2(s[2 * i], s[2 * i + 1]);
                 x[0][i] = fma2(x[0][i], c2, mul2(far, s2));
             }
@@ -425,7 +439,7 @@ struct Weights {
 // each tensor; `fetch` loads it into buffers, `work` takes it out of them (and
 // then starts their next loads, `next`) and writes the result. Buffers start
 // as zeros, so that the chunks that a lane lacks add nothing to its row's sums.
-template <typename T, int kMode>
+template <typename T, int kMode, bool kWhole>
 struct Forward {
     using Type = T;
     static constexpr int kC = LaneSetup<kMode>::kC;
@@ -477,7 +491,7 @@ struct Forward {
             if (live && L.on[c]) b.x[c].load(p.in + (L.e0[c] - L.e0[0]), vec);
     }
     template <typename F>
-    __device__ __forceinline__ void work(Buffers& b, const At& at, bool live, const Turns<kMode>& turns, float* row,
+    __device__ __forceinline__ void work(Buffers& b, const At& at, bool live, const Turns<kMode, kWhole>& turns, float* row,
                                          F next) {
         uint64_t v[kC][kE / 2];
 #pragma unroll
@@ -510,7 +524,7 @@ struct Forward {
     }
 };
 
-template <typename T, int kMode>
+template <typename T, int kMode, bool kWhole>
 struct Backward {
     using Type = T;
     static constexpr int kC = LaneSetup<kMode>::kC;
@@ -569,7 +583,7 @@ struct Backward {
             }
     }
     template <typename F>
-    __device__ __forceinline__ void work(Buffers& b, const At& at, bool live, const Turns<kMode>& turns, float* row,
+    __device__ __forceinline__ void work(Buffers& b, const At& at, bool live, const Turns<kMode, kWhole>& turns, float* row,
                                          F next) {
         uint64_t g[kC][kE / 2], v[kC][kE / 2], o[kC][kE / 2];
 #pragma unroll
@@ -620,7 +634,7 @@ struct Backward {
 // them), so many passes ahead in flight. Fewer: the lane groups take several
 // tokens' heads at once, the next blocks of tokens in flight. The first loads
 // start before the block's frequencies are laid out.
-template <int kMode, typename Op>
+template <int kMode, bool kWhole, typename Op>
 __device__ __forceinline__ void all_rows(const RotaryArgs& a, int heads, const LaneSetup<kMode>& L, Op& op,
                                          float freq, PairFreq* table, WarpSmem<kMode>& w, int64_t warp,
                                          int64_t warps) {
@@ -654,7 +668,7 @@ __device__ __forceinline__ void all_rows(const RotaryArgs& a, int heads, const L
                 op.advance_in(ahead, rpw);
             }
             turn_pairs<typename Op::Type>(a, a.pos + static_cast<int64_t>(token) * a.axes, 1, table, w, L.lane);
-            const Turns<kMode> turns(a, L, w.cs, Op::kDirection);
+            const Turns<kMode, kWhole> turns(a, L, w.cs, Op::kDirection);
             for (int hb = h0; hb < h1; hb += kAhead * rpw) {
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k) {
@@ -694,7 +708,7 @@ __device__ __forceinline__ void all_rows(const RotaryArgs& a, int heads, const L
                 pos.put(w.pos, count(b) * a.axes, L.lane);
                 turn_pairs<typename Op::Type>(a, w.pos, count(b), table, w, L.lane);
                 pos.load(a, (b + warps) * n, count(b + warps), L.lane);
-                const Turns<kMode> turns(a, L, w.cs + (mine < n ? mine : 0) * a.pairs, Op::kDirection);
+                const Turns<kMode, kWhole> turns(a, L, w.cs + (mine < n ? mine : 0) * a.pairs, Op::kDirection);
                 op.work(buf[k], op.at(token_of(b), h), there(b), turns, w.row[which],
                         [&] { op.fetch(buf[k], op.at(token_of(bn), h), there(bn)); });
                 which ^= 1;
@@ -704,7 +718,7 @@ __device__ __forceinline__ void all_rows(const RotaryArgs& a, int heads, const L
 }
 
 // Grid: (blocks, 2): q and k by blocks of their own.
-template <typename T, int kMode>
+template <typename T, int kMode, bool kWhole>
 __global__ void __launch_bounds__(kThreads, 2) rotary_forward_kernel(const __grid_constant__ RotaryArgs a) {
     __shared__ WarpSmem<kMode> smem[kWarps];
     __shared__ PairFreq table[kMaxD / 2];
@@ -712,15 +726,15 @@ __global__ void __launch_bounds__(kThreads, 2) rotary_forward_kernel(const __gri
     dependency_wait();
     const float freq = fetch_freq(a);
     const int t = blockIdx.y;
-    Forward<T, kMode> op(a, t, L);
-    all_rows<kMode>(a, t ? a.rows - a.hq : a.hq, L, op, freq, table, smem[threadIdx.x >> 5],
+    Forward<T, kMode, kWhole> op(a, t, L);
+    all_rows<kMode, kWhole>(a, t ? a.rows - a.hq : a.hq, L, op, freq, table, smem[threadIdx.x >> 5],
                     static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5),
                     static_cast<int64_t>(gridDim.x) * kWarps);
 }
 
 // 12 warps to an SM with 168 registers each, two rows of gradients and heads
 // in flight: with 16 warps the registers spill.
-template <typename T, int kMode>
+template <typename T, int kMode, bool kWhole>
 __global__ void __launch_bounds__(kBwdThreads, 3) rotary_backward_kernel(const __grid_constant__ RotaryArgs a) {
     constexpr int kC = LaneSetup<kMode>::kC;
     __shared__ WarpSmem<kMode> smem[kBwdWarps];
@@ -730,8 +744,8 @@ __global__ void __launch_bounds__(kBwdThreads, 3) rotary_backward_kernel(const _
     dependency_wait();
     const float freq = fetch_freq(a);
     const int t = blockIdx.y;
-    Backward<T, kMode> op(a, t, L);
-    all_rows<kMode>(a, t ? a.rows - a.hq : a.hq, L, op, freq, table, smem[threadIdx.x >> 5],
+    Backward<T, kMode, kWhole> op(a, t, L);
+    all_rows<kMode, kWhole>(a, t ? a.rows - a.hq : a.hq, L, op, freq, table, smem[threadIdx.x >> 5],
                     static_cast<int64_t>(blockIdx.x) * kBwdWarps + (threadIdx.x >> 5),
                     static_cast<int64_t>(gridDim.x) * kBwdWarps);
     if (!a.part) return;
@@ -805,29 +819,31 @@ int64_t blocks_for(const RotaryArgs& a, int warps) {
     return (static_cast<int64_t>(a.tokens) * a.parts + warps - 1) / warps;
 }
 
+template <typename T, bool kWhole>
+cudaError_t forward_of(const RotaryArgs& a, RotaryMode mode, dim3 g, cudaStream_t st) {
+    if (mode == kBeside) return launch_dependent(rotary_forward_kernel<T, kBeside, kWhole>, g, kThreads, 0, st, a);
+    if (mode == kChunks) return launch_dependent(rotary_forward_kernel<T, kChunks, kWhole>, g, kThreads, 0, st, a);
+    return launch_dependent(rotary_forward_kernel<T, kAnywhere, kWhole>, g, kThreads, 0, st, a);
+}
+
 template <typename T>
 cudaError_t forward_t(const RotaryArgs& a, RotaryMode mode, int64_t grid, cudaStream_t st) {
     const dim3 g(static_cast<unsigned>(grid), a.rows > a.hq ? 2u : 1u);
-    cudaError_t e;
-    if (mode == kBeside)
-        e = launch_dependent(rotary_forward_kernel<T, kBeside>, g, kThreads, 0, st, a);
-    else if (mode == kChunks)
-        e = launch_dependent(rotary_forward_kernel<T, kChunks>, g, kThreads, 0, st, a);
-    else
-        e = launch_dependent(rotary_forward_kernel<T, kAnywhere>, g, kThreads, 0, st, a);
-    return e;
+    return 2 * a.pairs == a.D ? forward_of<T, true>(a, mode, g, st) : forward_of<T, false>(a, mode, g, st);
+}
+
+template <typename T, bool kWhole>
+cudaError_t backward_of(const RotaryArgs& a, RotaryMode mode, dim3 g, cudaStream_t st) {
+    if (mode == kBeside) return launch_dependent(rotary_backward_kernel<T, kBeside, kWhole>, g, kBwdThreads, 0, st, a);
+    if (mode == kChunks) return launch_dependent(rotary_backward_kernel<T, kChunks, kWhole>, g, kBwdThreads, 0, st, a);
+    return launch_dependent(rotary_backward_kernel<T, kAnywhere, kWhole>, g, kBwdThreads, 0, st, a);
 }
 
 template <typename T>
 cudaError_t backward_t(const RotaryArgs& a, RotaryMode mode, int64_t grid, void* gqw, void* gkw, cudaStream_t st) {
     const dim3 g(static_cast<unsigned>(grid), a.rows > a.hq ? 2u : 1u);
-    cudaError_t e;
-    if (mode == kBeside)
-        e = launch_dependent(rotary_backward_kernel<T, kBeside>, g, kBwdThreads, 0, st, a);
-    else if (mode == kChunks)
-        e = launch_dependent(rotary_backward_kernel<T, kChunks>, g, kBwdThreads, 0, st, a);
-    else
-        e = launch_dependent(rotary_backward_kernel<T, kAnywhere>, g, kBwdThreads, 0, st, a);
+    const cudaError_t e =
+        2 * a.pairs == a.D ? backward_of<T, true>(a, mode, g, st) : backward_of<T, false>(a, mode, g, st);
     if (e != cudaSuccess || !a.part) return e;
     return launch_dependent(rotary_weight_sum_kernel<T>, dim3(static_cast<unsigned>(a.D / 8), 2), kThreads, 0, st,
                             static_cast<const float*>(a.part), static_cast<int>(grid), static_cast<int>(a.D),

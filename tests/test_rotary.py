@@ -211,6 +211,35 @@ def test_zero_rows_and_no_tokens():
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("d,sections,layout", [
+    (80, (8, 13, 13), "interleaved"), (64, (3,), "interleaved"),  # neighbours, the last lanes in part or not at all
+    (128, (16, 16), "half"), (128, (8, 16), "blocks"),             # runs of eight
+    (72, (3, 8, 7), "half"), (40, (5, 6), "blocks"),               # anywhere
+    (64, (0, 0), "half"),
+])
+def test_strays_in_elements_that_are_not_rotated(dtype, d, sections, layout):
+    """Without norm an element past the rotated ones is copied, infinities and
+    NaN too, and reaches no other."""
+    p = Problem(dtype, 7, 3, 1, d, sections, layout, False)
+    q = p.cuda("q")
+    args = (p.cuda("pos"), p.cuda("freq"), p.sections)
+    run = lambda x: mdcn.rotary(x, None, *args, layout=layout)[0]  # noqa: E731
+    back = lambda x: mdcn.rotary_backward(x, None, None, None, *args, layout=layout)["q"]  # noqa: E731
+    rotated = sorted(e for lo, hi, _ in _pairs(sections, layout) for e in (lo, hi))
+    still = [e for e in range(d) if e not in rotated]
+    for f in (run, back):
+        want = f(q)
+        assert torch.equal(want[..., still], q[..., still])
+        x = q.clone()
+        for i, e in enumerate(still):
+            x[i % 7, i % 3, e] = (math.inf, -math.inf, math.nan)[i // 3 % 3]
+        got = f(x)
+        assert torch.equal(got[..., rotated], want[..., rotated])
+        assert torch.equal(torch.nan_to_num(got[..., still], 7.0), torch.nan_to_num(x[..., still], 7.0))
+
+
+@gpu
 @pytest.mark.parametrize("q_weight", [True, False])
 def test_weight_of_no_heads(q_weight):
     """A k without heads: its weight's gradient is an empty sum, whatever the

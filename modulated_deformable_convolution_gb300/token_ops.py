@@ -53,6 +53,21 @@ def _done(result, name):
     return result
 
 
+def _call(function, args, small, name):
+    """function(*args). The C entry points take addresses on 16 bytes; where
+    one of the small inputs (the places ``small`` of args), a slice of a longer
+    tensor, is not, the call is made with copies of those that are not."""
+    result = function(*args)
+    if type(result) is int and result == _abi.MDCN_ERR_ALIGN:
+        off = [i for i in small if args[i] is not None and args[i].data_ptr() % 16]
+        if off:
+            args = list(args)
+            for i in off:
+                args[i] = args[i].clone()
+            result = function(*args)
+    return _done(result, name)
+
+
 def _bytes(result, name):
     status, n = result
     if status:
@@ -93,9 +108,10 @@ def rotary(q, k, positions, inv_freq, sections, layout="half", norm=False, q_wei
     """Queries q and keys k (or None) of one layer, [tokens, heads, head_dim],
     normed per head (``norm``) and rotated by the int32 positions [tokens,
     axes]: axis a turns sections[a] pairs of elements, with the float32
-    frequencies inv_freq. Returns (q_out, k_out), which may be q and k."""
-    return _done(_native().rotary_forward(q, k, positions, inv_freq, sections, q_out, k_out, _layout(layout), norm,
-                                          q_weight, k_weight, eps, None), "mdcn_rotary_forward")
+    frequencies inv_freq. Returns (q_out, k_out), which may be q and k.
+    positions and the other small inputs may be slices that start anywhere."""
+    return _call(_native().rotary_forward, (q, k, positions, inv_freq, sections, q_out, k_out, _layout(layout), norm,
+                                            q_weight, k_weight, eps, None), (2, 3, 9, 10), "mdcn_rotary_forward")
 
 
 def mdcn_rotary_backward(grad_q_out, grad_k_out, q, k, positions, inv_freq, sections, grad_q, grad_k, grad_q_weight,
@@ -122,9 +138,9 @@ def rotary_backward(grad_q_out, grad_k_out, q, k, positions, inv_freq, sections,
     """Gradients of sum(grad_q_out * q_out) + sum(grad_k_out * k_out) for
     (q_out, k_out) = rotary(q, k, ...). Returns a dict with q, k, q_weight and
     k_weight (None for what was not given)."""
-    g = _done(_native().rotary_backward(grad_q_out, grad_k_out, q, k, positions, inv_freq, sections, None, None, None,
-                                        None, workspace, True, _layout(layout), norm, q_weight, k_weight, eps, None),
-              "mdcn_rotary_backward")
+    g = _call(_native().rotary_backward, (grad_q_out, grad_k_out, q, k, positions, inv_freq, sections, None, None, None,
+                                          None, workspace, True, _layout(layout), norm, q_weight, k_weight, eps, None),
+              (4, 5, 15, 16), "mdcn_rotary_backward")
     return {"q": g[0], "k": g[1], "q_weight": g[2], "k_weight": g[3]}
 
 
@@ -160,8 +176,8 @@ def attention(q, k, v, q_starts, k_starts, k_lengths=None, causal=False, scale=N
     query sees every key, each one before it one key less. Returns (out, lse):
     the attended values, like q, and float32 [q_heads, q_tokens], the log of
     the sum of exp(scale * q . k)."""
-    return _done(_native().attention_forward(q, k, v, q_starts, k_starts, k_lengths, causal, scale, out, lse, workspace,
-                                             True, None), "mdcn_attention_forward")
+    return _call(_native().attention_forward, (q, k, v, q_starts, k_starts, k_lengths, causal, scale, out, lse, workspace,
+                                               True, None), (3, 4, 5), "mdcn_attention_forward")
 
 
 def mdcn_attention_backward_workspace_size(grad_out, q, k, v, out, lse, q_starts, k_starts, grad_q, grad_k, grad_v,
@@ -184,6 +200,7 @@ def attention_backward(grad_out, q, k, v, out, lse, q_starts, k_starts, k_length
                        workspace=None):
     """Gradients of sum(grad_out * out) for (out, lse) = attention(q, k, v,
     ...), as a dict with q, k and v."""
-    g = _done(_native().attention_backward(q, k, v, q_starts, k_starts, k_lengths, causal, scale, grad_out, out, None,
-                                           None, None, lse, workspace, True, None), "mdcn_attention_backward")
+    g = _call(_native().attention_backward, (q, k, v, q_starts, k_starts, k_lengths, causal, scale, grad_out, out, None,
+                                             None, None, lse, workspace, True, None), (3, 4, 5, 13),
+              "mdcn_attention_backward")
     return {"q": g[0], "k": g[1], "v": g[2]}

@@ -343,6 +343,26 @@ def test_deterministic_on_a_stream_and_status(dtype):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [BF, FS])
+def test_slices_of_starts_and_lengths(dtype):
+    """Some of the sequences, by slices of the offsets and lengths of all, and
+    rows of a longer lse."""
+    p = Problem(dtype, [9, 20, 30, 5], [20, 20, 33, 7], 2, 1, 64, True, room=[40] * 4, seed=3)
+    q, k, v, g, qs, ks, kn = (p.cuda(x) for x in ("q", "k", "v", "g", "qs", "ks", "kn"))
+    out, lse = mdcn.attention(q, k, v, qs, ks, k_lengths=kn, causal=True)
+    grads = mdcn.attention_backward(g, q, k, v, out, lse, qs, ks, k_lengths=kn, causal=True)
+    longer = torch.cat([lse.new_zeros(1), lse.flatten()])[1:].view_as(lse)
+    assert longer.data_ptr() % 16
+    for b in range(4):
+        rows, keys = slice(int(p.qs[b]), int(p.qs[b + 1])), slice(int(p.ks[b]), int(p.ks[b + 1]))
+        o, z = mdcn.attention(q, k, v, qs[b:b + 2], ks[b:b + 2], k_lengths=kn[b:b + 1], causal=True)
+        assert torch.equal(o[rows], out[rows]) and torch.equal(z[:, rows], lse[:, rows])
+        one = mdcn.attention_backward(g, q, k, v, out, longer, qs[b:b + 2], ks[b:b + 2], k_lengths=kn[b:b + 1], causal=True)
+        assert torch.equal(one["q"][rows], grads["q"][rows])
+        assert torch.equal(one["k"][keys], grads["k"][keys]) and torch.equal(one["v"][keys], grads["v"][keys])
+
+
+@gpu
 def test_capture_in_a_graph():
     p = Problem(BF, [200, 56], [200, 56], 4, 2, 64, True, seed=4)
     q, k, v, qs, ks = (p.cuda(x) for x in ("q", "k", "v", "qs", "ks"))

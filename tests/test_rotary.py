@@ -165,6 +165,28 @@ def test_rows_off_16_bytes():
 
 
 @gpu
+def test_slices_of_positions():
+    """A decoder's positions of one step after the other, rows of 12 bytes in one
+    tensor, and frequencies and weights that start off 16 bytes."""
+    p = Problem(torch.float16, 6, 3, 2, 48, (5, 8, 9), "half", True)
+    pos, freq = p.cuda("pos"), torch.cat([torch.zeros(1), p.freq]).cuda()[1:]
+    w = [torch.cat([torch.zeros(1, dtype=p.dtype), x]).cuda()[1:] for x in (p.qw, p.kw)]
+    assert freq.data_ptr() % 16 and w[0].data_ptr() % 16
+    q, k, gq, gk = (p.cuda(x) for x in ("q", "k", "gq", "gk"))
+    kw = dict(layout=p.layout, norm=True, eps=p.eps)
+    want = mdcn.rotary(q, k, pos, p.cuda("freq"), p.sections, q_weight=p.cuda("qw"), k_weight=p.cuda("kw"), **kw)
+    wg = mdcn.rotary_backward(gq, gk, q, k, pos, p.cuda("freq"), p.sections, q_weight=p.cuda("qw"), k_weight=p.cuda("kw"), **kw)
+    for t in range(6):
+        at = pos[t:t + 1]
+        got = mdcn.rotary(q[t:t + 1], k[t:t + 1], at, freq, p.sections, q_weight=w[0], k_weight=w[1], **kw)
+        g = mdcn.rotary_backward(gq[t:t + 1], gk[t:t + 1], q[t:t + 1], k[t:t + 1], at, freq, p.sections, q_weight=w[0], k_weight=w[1], **kw)
+        assert torch.equal(got[0], want[0][t:t + 1]) and torch.equal(got[1], want[1][t:t + 1])
+        assert torch.equal(g["q"], wg["q"][t:t + 1]) and torch.equal(g["k"], wg["k"][t:t + 1])
+    with pytest.raises(mdcn.MdcnError):  # the entry point itself takes what lies on 16 bytes
+        mdcn.mdcn_rotary_forward(q[:1], None, pos[1:2], freq, p.sections, torch.empty_like(q[:1]), None)
+
+
+@gpu
 def test_large_positions_keep_precision():
     """Positions near 2^24: the angle is reduced from the exact product."""
     p = Problem(torch.float32, 64, 2, 1, 64, (16, 16), "half", False, start=2**24 - 200)

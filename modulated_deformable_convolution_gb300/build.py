@@ -3,6 +3,9 @@ _token_binding.so, the binding of the operators on tokens, with g++.
 
     python -m modulated_deformable_convolution_gb300.build [--force]
 
+The library needs nvcc alone; a binding that does not build (no g++, no headers
+of Python or torch) is an error after the library has been linked.
+
 Objects go to ``_build/`` beside this file; translation units compile in
 parallel; ptxas resource usage (registers, shared memory, spills) is written
 to ``_build/ptxas.log``.
@@ -112,11 +115,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
     tmp_binding = BINDING + f".tmp{os.getpid()}"
     command, torch_version = _binding_command(home, tmp_binding)
     bind = force or _stale(BINDING, BINDING_SOURCE, [os.path.join(INCLUDE, "mdcn.h"), torch_version])
-    if bind:
-        jobs.append((command, None))
-    if jobs:
-        with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
+    bound = None
+    if jobs or bind:
+        with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs) + bind, os.cpu_count() or 1))) as ex:
             futs = [ex.submit(_compile, c, l) for c, l in jobs]
+            if bind:  # what goes wrong with it is raised below, once the library is there
+                bound = ex.submit(_compile, command)
             for f in futs:
                 out = f.result()
                 if verbose and out:
@@ -126,14 +130,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 p = os.path.join(BUILD, src + ".ptxas.log")
                 if os.path.exists(p):
                     f.write(open(p).read())
-    if bind:
-        os.replace(tmp_binding, BINDING)
     if force or jobs or not os.path.exists(LIB) or any(os.path.getmtime(o) > os.path.getmtime(LIB) for o in objs):
         tmp = LIB + f".tmp{os.getpid()}"
         lib64 = os.path.join(home, "lib64")
         cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcublas", "-Xlinker", f"-rpath,{lib64}"]
         _compile(cmd)
         os.replace(tmp, LIB)
+    if bound is not None:
+        bound.result()
+        os.replace(tmp_binding, BINDING)
     return LIB
 
 

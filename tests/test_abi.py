@@ -403,3 +403,24 @@ def test_32bit_limits_at_2_pow_31(lib, what, d, ok):
     s, n = ws_size(lib, h, dd, _abi.MDCN_F16)
     assert s == (_abi.MDCN_OK if ok else _abi.MDCN_ERR_UNSUPPORTED), (what, s)
     lib.mdcn_destroy(h)
+
+
+@pytest.mark.parametrize("why", ["source", "compiler"])
+def test_library_is_linked_without_the_binding(lib, tmp_path, monkeypatch, why):
+    """The binding of the operators on tokens needs g++ and the headers of Python
+    and torch; the C library does not and is there when the binding fails."""
+    from modulated_deformable_convolution_gb300 import build
+
+    bad = tmp_path / "binding.cpp"
+    bad.write_text("#error no headers\n")
+    target, binding = tmp_path / "libmdcn.so", tmp_path / "_token_binding.so"
+    monkeypatch.setattr(build, "LIB", str(target))
+    monkeypatch.setattr(build, "BINDING", str(binding))
+    if why == "source":
+        monkeypatch.setattr(build, "BINDING_SOURCE", str(bad))
+    else:
+        monkeypatch.setattr(build, "_binding_command", lambda home, out: ([str(tmp_path / "no-such-compiler")], build.__file__))
+    with pytest.raises((RuntimeError, OSError)):
+        build.build()
+    assert target.exists() and not binding.exists()
+    assert hasattr(ctypes.CDLL(str(target)), "mdcn_create")

@@ -199,6 +199,38 @@ def test_every_head_size_with_partial_tiles(dtype, d):
     _run(Problem(dtype, [5, 131, 44], [133, 40, 44], 2, 1, d, d % 16 == 0, seed=d))
 
 
+@gpu
+@pytest.mark.parametrize("dtype,hq,hk,d,causal", [(BF, 8, 8, 64, True), (FH, 8, 8, 64, False), (BF, 8, 8, 128, False), (FH, 8, 8, 128, True), (BF, 24, 8, 72, True)])
+def test_more_items_than_blocks(dtype, hq, hk, d, causal):
+    """Some 500 work items with work for each of the tensor-core kernels, several
+    to a block: what a block carries from one to the next, of one to three tiles
+    each, with empty ones between them."""
+    g = torch.Generator().manual_seed(d)
+    ql = [0 if i % 9 == 4 else int(n) for i, n in enumerate(torch.randint(1, 300, (72,), generator=g))]
+    kl = [max(0, n + int(e)) if i % 3 == 0 else n for i, (n, e) in enumerate(zip(ql, torch.randint(-40, 300, (72,), generator=g)))]
+    p = Problem(dtype, ql, kl, hq, hk, d, causal, seed=d)
+    assert sum(n > 0 for n in ql) * hk > 3 * 152 and sum(n > 0 for n in kl) * hk > 3 * 152
+    _run(p)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [BF, FH, FS])
+def test_heads_outermost(dtype):
+    """Tensors stored [heads][tokens][head_dim]: the head's stride is the larger."""
+    p = Problem(dtype, [150, 33], [150, 33], 4, 2, 64, True, seed=12)
+    r, tol = p.reference()
+    turned = {x: p.cuda(x).transpose(0, 1).contiguous().transpose(0, 1) for x in ("q", "k", "v", "g")}
+    out, lse = torch.empty_like(turned["q"]), torch.empty(4, 183, device="cuda")
+    assert out.stride(1) > out.stride(0)
+    mdcn.attention(turned["q"], turned["k"], turned["v"], p.cuda("qs"), p.cuda("ks"), causal=True, out=out, lse=lse)
+    p.check(out, r["out"], tol["out"], "out")
+    p.check(lse, r["lse"], tol["lse"], "lse")
+    g = mdcn.attention_backward(turned["g"], turned["q"], turned["k"], turned["v"], out, lse, p.cuda("qs"), p.cuda("ks"), causal=True)
+    want = p.backward(out.contiguous(), lse)
+    for x in ("q", "k", "v"):
+        assert torch.equal(g[x], want[x]), x
+
+
 def test_whole_warps_at_tensor_memory():
     """A load of results from tensor memory is the whole warp's, and the stores
     before it, in the loop's last turn, were those of the lanes that have a row: the

@@ -147,6 +147,8 @@ mdcn_status attn_check(const mdcn_attention_attrs* at, const mdcn_attention_dims
 // step is some four times as long, several blocks share an SM and most calls
 // have few: the SMs' work, and one item's length at the end. The join of the
 // shares costs a launch and the partial results' way to memory and back.
+// SMs and measured steps are those of the GB300 (152), not asked of the device: the
+// plan decides the workspace's size, which is asked without one.
 // (Measured: 4 maps of 80 x 80, 2 heads of 64: 114 us with one share, 102 with
 // two, 97 with three, 110 with four; 16 new tokens against up to 8192 keys: 90
 // with one, 77 to 81 with two to eight; a prompt of 1024 tokens, 32 heads: 28
@@ -216,7 +218,7 @@ AttnPlan attn_plan(const mdcn_attention_attrs& at, const mdcn_attention_dims& d,
 // out: as many as make three blocks of the first kind to an SM and six of the
 // second, each with two tiles at least. (Ragged sequences of up to 700, 6 heads
 // of 72 over 2: 374 us with neither shared, 146 with rows, 99 with both; 2
-// sequences of 2048, heads of 64: 972, 706 and 626.)
+// causal sequences of 2048, heads of 64: 972, 706 and 626.)
 struct AttnBwdPlan {
     int64_t tiles, kv_splits, q_splits;
     size_t off_g_size, off_v_size, off_sizes, off_kv, off_q, bytes;

@@ -20,8 +20,8 @@
 // Measured: forward, 2 sequences of 2048, 8 heads of 64 over 4: 470 us, 36
 // TFLOP/s of the 70 that a large float32 matrix product reaches; 6 maps of up to
 // 32 x 32, 8 heads of 40 over 4: 77 us. Backward, 4 ragged sequences of up to 700,
-// 6 heads of 72 over 2: 94 us; 2 sequences of 2048, 6 heads of 64 over 2: 626 us,
-// 36 TFLOP/s of seven products.
+// 6 heads of 72 over 2: 94 us; 2 causal sequences of 2048, 6 heads of 64 over 2: 615
+// us, 37 TFLOP/s of seven products (without the mask 1180 us, 38).
 #include <algorithm>
 #include <cfloat>
 #include <cstdint>
@@ -875,7 +875,7 @@ cudaError_t delta(const AttnArgs& a, cudaStream_t st) {
     const cudaError_t e = lanes == 8 ? launch_dependent(attn_delta_kernel<T, 8>, rows + values, kT, 0, st, a, rows)
                                      : launch_dependent(attn_delta_kernel<T, 16>, rows + values, kT, 0, st, a, rows);
     if (e != cudaSuccess || !a.sizes) return e;
-    // blocks that share a sequence's rows of a key head: two to an SM in all, 16 sizes to a thread
+    // blocks that share a sequence's rows of a key head: two to each of 152 SMs in all, 16 sizes to a thread
     const int64_t pairs = static_cast<int64_t>(a.batch) * a.hk;
     const int64_t words = (static_cast<int64_t>(a.tq) * a.group + a.tk) / a.batch / (16 * kT) + 1;
     const int64_t shares = std::min(std::max<int64_t>(2 * 152 / pairs, 1), words);

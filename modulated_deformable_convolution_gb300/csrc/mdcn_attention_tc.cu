@@ -22,8 +22,8 @@
 // Shared memory: Q once, K and V in a ring of 128-row tiles, 227 KB in all.
 //
 // Measured (32 heads of 128 over 8, bfloat16): 12 packed causal prompts of up to
-// 8192 tokens 1109 us, 1510 TFLOP/s of the pairs that are seen; 4 x 8192 without a mask
-// 2640 us, 1665 TFLOP/s. A step of both row tiles takes about 2600 cycles, of
+// 8192 tokens 1176 us, 1425 TFLOP/s of the pairs that are seen; 4 x 8192 without a mask
+// 2590 us, 1700 TFLOP/s. A step of both row tiles takes about 2600 cycles, of
 // which the tensor pipe works 2048: with P over S, the next S waits for it. At
 // D = 64 (4 maps of 80 x 80, 2 heads, float16) 92 us, 912 TFLOP/s: some 2000
 // cycles a step; the exponentials of a warp's 64 pairs of columns alone take

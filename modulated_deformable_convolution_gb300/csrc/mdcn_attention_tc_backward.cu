@@ -28,12 +28,13 @@
 // one tile runs, the next tile's S and dP, or this tile's sums, are computed.
 //
 // Measured with delta (bfloat16, 32 heads of 128 over 8): 9 packed causal prompts
-// of up to 6400 tokens 1482 us, 940 TFLOP/s of five products, 1315 of the seven;
-// 2 x 8192 without a mask 4.74 ms, 1160 and 1620. 16 maps of 32 x 32, 8 heads of
-// 64, float16: 152 us, 566 TFLOP/s of five products, 10 us of them for the sizes: at D = 64 the products of a
-// tile take half as long and its elementwise step as long as before (a grad_kv
-// block about 2130 cycles, exponentials 710, dS 510, loads and stores of tensor
-// memory and waits the rest; 16 elementwise warps instead of 8 changed nothing).
+// of up to 6400 tokens 1525 us, 912 TFLOP/s of five products, 1277 of the seven;
+// 2 x 8192 without a mask 4.7 to 4.9 ms, 1120 to 1170 and 1570 to 1640. 16 maps of
+// 32 x 32, 8 heads of 64, float16: 152 us, 566 TFLOP/s of five products, 10 us of
+// them for the sizes: at D = 64 the products of a tile take half as long and its
+// elementwise step as long as before (a grad_kv block about 2130 cycles,
+// exponentials 710, dS 510, loads and stores of tensor memory and waits the rest;
+// 16 elementwise warps instead of 8 changed nothing).
 #include <cuda.h>
 
 #include <cstdint>

@@ -855,7 +855,7 @@ cudaError_t backward_t(const RotaryArgs& a, RotaryMode mode, int64_t grid, void*
 cudaError_t launch_rotary_forward(int dtype, RotaryArgs a, int sms, cudaStream_t st) {
     const RotaryMode mode = plan_lanes(&a, sms);
     int64_t grid = blocks_for(a, kWarps);
-    if (grid > static_cast<int64_t>(sms) * 2) grid = static_cast<int64_t>(sms) * 2;  // one wave
+    if (grid > static_cast<int64_t>(sms) * 2) grid = static_cast<int64_t>(sms) * 2;  // one wave each for q and k
     if (dtype == kF32) return forward_t<float>(a, mode, grid, st);
     if (dtype == kF16) return forward_t<__half>(a, mode, grid, st);
     return forward_t<__nv_bfloat16>(a, mode, grid, st);
@@ -864,7 +864,7 @@ cudaError_t launch_rotary_forward(int dtype, RotaryArgs a, int sms, cudaStream_t
 cudaError_t launch_rotary_backward(int dtype, RotaryArgs a, void* gqw, void* gkw, int sms, cudaStream_t st) {
     const RotaryMode mode = plan_lanes(&a, sms);
     int64_t grid = blocks_for(a, kBwdWarps);
-    if (grid > static_cast<int64_t>(sms) * 3) grid = static_cast<int64_t>(sms) * 3;  // one wave
+    if (grid > static_cast<int64_t>(sms) * 3) grid = static_cast<int64_t>(sms) * 3;  // one wave each for q and k
     if (grid > kRotaryMaxBlocks) grid = kRotaryMaxBlocks;
     if (dtype == kF32) return backward_t<float>(a, mode, grid, gqw, gkw, st);
     if (dtype == kF16) return backward_t<__half>(a, mode, grid, gqw, gkw, st);

@@ -28,7 +28,7 @@ struct RotaryArgs {
     int32_t layout, norm;
     float eps;
     int32_t vec;         // every row of x, y and g starts on 16 bytes
-    int32_t lanes;       // lanes per row: power of two >= D / 8
+    int32_t lanes;       // lanes per row: power of two >= D / 16, or D / 8 through shared memory
     int32_t parts;       // warps that share one token's rows
 };
 

@@ -175,7 +175,12 @@ def attention(q, k, v, q_starts, k_starts, k_lengths=None, causal=False, scale=N
     k_starts[b + 1], or the first k_lengths[b] of them. ``causal``: the last
     query sees every key, each one before it one key less. Returns (out, lse):
     the attended values, like q, and float32 [q_heads, q_tokens], the log of
-    the sum of exp(scale * q . k)."""
+    the sum of exp(scale * q . k). Rows of no sequence are not written: where
+    ``out`` or ``lse`` is None they hold anything. A kernel's wait that gave up
+    is seen with mdcn_query_status on a ``workspace`` of one's own (of
+    mdcn_attention_workspace_size bytes or more); a workspace that is None or
+    too small is replaced by one that the call drops. Starts and lengths may be
+    slices that start anywhere."""
     return _call(_native().attention_forward, (q, k, v, q_starts, k_starts, k_lengths, causal, scale, out, lse, workspace,
                                                True, None), (3, 4, 5), "mdcn_attention_forward")
 
@@ -199,7 +204,8 @@ def mdcn_attention_backward(grad_out, q, k, v, out, lse, q_starts, k_starts, gra
 def attention_backward(grad_out, q, k, v, out, lse, q_starts, k_starts, k_lengths=None, causal=False, scale=None,
                        workspace=None):
     """Gradients of sum(grad_out * out) for (out, lse) = attention(q, k, v,
-    ...), as a dict with q, k and v."""
+    ...), as a dict with q, k and v. Rows of no sequence hold anything; starts,
+    lengths and ``workspace`` as for attention, lse may start anywhere."""
     g = _call(_native().attention_backward, (q, k, v, q_starts, k_starts, k_lengths, causal, scale, grad_out, out, None,
                                              None, None, lse, workspace, True, None), (3, 4, 5, 13),
               "mdcn_attention_backward")
